@@ -41,7 +41,8 @@
  *     N, T, E are pairs, tokens and experts resident on this GPU.
  *   - Dense inputs are row-major with a leading dimension ld (elements) and
  *     16-byte aligned rows; all dense inputs of one call share one dtype;
- *     columns must be a multiple of 8 (bf16) or 4 (fp32).  Outputs are fp32.
+ *     columns must be a multiple of 8 (bf16) or 4 (fp32).  Outputs are fp32
+ *     (the forward pass's and the router's have the types stated there).
  *   - Outputs are overwritten, never accumulated.  Experts with nothing kept
  *     get dW = 0; rows of dX that receive no kept pair are 0.
  *   - Inputs must be finite; otherwise the results are undefined.
@@ -491,8 +492,179 @@ size_t lrm_workspace_size(const lrm_problem* prob);
  * min(N, sum of quota[e]); -1 if a quota is negative or an argument is NULL. */
 int64_t lrm_max_kept(int32_t N, int32_t E, const int32_t* quota);
 
+/* ------------------------------------------------------------- the router */
+
+/* Routing to experts: the pairs that every other call takes.  For each token t
+ * with logits z_e, e in [0, E):
+ *   eligible experts: those with expert_mask[e] != 0 and z_e > -inf, in a row
+ *     with token_mask[t] != 0; what a masked place holds is never used (it may
+ *     be NaN or infinite).  A row may leave no expert.
+ *   scores: s_e = softmax of z over the eligible experts, or sigmoid(z_e)
+ *   keys:   c_e = s_e + bias[e]; the bias (a load-balancing term) takes part in
+ *     the choice only
+ *   groups: with n_group > 1 the experts form n_group runs of E / n_group; a
+ *     group's score is the largest key of its eligible experts
+ *     (LRM_GROUP_MAX) or the sum of the two largest (LRM_GROUP_TOP2; of the
+ *     only one where there is one); experts outside the topk_group best groups
+ *     are left out (ties to the lower group)
+ *   choice: the k experts of the largest keys, in descending order, ties to
+ *     the lower index; slots beyond the eligible experts stay empty
+ *   weights: scale * s_e, or with LRM_ROUTE_RENORM scale * s_e / (sum of s over
+ *     the chosen), evaluated without underflow of the sum
+ * The order is that of the exact keys: keys that 32 bits cannot tell apart are
+ * compared in 64 (without a bias, the scores' order is the logits').
+ * Unmasked logits must not be NaN or +inf (the results are then undefined,
+ * every access stays in bounds). */
+typedef enum lrm_route_score { LRM_SOFTMAX = 0, LRM_SIGMOID = 1 } lrm_route_score;
+typedef enum lrm_group_rule { LRM_GROUP_MAX = 0, LRM_GROUP_TOP2 = 1 } lrm_group_rule;
+#define LRM_ROUTE_RENORM 1u
+
+typedef struct lrm_router {
+  int32_t T, E, k;       /* tokens >= 0, experts 1..4096, choices 1..min(E, 64); T * k < 2^31 */
+  int32_t score;         /* lrm_route_score */
+  uint32_t flags;        /* LRM_ROUTE_RENORM */
+  int32_t n_group;       /* groups, 1..64, dividing E (1: none) */
+  int32_t topk_group;    /* groups kept, 1..n_group */
+  int32_t group_rule;    /* lrm_group_rule */
+  float scale;           /* factor of the weights, finite */
+  int32_t dtype;         /* lrm_dtype of the logits */
+  const void* logits;    /* device [T][E], rows ld elements apart, element-aligned */
+  int64_t ld;            /* >= E */
+  const float* bias;           /* device [E], or NULL */
+  const uint8_t* expert_mask;  /* device [E], or NULL: every expert */
+  const uint8_t* token_mask;   /* device [T], or NULL: every token */
+} lrm_router;
+
+/* The choice and its weights:
+ *   expert: device [T*k] output, the chosen experts of token t at t*k ..,
+ *           -1 in empty slots
+ *   weight: device [T*k] output, 0 in empty slots
+ *   token:  device [T*k] output (slot / k), or NULL
+ *   counts: device [E] output, slots per expert (the controller's counts), or
+ *           NULL
+ * Where no slot is empty and every expert is resident, token, expert and
+ * weight are the arrays of lrm_pairs with N = T*k; otherwise
+ * lrm_route_share makes them.
+ * ws: device scratch of lrm_route_workspace_size(r) bytes, needed for counts
+ * only (may be NULL otherwise). */
+lrm_status lrm_route(const lrm_router* r, int32_t* expert, float* weight, int32_t* token,
+                     int32_t* counts, void* ws, size_t ws_bytes, void* stream);
+size_t lrm_route_workspace_size(const lrm_router* r);
+
+/* Gradient of the routing: from the gradient of the weights to that of the
+ * logits.  The choice itself has none, nor has the bias.
+ *   expert:  device [T*k], the choice (of lrm_route, or any: entries outside
+ *            [0, E) and masked experts are empty slots)
+ *   dweight: device [T*k] fp32, the gradient of the loss with respect to the
+ *            weights (0 for slots that other GPUs hold; what empty slots hold is not used)
+ *   dlogits: device [T][E] output of the logits' dtype, rows ldd >= E elements
+ *            apart, every element written (0 for masked ones) */
+lrm_status lrm_route_bwd(const lrm_router* r, const int32_t* expert, const float* dweight,
+                         void* dlogits, int64_t ldd, void* stream);
+
+/* The pairs of one GPU's experts: the slots of lrm_route whose expert lies in
+ * [e0, e0 + E), in slot order (token-major), empty slots left out:
+ *   expert, weight: device [T*k] of lrm_route
+ *   out_token, out_expert (less e0), out_weight, out_slot: device [T*k]
+ *           outputs, the first n entries written; out_slot and out_token may be
+ *           NULL
+ *   out_n:  device [1] output, n
+ * ws: device scratch of lrm_route_share_workspace_size(T, k) bytes. */
+lrm_status lrm_route_share(int32_t T, int32_t k, const int32_t* expert, const float* weight,
+                           int32_t e0, int32_t E, int32_t* out_token, int32_t* out_expert,
+                           float* out_weight, int32_t* out_slot, int32_t* out_n, void* ws,
+                           size_t ws_bytes, void* stream);
+size_t lrm_route_share_workspace_size(int32_t T, int32_t k);
+
+/* ------------------------------------------------------- the experts forward */
+
+/* Activation of a LINEAR projection (GELU: z * Phi(z), the exact form). */
+typedef enum lrm_act { LRM_ACT_NONE = 0, LRM_ACT_RELU = 1, LRM_ACT_GELU = 2, LRM_ACT_SILU = 3 } lrm_act;
+
+/* The complete forward pass of one layer call (the pages: the forward stays
+ * complete), the counterpart of lrm_problem:
+ *   LINEAR: z_p = W_e x_p + bias_e,  y_p = act(z_p)
+ *   SWIGLU: a_p = W_gate,e x_p, b_p = W_up,e x_p, y_p = W_down,e (silu(a_p) b_p)
+ *   Y[t] = R[t] + sum over the pairs p of t of w_p y_p
+ * with e the expert of p.  bf16 runs on MFMA with fp32 accumulation, fp32 in
+ * fp32; silu(a) b is rounded to the inputs' dtype between the two products;
+ * bias, activation, weights, the sum over pairs and the residual are fp32 and
+ * rounded once. */
+typedef struct lrm_forward {
+  int32_t kind;  /* lrm_kind */
+  int32_t act;   /* lrm_act (LINEAR; NONE for SWIGLU) */
+  int32_t dtype; /* lrm_dtype of every dense input and output */
+  int32_t _pad;
+  lrm_pairs pairs;
+  lrm_mat X; /* LINEAR: TOKEN or PAIR, d_in cols; SWIGLU: TOKEN, H cols */
+  lrm_mat R; /* residual: TOKEN, d_out (H) cols; ptr NULL: none */
+  /* LINEAR (as in lrm_problem) */
+  const void* W;
+  int64_t w_stride;
+  const void* bias;    /* device [E][d_out] dense, or NULL */
+  int32_t d_in, d_out; /* each 1..2^20-1 */
+  /* SWIGLU (as in lrm_problem) */
+  const void* W_gate;
+  const void* W_up;
+  const void* W_down;
+  int32_t H, I;
+} lrm_forward;
+
+/* Outputs, device, dense, of the inputs' dtype (h_sumsq fp64); NULL: not
+ * wanted, at least one is.  Rows of pairs that are absent (index out of range)
+ * are left as they were in the PAIR outputs and add nothing to Y. */
+typedef struct lrm_forward_outputs {
+  void* Y;         /* [T][d_out] (SWIGLU: [T][H]); may be R itself when R.ld is its columns */
+  void* Yp;        /* [N][d_out] ([N][H]): y_p of every pair, not weighted */
+  void* Z;         /* LINEAR: [N][d_out], z_p */
+  void* A;         /* SWIGLU: [N][I], a_p, as lrm_problem takes it */
+  void* B;         /* SWIGLU: [N][I], b_p */
+  double* h_sumsq; /* SWIGLU: [N], |h_p|^2 of h_p = silu(a_p) b_p as the down product takes it,
+                      as lrm_problem takes it */
+} lrm_forward_outputs;
+
+/* ws: device scratch of lrm_forward_workspace_size(f) bytes, 256-byte aligned;
+ * its first word is the device error word (lrm_check_device_errors). */
+lrm_status lrm_expert_forward(const lrm_forward* f, const lrm_forward_outputs* out, void* ws,
+                              size_t ws_bytes, void* stream);
+size_t lrm_forward_workspace_size(const lrm_forward* f);
+
+/* Backward pass of the forward's epilogue.  With y_p = act(z_p) and dy_p the
+ * dY row of p:
+ *   dweight[p] = <dy_p, act(z_p)>            (gradient of the routing weight)
+ *   G[p]       = dy_p act'(z_p)              (unscaled by w_p, as lrm_problem
+ *                                             takes it, rounded to the dtype)
+ *   dbias[e]   = sum over the pairs p of e of w_p dy_p act'(z_p)   (fp32)
+ * For SWIGLU experts z is Yp and act NONE.  act'(0) of RELU is 0. */
+typedef struct lrm_pair_grad_problem {
+  int32_t act;   /* lrm_act */
+  int32_t dtype; /* lrm_dtype of dY, Z and G */
+  lrm_pairs pairs;
+  lrm_mat dY;    /* TOKEN or PAIR, d cols */
+  lrm_mat Z;     /* PAIR, d cols, d 1..2^20-1 */
+} lrm_pair_grad_problem;
+
+/* Outputs, device, NULL: not wanted, at least one is.  Absent pairs (index out
+ * of range) get 0 in dweight and G and add nothing to dbias; their Z rows are
+ * not used. */
+typedef struct lrm_pair_grad_outputs {
+  float* dweight; /* [N] */
+  void* G;        /* [N][d] dense */
+  float* dbias;   /* [E][d], 0 for experts without pairs */
+} lrm_pair_grad_outputs;
+
+/* ws: device scratch of lrm_pair_grad_workspace_size(g) bytes, 256-byte
+ * aligned; its first word is the device error word when dbias is wanted
+ * (0 otherwise). */
+lrm_status lrm_pair_grad(const lrm_pair_grad_problem* g, const lrm_pair_grad_outputs* out,
+                         void* ws, size_t ws_bytes, void* stream);
+size_t lrm_pair_grad_workspace_size(const lrm_pair_grad_problem* g);
+
+/* ------------------------------------------------------------------ errors */
+
 /* Synchronises the stream, then reads the device error word at the start of
- * a workspace used by lrm_select, lrm_expert_backward or lrm_receiver_layout:
+ * a workspace used by lrm_select, lrm_expert_backward, lrm_receiver_layout,
+ * lrm_expert_forward or lrm_pair_grad:
  * LRM_OK, or LRM_ERR_INDEX if an expert index was out of range or token[]
  * was out of range or decreasing (such pairs are treated as absent), or a
  * replica assignment did not match the kept counts; otherwise

@@ -48,6 +48,18 @@ __device__ __forceinline__ int wave_sum(int v) {
 
 __device__ __forceinline__ int lane_id() { return threadIdx.x & (kWave - 1); }
 
+// Orders a wave's LDS accesses before and after it (the LDS serves one wave's
+// accesses in order, so this only holds the compiler).
+__device__ __forceinline__ void wave_sync() {
+#ifndef LRM_CPU_EMU
+  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+#endif
+  __builtin_amdgcn_wave_barrier();
+#ifndef LRM_CPU_EMU
+  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+#endif
+}
+
 // Inclusive scan across a wave with DPP moves (no LDS round trips):
 // Hillis-Steele inside each 16-lane row (row_shr 1, 2, 4, 8; lanes whose
 // source falls before the row keep the 0 passed as "old"), then row 0's total
@@ -70,6 +82,36 @@ __device__ __forceinline__ int64_t pair_row(int rows_is_pair, const int32_t* tok
 
 // SiLU pieces in fp32 (accurate expf).
 __device__ __forceinline__ float sigmoidf_acc(float a) { return 1.0f / (1.0f + expf(-a)); }
+
+// Activations of the forward pass (lrm_act) in fp32 and their derivatives.
+// GELU is z * Phi(z), Phi the normal distribution function.
+constexpr int kActNone = 0, kActRelu = 1, kActGelu = 2, kActSilu = 3;
+template <int ACT>
+__device__ __forceinline__ float act_of(float z) {
+  if constexpr (ACT == kActRelu) return z > 0.f ? z : 0.f;
+  if constexpr (ACT == kActGelu) return 0.5f * z * (1.f + erff(z * 0.70710678118654752f));
+  if constexpr (ACT == kActSilu) return z * sigmoidf_acc(z);
+  return z;
+}
+// act(z) in y and act'(z) in g
+template <int ACT>
+__device__ __forceinline__ void act_both(float z, float& y, float& g) {
+  if constexpr (ACT == kActRelu) {
+    y = z > 0.f ? z : 0.f;
+    g = z > 0.f ? 1.f : 0.f;
+  } else if constexpr (ACT == kActGelu) {
+    const float phi = 0.5f * (1.f + erff(z * 0.70710678118654752f));
+    y = z * phi;
+    g = phi + z * 0.39894228040143268f * expf(-0.5f * z * z);
+  } else if constexpr (ACT == kActSilu) {
+    const float s = sigmoidf_acc(z);
+    y = z * s;
+    g = s * (1.f + z * (1.f - s));
+  } else {
+    y = z;
+    g = 1.f;
+  }
+}
 
 // Device error bits (written into the first word of a workspace).
 enum : uint32_t {

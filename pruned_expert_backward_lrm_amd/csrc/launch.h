@@ -232,4 +232,94 @@ struct GluBwdArgs {
 };
 hipError_t launch_glu_bwd(const GluBwdArgs& a, hipStream_t s);
 
+// ---------------------------------------------------------------- router
+// lrm_router, with the group rule and score as flags.  vec: every logits row
+// starts on a 16-byte boundary.
+struct RouteArgs {
+  int T, E, k, softmax, renorm, n_group, topk_group, group_top2, bf16, vec;
+  float scale;
+  const void* logits; int64_t ld;
+  const float* bias;
+  const uint8_t* expert_mask;
+  const uint8_t* token_mask;
+  int32_t* expert;
+  float* weight;
+  int32_t* token;   // or nullptr
+  int32_t* counts;  // scratch [kRouteBlocks][E] (needed when counts are wanted)
+};
+constexpr int kRouteBlocks = 2048;  // persistent blocks of the routing kernel, at most
+hipError_t launch_route(const RouteArgs& a, int32_t* counts, hipStream_t s);
+hipError_t launch_route_bwd(const RouteArgs& a, const int32_t* expert, const float* dweight,
+                            void* dlogits, int64_t ldd, int vec_out, hipStream_t s);
+constexpr int kShareBlocks = 1024;  // blocks of the share's compaction, at most
+// cnt: scratch [kShareBlocks]
+hipError_t launch_route_share(int64_t n, int k, const int32_t* expert, const float* weight, int e0,
+                              int E, int32_t* out_token, int32_t* out_expert, float* out_weight,
+                              int32_t* out_slot, int32_t* out_n, int32_t* cnt, hipStream_t s);
+
+// ------------------------------------------------- epilogue backward
+// lrm_pair_grad.  With dbias: the pairs bucketed by expert (offsets [E+1], kept
+// [N], pos [N], by launch_bucket with keep_all) and part, scratch of
+// [pair_grad_splits(N, E)][E][d].  err: set to 0 when dbias is not wanted (with
+// dbias the bucketing writes it).
+struct PairGradArgs {
+  int N, T, E, d, bf16, act;
+  const int32_t* token;
+  const int32_t* expert;
+  const float* weight;
+  const void* dY; int64_t ldy; int dy_pair;
+  const void* Z; int64_t ldz;
+  float* dweight;
+  void* G;
+  float* dbias;
+  const int32_t* offsets;
+  const int32_t* kept;
+  const int32_t* pos;
+  float* part;
+  uint32_t* err;
+};
+// widest rows that one pass takes with their column sums in registers
+constexpr int kPairGradCols = 2048;
+int pair_grad_splits(int N, int E);
+hipError_t launch_pair_grad(const PairGradArgs& a, hipStream_t s);
+
+// ------------------------------------------------------- experts forward
+// One grouped product of the forward pass over the packed rows of all experts
+// (offsets [E+1], kept [N], mt_off [E+1] the prefix of row tiles of
+// fwd_tile_rows rows).  The A operand's row of packed row m is row m of X
+// (gather 0), or the row of pair kept[m]: itself (x_pair) or its token's.
+//   glu: u = W0_e x, v = W1_e x: A[p] = u, B[p] = v (either may be null),
+//        H[m] = silu(u) v
+//   else: z = W0_e x + bias_e: Z[p] = z, Y[p] = act(z) (either may be null);
+//        Ylo[p]: the 8 bits below bf16 of Y (bf16; null: not wanted)
+// All outputs have n dense columns.
+struct FwdGemmArgs {
+  int N, E, bf16, K, n, glu, act, gather, x_pair;
+  const int32_t* offsets;
+  const int32_t* kept;
+  const int32_t* mt_off;
+  const int32_t* token;
+  const void* X; int64_t ldx;
+  const void* W0; const void* W1; int64_t w_stride;  // [E][n][K]
+  const void* bias;  // [E][n] or null
+  void* A; void* B; void* H;
+  void* Z; void* Y; int8_t* Ylo;
+};
+int fwd_tile_rows(const FwdGemmArgs& g);
+hipError_t launch_fwd_gemm(const FwdGemmArgs& g, hipStream_t s);
+// out[kept[m]] = |H[m]|^2 in fp64 (glu)
+hipError_t launch_fwd_sumsq(const FwdGemmArgs& g, double* out, hipStream_t s);
+// out[t] = R[t] + sum over the pairs p of t with pos[p] >= 0, in pair order, of
+// w_p (Y[p] + Ylo[p])
+struct FwdJoinArgs {
+  int N, T, d, bf16;
+  const int32_t* tok_off;
+  const int32_t* pos;
+  const float* weight;
+  const void* Y; const int8_t* Ylo;
+  const void* R; int64_t ldr;  // null: none
+  void* out;
+};
+hipError_t launch_fwd_join(const FwdJoinArgs& a, hipStream_t s);
+
 }  // namespace lrm

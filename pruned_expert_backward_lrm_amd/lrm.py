@@ -35,7 +35,11 @@ LRM_DW_BF16 = 2
 LRM_QUOTA_ON_DEVICE = 4
 LRM_DEBUG_CHECKS = 8
 LRM_GATHER_LOADS = 16
+LRM_ROUTE_RENORM = 1
 ROWS = {"token": LRM_ROWS_TOKEN, "pair": LRM_ROWS_PAIR}
+SCORES = {"softmax": 0, "sigmoid": 1}
+GROUP_RULES = {"max": 0, "top2": 1}
+ACTS = {"none": 0, "relu": 1, "gelu": 2, "silu": 3}
 
 
 class LrmError(RuntimeError):
@@ -71,6 +75,36 @@ class lrm_outputs(C.Structure):
     _fields_ = [(n, C.c_void_p) for n in (
         "dW", "dW_gate", "dW_up", "dW_down", "dX", "score", "pos", "offsets", "score_gate",
         "score_up", "pos_gate", "pos_up", "offsets_gate", "offsets_up", "dH")]
+
+
+class lrm_router(C.Structure):
+    _fields_ = [("T", C.c_int32), ("E", C.c_int32), ("k", C.c_int32), ("score", C.c_int32),
+                ("flags", C.c_uint32), ("n_group", C.c_int32), ("topk_group", C.c_int32),
+                ("group_rule", C.c_int32), ("scale", C.c_float), ("dtype", C.c_int32),
+                ("logits", C.c_void_p), ("ld", C.c_int64), ("bias", C.c_void_p),
+                ("expert_mask", C.c_void_p), ("token_mask", C.c_void_p)]
+
+
+class lrm_forward(C.Structure):
+    _fields_ = [("kind", C.c_int32), ("act", C.c_int32), ("dtype", C.c_int32),
+                ("_pad", C.c_int32), ("pairs", lrm_pairs), ("X", lrm_mat), ("R", lrm_mat),
+                ("W", C.c_void_p), ("w_stride", C.c_int64), ("bias", C.c_void_p),
+                ("d_in", C.c_int32), ("d_out", C.c_int32), ("W_gate", C.c_void_p),
+                ("W_up", C.c_void_p), ("W_down", C.c_void_p), ("H", C.c_int32),
+                ("I", C.c_int32)]
+
+
+class lrm_forward_outputs(C.Structure):
+    _fields_ = [(n, C.c_void_p) for n in ("Y", "Yp", "Z", "A", "B", "h_sumsq")]
+
+
+class lrm_pair_grad_problem(C.Structure):
+    _fields_ = [("act", C.c_int32), ("dtype", C.c_int32), ("pairs", lrm_pairs), ("dY", lrm_mat),
+                ("Z", lrm_mat)]
+
+
+class lrm_pair_grad_outputs(C.Structure):
+    _fields_ = [(n, C.c_void_p) for n in ("dweight", "G", "dbias")]
 
 
 _P = C.c_void_p
@@ -111,6 +145,18 @@ _sigs = {
     "lrm_redistribute_workspace_size": (_SZ, [_I32, _I32]),
     "lrm_receiver_layout": (C.c_int, [_I32, _I32, _P, _P, _I32, _P, _P, _P, _P, _SZ, _P]),
     "lrm_receiver_layout_workspace_size": (_SZ, [_I32, _I32]),
+    "lrm_route": (C.c_int, [C.POINTER(lrm_router), _P, _P, _P, _P, _P, _SZ, _P]),
+    "lrm_route_workspace_size": (_SZ, [C.POINTER(lrm_router)]),
+    "lrm_route_bwd": (C.c_int, [C.POINTER(lrm_router), _P, _P, _P, C.c_int64, _P]),
+    "lrm_route_share": (C.c_int, [_I32, _I32, _P, _P, _I32, _I32, _P, _P, _P, _P, _P, _P, _SZ,
+                                  _P]),
+    "lrm_route_share_workspace_size": (_SZ, [_I32, _I32]),
+    "lrm_expert_forward": (C.c_int, [C.POINTER(lrm_forward), C.POINTER(lrm_forward_outputs), _P,
+                                     _SZ, _P]),
+    "lrm_forward_workspace_size": (_SZ, [C.POINTER(lrm_forward)]),
+    "lrm_pair_grad": (C.c_int, [C.POINTER(lrm_pair_grad_problem),
+                                C.POINTER(lrm_pair_grad_outputs), _P, _SZ, _P]),
+    "lrm_pair_grad_workspace_size": (_SZ, [C.POINTER(lrm_pair_grad_problem)]),
 }
 for _name, (_res, _args) in _sigs.items():
     _f = getattr(_lib, _name)
@@ -411,4 +457,210 @@ def lrm_expert_backward_events(pb: Problem, outputs: dict, events, ws=None, stre
     _check(_lib.lrm_expert_backward_events(C.byref(pb.c), C.byref(o), _ptr(ws), ws.numel(),
                                            _stream(stream), arr, len(events)),
            "lrm_expert_backward_events")
+    return ws
+
+
+# -------------------------------------------------------------- the router
+class Router:
+    """An lrm_router over logits [T][E] (fp32 or bf16, unit column stride) plus
+    the tensors that keep its memory alive.  bias: fp32 [E]; expert_mask [E]
+    and token_mask [T]: uint8 or bool, nonzero where the expert or token takes
+    part."""
+
+    def __init__(self, logits: torch.Tensor, k: int, score: str = "softmax", renorm: bool = True,
+                 scale: float = 1.0, n_group: int = 1, topk_group: int = 1,
+                 group_rule: str = "top2", bias=None, expert_mask=None, token_mask=None):
+        if logits.dim() != 2 or (logits.shape[1] > 1 and logits.stride(1) != 1):
+            raise ValueError("logits must be 2-D with unit column stride")
+        T, E = logits.shape
+        for name, t, n, dts in (("bias", bias, E, (torch.float32,)),
+                                ("expert_mask", expert_mask, E, (torch.uint8, torch.bool)),
+                                ("token_mask", token_mask, T, (torch.uint8, torch.bool))):
+            if t is not None and (t.dtype not in dts or t.shape != (n,) or not t.is_contiguous()
+                                  or t.device != logits.device):
+                raise ValueError(f"{name} must be a contiguous {dts[0]} tensor of {n} entries "
+                                 "on the logits' device")
+        self.T, self.E, self.k = int(T), int(E), int(k)
+        self.keep = [logits, bias, expert_mask, token_mask]
+        ld = logits.stride(0) if T > 1 else max(logits.stride(0), E)
+        self.c = lrm_router(self.T, self.E, self.k, SCORES[score],
+                            LRM_ROUTE_RENORM if renorm else 0, int(n_group), int(topk_group),
+                            GROUP_RULES[group_rule], float(scale), dtype_code(logits),
+                            _ptr(logits), ld, _ptr(bias), _ptr(expert_mask), _ptr(token_mask))
+        self.ws_bytes = int(_lib.lrm_route_workspace_size(C.byref(self.c)))
+
+
+def _slots(name, t, n, dtype):
+    """A dense device array of at least n entries of a type, or None."""
+    if t is not None and (t.dtype != dtype or t.numel() < n or not t.is_contiguous()):
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor of at least {n} entries")
+
+
+def lrm_route(r: Router, expert, weight, token=None, counts=None, ws=None, stream=None):
+    """The k experts of every token (int32 [T*k], -1 in empty slots) and their
+    weights (fp32 [T*k]); optionally the slots' tokens and the experts' counts."""
+    n = r.T * r.k
+    _slots("expert", expert, n, torch.int32)
+    _slots("weight", weight, n, torch.float32)
+    _slots("token", token, n, torch.int32)
+    _slots("counts", counts, r.E, torch.int32)
+    if counts is not None:
+        ws = _ws(r.ws_bytes, counts.device, ws)
+    _check(_lib.lrm_route(C.byref(r.c), _ptr(expert), _ptr(weight), _ptr(token), _ptr(counts),
+                          _ptr(ws), ws.numel() if ws is not None else 0, _stream(stream)),
+           "lrm_route")
+
+
+def lrm_route_bwd(r: Router, expert, dweight, dlogits: torch.Tensor, stream=None):
+    """Gradient of the logits (their dtype, [T][E]) from the gradient of the
+    weights (fp32 [T*k]) of a choice (int32 [T*k])."""
+    n = r.T * r.k
+    _slots("expert", expert, n, torch.int32)
+    _slots("dweight", dweight, n, torch.float32)
+    if dlogits.shape != (r.T, r.E) or (r.E > 1 and dlogits.stride(1) != 1) or \
+            dtype_code(dlogits) != r.c.dtype:
+        raise ValueError("dlogits must be [T][E] of the logits' dtype with unit column stride")
+    ldd = dlogits.stride(0) if r.T > 1 else max(dlogits.stride(0), r.E)
+    _check(_lib.lrm_route_bwd(C.byref(r.c), _ptr(expert), _ptr(dweight), _ptr(dlogits), ldd,
+                              _stream(stream)), "lrm_route_bwd")
+
+
+def lrm_route_share(T: int, k: int, expert, weight, e0: int, E: int, out_token, out_expert,
+                    out_weight, out_n, out_slot=None, ws=None, stream=None):
+    """The pairs of the experts [e0, e0 + E), in slot order: token, local
+    expert, weight and slot arrays [T*k] (the first out_n[0] entries)."""
+    n = int(T) * int(k)
+    for name, t, m, dt in (("expert", expert, n, torch.int32), ("weight", weight, n, torch.float32),
+                           ("out_token", out_token, n, torch.int32),
+                           ("out_expert", out_expert, n, torch.int32),
+                           ("out_weight", out_weight, n, torch.float32),
+                           ("out_slot", out_slot, n, torch.int32), ("out_n", out_n, 1, torch.int32)):
+        _slots(name, t, m, dt)
+    ws = _ws(_lib.lrm_route_share_workspace_size(int(T), int(k)), out_n.device, ws)
+    _check(_lib.lrm_route_share(int(T), int(k), _ptr(expert), _ptr(weight), int(e0), int(E),
+                                _ptr(out_token), _ptr(out_expert), _ptr(out_weight),
+                                _ptr(out_slot), _ptr(out_n), _ptr(ws), ws.numel(),
+                                _stream(stream)), "lrm_route_share")
+
+
+# ------------------------------------------------------ the experts forward
+class Forward:
+    """An lrm_forward plus the objects that keep its memory alive."""
+
+    def __init__(self, kind: int, pairs: Pairs, X, x_rows, residual, act: str = "none"):
+        self.pairs = pairs
+        self.keep = [pairs, X, residual]
+        self.c = lrm_forward()
+        self.c.kind, self.c.act, self.c.dtype = kind, ACTS[act], dtype_code(X)
+        self.c.pairs, self.c.X = pairs.c, mat(X, x_rows)
+        self.c.R = mat(residual, "token")
+
+
+def _dense(name, t, shape, dtype):
+    if tuple(t.shape) != tuple(shape) or t.dtype != dtype or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)}")
+
+
+def linear_forward(pairs: Pairs, X, x_rows, W, act="none", bias=None, residual=None) -> Forward:
+    """y_p = act(W_e x_p + bias_e) with W [E][d_out][d_in], bias [E][d_out]."""
+    if W.dim() != 3 or W.shape[0] != pairs.E or W.dtype != X.dtype or W.stride(2) != 1 or \
+            W.stride(1) != W.shape[2] or W.shape[2] != X.shape[1]:
+        raise ValueError("W must be [E][d_out][d_in] of X's dtype, dense inside an expert")
+    if bias is not None:
+        _dense("bias", bias, W.shape[:2], X.dtype)
+    f = Forward(LRM_LINEAR, pairs, X, x_rows, residual, act)
+    f.keep += [W, bias]
+    c = f.c
+    c.W, c.w_stride = _ptr(W), max(W.stride(0), W.shape[1] * W.shape[2])
+    c.bias = _ptr(bias)
+    c.d_in, c.d_out = W.shape[2], W.shape[1]
+    return f
+
+
+def swiglu_forward(pairs: Pairs, X, W_gate, W_up, W_down, residual=None) -> Forward:
+    """y_p = W_down (silu(W_gate x) * (W_up x)), weights as in swiglu_problem."""
+    H, I = X.shape[1], W_gate.shape[1]  # noqa: E741
+    for name, w, shape in (("W_gate", W_gate, (pairs.E, I, H)), ("W_up", W_up, (pairs.E, I, H)),
+                           ("W_down", W_down, (pairs.E, H, I))):
+        _dense(name, w, shape, X.dtype)
+    f = Forward(LRM_SWIGLU, pairs, X, "token", residual)
+    f.keep += [W_gate, W_up, W_down]
+    c = f.c
+    c.W_gate, c.W_up, c.W_down = _ptr(W_gate), _ptr(W_up), _ptr(W_down)
+    c.H, c.I = H, I
+    return f
+
+
+def lrm_forward_workspace_size(f: Forward) -> int:
+    return int(_lib.lrm_forward_workspace_size(C.byref(f.c)))
+
+
+def _marshal(struct, outputs: dict):
+    o = struct()
+    o._tensors = dict(outputs)  # the descriptor keeps its memory alive
+    for k, v in outputs.items():
+        if v is not None and not v.is_contiguous():
+            raise ValueError(f"output {k} must be contiguous")
+        setattr(o, k, _ptr(v))
+    return o
+
+
+def forward_outputs(outputs: dict) -> lrm_forward_outputs:
+    """The outputs of lrm_expert_forward (Y, Yp, Z, A, B, h_sumsq), marshalled
+    once for several calls."""
+    return _marshal(lrm_forward_outputs, outputs)
+
+
+def _grown(ws, need, device):
+    if ws is not None:
+        return ws
+    if need == 0:
+        return None
+    return torch.empty(need, dtype=torch.uint8, device=device)
+
+
+def lrm_expert_forward(f: Forward, outputs, ws=None, stream=None):
+    """The experts' forward pass; outputs: a dict or forward_outputs(dict)."""
+    o = forward_outputs(outputs) if isinstance(outputs, dict) else outputs
+    if ws is None:
+        ws = _grown(ws, lrm_forward_workspace_size(f), f.pairs.token.device)
+    _check(_lib.lrm_expert_forward(C.byref(f.c), C.byref(o), _ptr(ws),
+                                   ws.numel() if ws is not None else 0, _stream(stream)),
+           "lrm_expert_forward")
+    return ws
+
+
+# -------------------------------------------------- the epilogue's backward
+class PairGrad:
+    """An lrm_pair_grad_problem plus the objects that keep its memory alive."""
+
+    def __init__(self, pairs: Pairs, dY, dy_rows, Z, act: str):
+        self.pairs = pairs
+        self.keep = [pairs, dY, Z]
+        self.c = lrm_pair_grad_problem(ACTS[act], dtype_code(Z), pairs.c, mat(dY, dy_rows),
+                                       mat(Z, "pair"))
+
+
+def pair_grad_problem(pairs: Pairs, dY, dy_rows, Z, act="none") -> PairGrad:
+    return PairGrad(pairs, dY, dy_rows, Z, act)
+
+
+def lrm_pair_grad_workspace_size(g: PairGrad) -> int:
+    return int(_lib.lrm_pair_grad_workspace_size(C.byref(g.c)))
+
+
+def pair_grad_outputs(outputs: dict) -> lrm_pair_grad_outputs:
+    """The outputs of lrm_pair_grad (dweight, G, dbias), marshalled once."""
+    return _marshal(lrm_pair_grad_outputs, outputs)
+
+
+def lrm_pair_grad(g: PairGrad, outputs, ws=None, stream=None):
+    """Gradients of the routing weights, the projection's output and the bias;
+    outputs: a dict or pair_grad_outputs(dict)."""
+    o = pair_grad_outputs(outputs) if isinstance(outputs, dict) else outputs
+    if ws is None:
+        ws = _grown(ws, lrm_pair_grad_workspace_size(g), g.pairs.token.device)
+    _check(_lib.lrm_pair_grad(C.byref(g.c), C.byref(o), _ptr(ws),
+                              ws.numel() if ws is not None else 0, _stream(stream)),
+           "lrm_pair_grad")
     return ws
