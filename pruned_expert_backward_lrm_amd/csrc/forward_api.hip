@@ -148,7 +148,13 @@ struct FwdWs {
   void* H;       // SWIGLU: packed silu(a) b, [N][I]
   void* Yp;      // [N][d_out]
   int8_t* Ylo;   // bf16: [N][d_out]
+  void* Xp;      // X in packed order, where X is too large to gather from
 };
+
+int64_t x_bytes(const lrm_forward* f) {
+  const int64_t rows = f->X.rows == LRM_ROWS_PAIR ? f->pairs.N : f->pairs.T;
+  return rows > 0 ? ((rows - 1) * f->X.ld + f->X.cols) * esize(f->dtype) : 0;
+}
 
 FwdWs carve_forward(Carve& c, const lrm_forward* f) {
   FwdWs w{};
@@ -160,6 +166,7 @@ FwdWs carve_forward(Carve& c, const lrm_forward* f) {
   if (glu) w.H = c.take<char>(N * f->I * es);
   w.Yp = c.take<char>(N * d * es);
   if (f->dtype == LRM_BF16) w.Ylo = c.take<int8_t>(N * d);
+  if (x_bytes(f) > kFwdGatherMax) w.Xp = c.take<char>(N * f->X.cols * es);
   return w;
 }
 
@@ -175,6 +182,12 @@ lrm_status run_forward(const lrm_forward* f, const lrm_forward_outputs* out, voi
   g.offsets = w.b.offsets; g.kept = w.b.kept; g.mt_off = w.b.mt_off; g.token = p->token;
   g.gather = 1; g.x_pair = f->X.rows == LRM_ROWS_PAIR; g.X = f->X.ptr; g.ldx = f->X.ld;
   LRM_TRY_HIP(run_bucket(p, w.b, out->Y != nullptr, fwd_tile_rows(g), s));
+  g.x_bytes = x_bytes(f);
+  if (w.Xp) {
+    g.K = f->X.cols;
+    LRM_TRY_HIP(launch_fwd_pack(g, w.Xp, s));
+    g.gather = 0; g.X = w.Xp; g.ldx = g.K;
+  }
   const bool y_wanted = out->Y || out->Yp;
   void* const Y = out->Yp ? out->Yp : (out->Y ? w.Yp : nullptr);
   int d;

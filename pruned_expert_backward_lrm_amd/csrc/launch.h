@@ -300,12 +300,22 @@ struct FwdGemmArgs {
   const int32_t* mt_off;
   const int32_t* token;
   const void* X; int64_t ldx;
+  int64_t x_bytes;  // gather: from the first row of X to the end of the last one
   const void* W0; const void* W1; int64_t w_stride;  // [E][n][K]
   const void* bias;  // [E][n] or null
   void* A; void* B; void* H;
   void* Z; void* Y; int8_t* Ylo;
 };
+// The most x_bytes a gathering product takes (32-bit byte offsets, below the
+// one that stands for "outside"); larger inputs are packed first.  (The
+// CPU-emulation test build lowers it, so that its small cases pack.)
+#ifndef LRM_FWD_GATHER_MAX
+#define LRM_FWD_GATHER_MAX 0x7fff0000
+#endif
+constexpr int64_t kFwdGatherMax = LRM_FWD_GATHER_MAX;
 int fwd_tile_rows(const FwdGemmArgs& g);
+// out[m] = the A operand's row of packed row m, K dense columns
+hipError_t launch_fwd_pack(const FwdGemmArgs& g, void* out, hipStream_t s);
 hipError_t launch_fwd_gemm(const FwdGemmArgs& g, hipStream_t s);
 // out[kept[m]] = |H[m]|^2 in fp64 (glu)
 hipError_t launch_fwd_sumsq(const FwdGemmArgs& g, double* out, hipStream_t s);

@@ -167,6 +167,28 @@ inline F4 mfma16x16x32(V8 a, V8 b, F4 c) {
   return c;
 }
 
+// fp32: one k per lane group, A row = B column = lane % 16, k = lane / 16
+template <typename F4>
+inline F4 mfma16x16x4f32(float a, float b, F4 c) {
+  Wave& w = wave();
+  std::memcpy(w.wide[ctx.lane], &a, 4);
+  std::memcpy(w.wide[ctx.lane] + 16, &b, 4);
+  w.bar->arrive_and_wait();
+  const int l = ctx.lane;
+  for (int i = 0; i < 4; ++i) {
+    float s = c[i];
+    for (int k = 0; k < 4; ++k) {
+      float av, bv;
+      std::memcpy(&av, w.wide[4 * (l / 16) + i + 16 * k], 4);
+      std::memcpy(&bv, w.wide[l % 16 + 16 * k] + 16, 4);
+      s = std::fma(av, bv, s);
+    }
+    c[i] = s;
+  }
+  w.bar->arrive_and_wait();
+  return c;
+}
+
 template <typename... KArgs>
 struct Launch {
   dim3 g, b;
@@ -314,6 +336,7 @@ inline int update_dpp(int old, int src, int ctrl, int row_mask) {
 #define LRM_DYN_SHARED(T, name) T* name = reinterpret_cast<T*>(::emu::g_dyn)
 #define __builtin_amdgcn_wave_barrier() ::emu::wave_barrier()
 #define __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, x, y, z) ::emu::mfma16x16x32((a), (b), (c))
+#define __builtin_amdgcn_mfma_f32_16x16x4f32(a, b, c, x, y, z) ::emu::mfma16x16x4f32((a), (b), (c))
 
 namespace emu {
 // ds_read_b64_tr_b16: each lane addresses 8 bytes (four 16-bit elements);

@@ -18,6 +18,9 @@ import forward_cases as FC
 from test_cpu_emu import CLANG, CSRC, EMU, FLAGS, ROOT, _sources
 
 FULL = bool(os.environ.get("LRM_EMU_FULL"))
+# inputs of more bytes than this are packed before the product (2 GiB in the
+# product build; lowered here so that some of the small cases pack)
+GATHER_MAX = 20000
 
 
 @pytest.fixture(scope="module")
@@ -28,7 +31,7 @@ def driver(tmp_path_factory):
 
     def compile_one(src):
         obj = os.path.join(out, os.path.basename(src) + ".o")
-        r = subprocess.run([CLANG, *FLAGS, "-DLRM_CPU_EMU", "-x", "c++", "-I", EMU, "-I",
+        r = subprocess.run([CLANG, *FLAGS, "-DLRM_CPU_EMU", f"-DLRM_FWD_GATHER_MAX={GATHER_MAX}", "-x", "c++", "-I", EMU, "-I",
                             os.path.join(ROOT, "include"), "-I", CSRC, "-c", src, "-o", obj],
                            capture_output=True, text=True)
         if r.returncode != 0:
@@ -54,7 +57,7 @@ def _raw(v) -> bytes:
     return np.int64(len(b)).tobytes() + b
 
 
-def call(exe, tmp_path, nums, arrays, outs, expect=(0, 0)):
+def call(exe, tmp_path, nums, arrays, outs, expect=(0, 0), env_extra=None):
     """outs: [(shape, dtype)] in the driver's order; returns CPU tensors that
     held bytes 0xCD before the call."""
     h = np.zeros(32, np.int64)
@@ -62,6 +65,8 @@ def call(exe, tmp_path, nums, arrays, outs, expect=(0, 0)):
     fin, fout = tmp_path / "in.bin", tmp_path / "out.bin"
     fin.write_bytes(h.tobytes() + b"".join(_raw(a) for a in arrays))
     env = dict(os.environ, ASAN_OPTIONS="detect_leaks=0:abort_on_error=1")
+    env.pop("LRM_FWD_TILE", None)
+    env.update(env_extra or {})
     res = subprocess.run([exe, str(fin), str(fout)], capture_output=True, text=True, timeout=600,
                          env=env)
     assert res.returncode == 0, f"emulated run failed ({res.returncode}):\n{res.stderr[-6000:]}"
@@ -153,7 +158,7 @@ def test_emu_share(driver, tmp_path, T, k, e0, E):
         assert (got[m:].view(torch.uint8) == 0xCD).all()
 
 
-def emu_forward(driver, tmp_path, c):
+def emu_forward(driver, tmp_path, c, env_extra=None):
     shapes = FC.forward_shapes(c)
     order = ("Y", "Yp", "Z", "A", "B", "h_sumsq")
     pr = c["pairs"]
@@ -165,7 +170,7 @@ def emu_forward(driver, tmp_path, c):
     x = x[:x.numel() - (c["ldx"] - c["d_in"])]
     w = [c["W"], c["bias_t"]] if c["kind"] == "linear" else [c["W_gate"], c["W_up"], c["W_down"]]
     got = call(driver, tmp_path, nums, [pr["token"], pr["expert"], pr["weight"], x, c["R"], *w],
-               [shapes[k] for k in order if k in shapes], expect=(0, 8 if c["bad"] else 0))
+               [shapes[k] for k in order if k in shapes], expect=(0, 8 if c["bad"] else 0), env_extra=env_extra)
     got = dict(zip([k for k in order if k in shapes], got))
     FC.judge_forward(c, got, {k: held(*shapes[k]) for k in got})
 
@@ -177,6 +182,14 @@ SMALL_FORWARD = ["lin_one", "lin_one_f32", "lin_odd", "lin_none", "lin_bad", "gl
 @pytest.mark.parametrize("name", list(FC.FORWARD_CASES) if FULL else SMALL_FORWARD)
 def test_emu_forward(driver, tmp_path, name):
     emu_forward(driver, tmp_path, FC.forward_case(name))
+
+
+@pytest.mark.parametrize("name", ["lin_skew", "lin_odd_f32", "glu_small", "glu_small_f32"])
+@pytest.mark.parametrize("tile", ["128", "256"])
+def test_emu_forward_tiles(driver, tmp_path, name, tile):
+    """The larger tiles on cases small enough to emulate (one that packs its
+    input first among them)."""
+    emu_forward(driver, tmp_path, FC.forward_case(name), {"LRM_FWD_TILE": tile})
 
 
 @pytest.mark.parametrize("name", list(FC.PAIR_GRAD_CASES) if FULL else

@@ -174,6 +174,42 @@ def test_forward(L, name):
         assert torch.equal(out[k].view(torch.uint8), again[k].view(torch.uint8)), k
 
 
+@pytest.mark.parametrize("tile", ["64", "128", "256"])
+@pytest.mark.parametrize("name", ["lin_one", "lin_tiny_f32", "lin_odd", "lin_odd_f32", "lin_skew",
+                                  "lin_bad", "glu_t17", "glu_small", "glu_small_f32", "glu_mid"])
+def test_forward_tiles(L, monkeypatch, name, tile):
+    """Every row tile of the products on every kind of case."""
+    monkeypatch.setenv("LRM_FWD_TILE", tile)
+    c = FC.forward_case(name)
+    out, before = run_forward(L, c)
+    FC.judge_forward(c, out, before)
+
+
+def test_forward_input_past_2_gib(L):
+    """X of more than 2 GiB: byte offsets of its last rows pass 31 bits."""
+    T, H, d, k = 540_000, 2048, 64, 1
+    rng = np.random.default_rng(1)
+    rows = np.unique(np.concatenate([[0, 1, T - 1], rng.integers(0, T, 90)])).astype(np.int32)
+    N = rows.size
+    c = dict(kind="linear", T=T, E=2, k=k, d_in=H, d=d, dtype="bf16", act="none", x_rows="token",
+             N=N, bias_t=None, R=None, d_out=d, bad=False, outs=("Yp",))
+    c["pairs"] = dict(token=rows, expert=rng.integers(0, 2, N).astype(np.int32),
+                      weight=np.ones(N, np.float32))
+    g = FC.gen("big")
+    c["W"] = FC.normal(g, 2, d, H, std=0.02, dtype=torch.bfloat16)
+    small = FC.normal(g, N, H, dtype=torch.bfloat16)
+    X = torch.full((T, H), float("nan"), dtype=torch.bfloat16, device=DEV)  # rows no pair reads
+    X[dev(torch.from_numpy(rows)).long()] = dev(small)
+    f = L.linear_forward(gpu_pairs(L, c), X, "token", dev(c["W"]))
+    out = dict(Yp=filled((N, d), torch.bfloat16))
+    L.lrm_expert_forward(f, out)
+    torch.cuda.synchronize()
+    # the same pairs over the rows alone
+    c["pairs"] = dict(c["pairs"], token=np.arange(N, dtype=np.int32))
+    c.update(T=N, X=small)
+    FC.judge_forward(c, out)
+
+
 def test_forward_in_place_residual(L):
     c = FC.forward_case("glu_small")
     f = make_forward(L, c)
