@@ -28,6 +28,16 @@ __device__ __forceinline__ uint32_t f32_to_bf16_bits(float f) {
 __device__ __forceinline__ uint32_t pack_bf16x2(float lo, float hi) {
   return f32_to_bf16_bits(lo) | (f32_to_bf16_bits(hi) << 16);
 }
+// The same two roundings in one instruction of gfx950 (infinities and NaN kept).
+__device__ __forceinline__ uint32_t cvt_pk_bf16(float lo, float hi) {
+#ifdef LRM_CPU_EMU
+  return pack_bf16x2(lo, hi);
+#else
+  typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+  typedef float f32x2 __attribute__((ext_vector_type(2)));
+  return __builtin_bit_cast(uint32_t, __builtin_convertvector((f32x2{lo, hi}), bf16x2));
+#endif
+}
 
 // ------------------------------------------------------- wave reductions
 __device__ __forceinline__ double wave_sum(double v) {

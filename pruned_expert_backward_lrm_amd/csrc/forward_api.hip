@@ -66,6 +66,7 @@ struct BucketWs {
   int32_t* offsets;
   int32_t* kept;
   int32_t* pos;
+  int32_t* tokens;
   int32_t* tok_off;
   int32_t* mt_off;
 };
@@ -80,6 +81,7 @@ BucketWs carve_bucket(Carve& c, const lrm_pairs* p) {
   w.offsets = c.take<int32_t>(p->E + 1);
   w.kept = c.take<int32_t>(p->N);
   w.pos = c.take<int32_t>(p->N);
+  w.tokens = c.take<int32_t>(p->N);
   w.tok_off = c.take<int32_t>((int64_t)p->T + 1);
   w.mt_off = c.take<int32_t>(p->E + 1);
   return w;
@@ -89,7 +91,7 @@ hipError_t run_bucket(const lrm_pairs* p, const BucketWs& w, bool tok, int mt_bm
   BucketArgs b{};
   b.N = p->N; b.T = p->T; b.E = p->E; b.token = p->token; b.expert = p->expert;
   b.blkcnt = w.blkcnt; b.cand_off = w.cand_off; b.offsets = w.offsets; b.cand = w.kept;
-  b.pos = w.pos; b.keep_all = 1; b.err = w.err; b.blkerr = w.blkerr;
+  b.pos = w.pos; b.tokens = w.tokens; b.keep_all = 1; b.err = w.err; b.blkerr = w.blkerr;
   b.tok_off = tok && p->N > 0 ? w.tok_off : nullptr;
   b.mt_off = mt_bm > 0 ? w.mt_off : nullptr; b.mt_bm = mt_bm; b.max_kept = -1;
   hipError_t e = launch_bucket(b, s);
@@ -148,6 +150,7 @@ struct FwdWs {
   void* H;       // SWIGLU: packed silu(a) b, [N][I]
   void* Yp;      // [N][d_out]
   int8_t* Ylo;   // bf16: [N][d_out]
+  void* dump;    // 1 KB that lanes outside a tile store to
   void* Xp;      // X in packed order, where X is too large to gather from
 };
 
@@ -166,6 +169,7 @@ FwdWs carve_forward(Carve& c, const lrm_forward* f) {
   if (glu) w.H = c.take<char>(N * f->I * es);
   w.Yp = c.take<char>(N * d * es);
   if (f->dtype == LRM_BF16) w.Ylo = c.take<int8_t>(N * d);
+  w.dump = c.take<char>(1024);
   if (x_bytes(f) > kFwdGatherMax) w.Xp = c.take<char>(N * f->X.cols * es);
   return w;
 }
@@ -179,8 +183,9 @@ lrm_status run_forward(const lrm_forward* f, const lrm_forward_outputs* out, voi
   const FwdWs w = carve_forward(c, f);
   FwdGemmArgs g{};
   g.N = p->N; g.E = p->E; g.bf16 = bf16;
-  g.offsets = w.b.offsets; g.kept = w.b.kept; g.mt_off = w.b.mt_off; g.token = p->token;
-  g.gather = 1; g.x_pair = f->X.rows == LRM_ROWS_PAIR; g.X = f->X.ptr; g.ldx = f->X.ld;
+  g.offsets = w.b.offsets; g.kept = w.b.kept; g.mt_off = w.b.mt_off; g.dump = w.dump;
+  g.rows = f->X.rows == LRM_ROWS_PAIR ? w.b.kept : w.b.tokens;
+  g.gather = 1; g.X = f->X.ptr; g.ldx = f->X.ld;
   LRM_TRY_HIP(run_bucket(p, w.b, out->Y != nullptr, fwd_tile_rows(g), s));
   g.x_bytes = x_bytes(f);
   if (w.Xp) {

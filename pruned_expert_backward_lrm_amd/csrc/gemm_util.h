@@ -118,6 +118,16 @@ __device__ __forceinline__ void dma16(dma_rsrc r, uint16_t* lds, int voff) {
   const u32x4 v = bload(r, voff);
   std::memcpy(reinterpret_cast<char*>(lds) + 16 * lane_id(), &v, 16);
 }
+// the same at byte voff + soff (soff wave-uniform)
+__device__ __forceinline__ void dma16(dma_rsrc r, uint16_t* lds, int voff, int soff) {
+  dma16(r, lds, voff + soff);
+}
+// 4 bytes per lane, to LDS at lds + 4 * lane
+__device__ __forceinline__ void dma4(dma_rsrc r, int* lds, int voff) {
+  int v = 0;
+  if (voff + 4 <= r.n) std::memcpy(&v, r.base + voff, 4);
+  lds[lane_id()] = v;
+}
 __device__ __forceinline__ dma_rsrc uniform(dma_rsrc r) { return r; }
 #else
 typedef u32x4 dma_rsrc;  // buffer resource words: base, bound, raw access
@@ -129,6 +139,22 @@ __device__ __forceinline__ dma_rsrc make_dma_rsrc(const char* base, int64_t nbyt
 __device__ __forceinline__ void dma16(dma_rsrc r, uint16_t* lds, int voff) {
   const uint32_t la = (uint32_t)(uintptr_t)(lds_vptr)lds;
   asm volatile("s_nop 4\n\tbuffer_load_dwordx4 %0, %1, 0 offen lds"
+               :
+               : "v"(voff), "s"(r), "{m0}"(la)
+               : "memory");
+}
+// the same at byte voff + soff (soff wave-uniform)
+__device__ __forceinline__ void dma16(dma_rsrc r, uint16_t* lds, int voff, int soff) {
+  const uint32_t la = (uint32_t)(uintptr_t)(lds_vptr)lds;
+  asm volatile("s_nop 4\n\tbuffer_load_dwordx4 %0, %1, %2 offen lds"
+               :
+               : "v"(voff), "s"(r), "s"(soff), "{m0}"(la)
+               : "memory");
+}
+// 4 bytes per lane, to LDS at lds + 4 * lane
+__device__ __forceinline__ void dma4(dma_rsrc r, int* lds, int voff) {
+  const uint32_t la = (uint32_t)(uintptr_t)(lds_vptr)lds;
+  asm volatile("s_nop 4\n\tbuffer_load_dword %0, %1, 0 offen lds"
                :
                : "v"(voff), "s"(r), "{m0}"(la)
                : "memory");

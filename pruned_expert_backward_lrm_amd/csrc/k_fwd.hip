@@ -8,6 +8,7 @@
 //   join: out[t] = R[t] + sum over the pairs p of t of w_p y_p
 // x is row token[p] or p of X, or row m of the packed H.
 #include <cstdlib>
+#include <type_traits>
 
 #include "common.h"
 #include "gemm_util.h"
@@ -27,15 +28,43 @@ __device__ __forceinline__ float act_rt(int act, float z) {
 }
 
 // y between the down product and the join takes 24 bits: its bf16 rounding
-// (which is Yp where the caller wants it) and the next 8 bits of the
-// difference, as a signed byte of the bit pattern.  With bf16 alone Y would
-// carry two roundings of half the terms' size on top of its own.
-__device__ __forceinline__ uint32_t split_lo(float y, uint32_t hi) {
-  const int d = ((int)__float_as_uint(y) - (int)(hi << 16) + 128) >> 8;
-  return (uint32_t)(d > 127 ? 127 : d) & 0xffu;
+// (which is Yp where the caller wants it) and the next 8 bits, a signed byte of
+// the difference of the bit patterns.  With bf16 alone Y would carry two
+// roundings of half the terms' size on top of its own.  The lowest bit is set
+// first, so that no value lies half-way between two bf16 values: the byte is
+// then bits 8 .. 15 themselves, read as signed.  The join adds half of the last
+// place: 2^-16 of the value at most.
+__device__ __forceinline__ float odd(float y) { return __uint_as_float(__float_as_uint(y) | 1u); }
+// bits 8 .. 15 of four values
+__device__ __forceinline__ uint32_t next_bytes(f32x4 y) {
+  const uint32_t lo = __builtin_amdgcn_perm(__float_as_uint(y[1]), __float_as_uint(y[0]), 0x00000501u);
+  const uint32_t hi = __builtin_amdgcn_perm(__float_as_uint(y[3]), __float_as_uint(y[2]), 0x00000501u);
+  return (lo & 0xffffu) | hi << 16;
 }
 __device__ __forceinline__ float join_bits(uint32_t hi16, int lo8) {
-  return __uint_as_float((hi16 << 16) + (uint32_t)(lo8 << 8));
+  return __uint_as_float((hi16 << 16) + (uint32_t)(lo8 * 256 + 128));
+}
+
+// act of a wave's row of fragments; one loop over registers for each kind
+template <int FO>
+__device__ __forceinline__ void act_rows(int act, f32x4 (&u)[FO]) {
+  auto all = [&](auto f) {
+#pragma unroll
+    for (int j = 0; j < FO; ++j)
+#pragma unroll
+      for (int q = 0; q < 4; ++q) u[j][q] = f(u[j][q]);
+  };
+  if (act == kActRelu)
+    all([](float z) { return act_of<kActRelu>(z); });
+  else if (act == kActGelu)
+    all([](float z) { return act_of<kActGelu>(z); });
+  else
+    all([](float z) { return act_of<kActSilu>(z); });
+}
+
+// silu for results that are rounded to bf16: the hardware's exp2 and reciprocal
+__device__ __forceinline__ float silu_fast(float a) {
+  return a * __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(a * -1.44269504088896341f));
 }
 
 // V consecutive columns of a row, V = 8 in bf16 and 4 in fp32 (16 bytes).
@@ -69,7 +98,7 @@ struct Vec {
   }
 };
 
-// The outputs of V consecutive columns c .. (c < n, n a multiple of V) of
+// fp32: the outputs of V consecutive columns c .. (c < n, n a multiple of V) of
 // packed row m, pair p: u = W0 x, v = W1 x (GLU).
 template <bool BF16, bool GLU>
 __device__ __forceinline__ void emit(const FwdGemmArgs& g, int e, int m, int p, int c, Vec<BF16> u,
@@ -95,15 +124,6 @@ __device__ __forceinline__ void emit(const FwdGemmArgs& g, int e, int m, int p, 
       for (int j = 0; j < V; ++j) u.v[j] = act_rt(g.act, u.v[j]);
     }
     u.store(g.Y, pr);
-    if constexpr (BF16) {
-      if (g.Ylo) {
-        uint32_t lo[2] = {0u, 0u};
-#pragma unroll
-        for (int j = 0; j < 8; ++j)
-          lo[j >> 2] |= split_lo(u.v[j], f32_to_bf16_bits(u.v[j])) << (8 * (j & 3));
-        *reinterpret_cast<u32x2*>(g.Ylo + pr) = u32x2{lo[0], lo[1]};
-      }
-    }
   }
 }
 
@@ -111,30 +131,42 @@ __device__ __forceinline__ void emit(const FwdGemmArgs& g, int e, int m, int p, 
 //
 // Output tiles of BM packed rows of one expert x BN weight rows (GLU: BN/2 of
 // W0 and the same BN/2 of W1, so that a lane holds a and b of the same
-// elements).  Both operands have k contiguous in memory: 128-byte pieces of
-// their rows (64 k in bf16, 32 in fp32) go straight from memory into LDS
-// (dma16), two stages deep, in the swizzled granule order of lds_off; a row
-// gathered through kept and token costs nothing more, since every lane brings
-// its own offset.  Lanes past an expert's rows, past the columns or past K
-// take an offset outside the bound and write zeros.
+// elements).  Both operands have k contiguous in memory: 64-byte pieces of
+// their rows (32 k in bf16, 16 in fp32) go straight from memory into LDS
+// (dma16), kStages deep; a row gathered through the pairs costs nothing more,
+// since every lane brings its own offset.  Lanes past an expert's rows, past
+// the columns or past K take an offset outside the bound and write zeros.
+// Granule G (16 bytes) of row r sits at G ^ swz64(r): the four 16-lane passes
+// of a 16-byte LDS read then hit 16 distinct slots of the banks each.
+//
+// Pipeline: while the products of k-tile k run from registers, the fragments
+// of k + 1 are read from LDS and the loads of k + 2 .. k + 4 are in flight.
+// Depth decides: with two stages of 64 k (one k-tile in flight) the same
+// products took 857 us instead of 592 when the loads were left out (Qwen3
+// gate/up, 131072 rows, without stores).  Waits name how many younger memory
+// instructions may stand (the counter retires in order), so that neither the
+// loads behind a k-tile nor a finished tile's stores are waited for.
 //
 // Persistent blocks: each XCD (block b runs on XCD b mod 8) owns a contiguous
 // eighth of the tiles, in which an expert's tiles lie 8 row tiles high, column
 // by column, so that the tiles running on it at a time share operand panels in
-// its L2.  The next tile's rows are looked up during the current one, and its
-// first loads are in flight while the current tile is stored.
+// its L2 (1.24 GB fetched for 0.8 GB of weights and 0.54 GB of gathered rows).
 //
 // fp32 runs v_mfma_f32_16x16x4: a lane's 16-byte granule holds four k, and
 // step s multiplies the s-th of every lane.  Which k those are is the same for
 // both operands, so every k is met once.
+constexpr int kStages = 4;
+
 template <int BM_, int BN_, int WGM_, int WGN_>
 struct FwdCfg {
   static constexpr int BM = BM_, BN = BN_, WGM = WGM_, WGN = WGN_, NW = WGM * WGN, NT = 64 * NW;
   static constexpr int TM = BM / WGM, TN = BN / WGN, FM = TM / 16, FN = TN / 16;
-  static constexpr int QA = BM / 8 / NW, QB = BN / 8 / NW;  // 1 KB loads per wave and stage
-  static constexpr int SA = BM * 128, SS = (BM + BN) * 128;  // bytes of a stage
-  static_assert(BM % (8 * NW) == 0 && BN % (8 * NW) == 0 && TN % 32 == 0 && TM % 16 == 0, "tile");
+  static constexpr int QA = BM / 16 / NW, QB = BN / 16 / NW;  // 1 KB loads per wave and stage
+  static constexpr int SA = BM * 64, SS = (BM + BN) * 64;     // bytes of a stage
+  static_assert(BM % (16 * NW) == 0 && BN % (16 * NW) == 0 && TN % 32 == 0 && TM % 32 == 0, "tile");
 };
+
+__device__ __forceinline__ int swz64(int r) { return (4 - ((r >> 2) & 3)) & 3; }
 
 struct FwdJob {
   int e, m0, rows, n0;
@@ -174,71 +206,243 @@ __device__ __forceinline__ f32x4 mma(u32x4 b, u32x4 a, f32x4 c) {
   }
 }
 
-// All of this wave's loads into LDS have arrived, and every wave's have.
-__device__ __forceinline__ void stage_barrier() {
+// Waits until at most n of this wave's memory instructions are outstanding (n
+// rounded down to a value of the ladder; L loads make a stage) and all its LDS
+// reads have arrived, then the barrier.  The empty asm statements keep memory
+// accesses on their side.
+template <int L>
+__device__ __forceinline__ void stage_barrier(int n) {
   asm volatile("" ::: "memory");
-  wait_vm<0>();
+  if (n == 2 * L) wait_vm<2 * L>();
+  else if (n >= 56) wait_vm<56>();
+  else if (n >= 40) wait_vm<40>();
+  else if (n >= 32) wait_vm<32>();
+  else if (n >= 24) wait_vm<24>();
+  else if (n >= 16) wait_vm<16>();
+  else if (n >= 2 * L) wait_vm<2 * L>();
+  else if (n >= L) wait_vm<L>();
+  else wait_vm<0>();
   __builtin_amdgcn_s_barrier();
   asm volatile("" ::: "memory");
 }
 
 // ---------------------------------------------------------------- tile store
-// The sums of a tile go through LDS (the stage just consumed, in passes of two
-// fragment rows of every wave), so that the epilogue works on whole rows: a
-// thread takes 16 output bytes of a row, its neighbours the next ones.  In the
-// MFMA layout a store would write 16 rows x 8 bytes, at a quarter of the rate
-// (measured for the backward products' tiles).  LDS rows hold the BN sums of a
-// row, granules of four swizzled by the row.
-template <class C, bool BF16, bool GLU>
-__device__ __forceinline__ void fwd_store(const FwdGemmArgs& g, const FwdJob& job,
-                                          const f32x4 (&acc)[C::FM][C::FN], char* buf, const int* prow,
-                                          int w, int l) {
-  constexpr int BNO = GLU ? C::BN / 2 : C::BN, HN = C::TN / 2;
-  constexpr int V = Vec<BF16>::V, QR = BNO / V, RB = C::BN * 4, ROWS = C::WGM * 32;
-  static_assert(ROWS * RB <= C::SS, "a pass fits a stage");
+// A wave stores its sub-tile 16 rows at a time through a piece of LDS of its
+// own (kStoreBytes; no other wave waits), so that 8 lanes write 128 bytes of a
+// row (fewer where the wave's sub-tile is narrower): in the MFMA layout a bf16
+// store writes 16 rows x 8 bytes, at a quarter of the rate (measured for the
+// backward products' tiles).  The LDS serves a wave in order, so the next
+// piece is written as soon as this one's reads are issued.  Granules of 16
+// bytes are swizzled by the row.  Lanes outside the tile store to a dump in
+// the workspace instead of being masked off: every store is then issued, and
+// their number, which the function returns, is known to the waits.
+//
+// fp32 lanes hold 16 bytes of a row and store them directly (not counted: 0).
+constexpr int kStoreBytes = 3072;
+
+// 16 rows of FO * 16 bf16 columns from the MFMA layout (v: four columns a
+// fragment) to granules: lane l then holds granule l % (2 FO) of rows
+// l / (2 FO) + q * 32 / FO in out[q] (FO = 1: lanes 0 .. 31 only).
+template <int FO>
+struct Piece {
+  static constexpr int GR = 2 * FO, NQ = FO > 1 ? FO / 2 : 1, STEP = 64 / GR;
+  __device__ __forceinline__ static int row(int l, int q) { return (l / GR + q * STEP) & 15; }
+  __device__ __forceinline__ static void pass(char* buf, int l, const u32x2 (&v)[FO], u32x4 (&out)[NQ]) {
+    const int lrow = l & 15, lq = l >> 4;
+#pragma unroll
+    for (int j = 0; j < FO; ++j)
+      *reinterpret_cast<u32x2*>(buf + lrow * (GR * 16) + (((j * 2 + (lq >> 1)) ^ (lrow & (GR - 1))) << 4) +
+                                (lq & 1) * 8) = v[j];
+    wave_sync();
+#pragma unroll
+    for (int q = 0; q < NQ; ++q) {
+      const int r = row(l, q);
+      out[q] = *reinterpret_cast<const u32x4*>(buf + r * (GR * 16) + (((l % GR) ^ (r & (GR - 1))) << 4));
+    }
+    wave_sync();
+  }
+};
+
+__device__ __forceinline__ u32x2 pack4(f32x4 v) {
+  return u32x2{cvt_pk_bf16(v[0], v[1]), cvt_pk_bf16(v[2], v[3])};
+}
+
+// EPI: with a bias, an activation or Z (not GLU)
+template <class C, bool BF16, bool GLU, bool EPI>
+__device__ __forceinline__ int fwd_store(const FwdGemmArgs& g, const FwdJob& job,
+                                         const f32x4 (&acc)[C::FM][C::FN], char* buf, const int* prow,
+                                         int w, int l) {
+  constexpr int FO = GLU ? C::FN / 2 : C::FN;  // output fragments of a wave row
+  typedef Piece<FO> P;
   const int wm = w / C::WGN, wn = w % C::WGN;
+  const int cw = job.n0 + wn * FO * 16;  // first column of the wave
+  const int lrow = l & 15, lq = l >> 4;  // MFMA layout: row, four columns
+  char* const dump = (char*)g.dump + l * 16;
+  int stores = 0;
 #pragma unroll
-  for (int i0 = 0; i0 < C::FM; i0 += 2) {
-    __syncthreads();  // the buffer's readers are done
+  for (int i = 0; i < C::FM; ++i) {
+    const int r0 = wm * C::TM + i * 16;
+    if (r0 >= job.rows) break;
+    if constexpr (!BF16) {
+      if (r0 + lrow >= job.rows) continue;
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const int r = wm * 32 + i * 16 + (l & 15);
+      for (int j = 0; j < FO; ++j) {
+        const int c = cw + j * 16 + lq * 4;
+        if (c >= g.n) continue;
+        Vec<BF16> u, v;
 #pragma unroll
-      for (int j = 0; j < C::FN; ++j) {
-        // column of the sums in the LDS row: W0's, then W1's
-        const int c = !GLU ? wn * C::TN + j * 16
-                           : (j * 16 >= HN ? BNO - HN : 0) + wn * HN + j * 16;
-        const int q = c / 4 + (l >> 4);
-        *reinterpret_cast<f32x4*>(buf + r * RB + ((q ^ (r & 15)) << 4)) = acc[i0 + i][j];
+        for (int q = 0; q < 4; ++q) {
+          u.v[q] = acc[i][j][q];
+          v.v[q] = acc[i][GLU ? j + FO : j][q];
+        }
+        emit<BF16, GLU>(g, job.e, job.m0 + r0 + lrow, prow[r0 + lrow], c, u, v);
+      }
+    } else {
+      // the lane's rows and columns of a piece
+      int64_t at[P::NQ];  // element in a PAIR output
+      bool in[P::NQ];
+      const int c = cw + l % P::GR * 8;
+#pragma unroll
+      for (int q = 0; q < P::NQ; ++q) {
+        const int r = r0 + P::row(l, q);
+        in[q] = r < job.rows && c < g.n && (FO > 1 || l < 32);
+        at[q] = (int64_t)prow[r] * g.n + c;
+      }
+      auto put = [&](void* base, const u32x2 (&v)[FO]) {
+        u32x4 out[P::NQ];
+        P::pass(buf, l, v, out);
+#pragma unroll
+        for (int q = 0; q < P::NQ; ++q)
+          *reinterpret_cast<u32x4*>(in[q] ? (char*)base + at[q] * 2 : dump) = out[q];
+        stores += P::NQ;
+      };
+      u32x2 v[FO];
+      if constexpr (GLU) {
+        if (g.A) {
+#pragma unroll
+          for (int j = 0; j < FO; ++j) v[j] = pack4(acc[i][j]);
+          put(g.A, v);
+        }
+        if (g.B) {
+#pragma unroll
+          for (int j = 0; j < FO; ++j) v[j] = pack4(acc[i][j + FO]);
+          put(g.B, v);
+        }
+#pragma unroll
+        for (int j = 0; j < FO; ++j) {
+          const f32x4 x = acc[i][j], y = acc[i][j + FO];
+          f32x4 h;
+#pragma unroll
+          for (int q = 0; q < 4; ++q) h[q] = silu_fast(x[q]) * y[q];
+          v[j] = pack4(h);
+        }
+#pragma unroll
+        for (int q = 0; q < P::NQ; ++q) at[q] = (int64_t)(job.m0 + r0 + P::row(l, q)) * g.n + c;
+        put(g.H, v);
+      } else {
+        f32x4 u[FO];
+#pragma unroll
+        for (int j = 0; j < FO; ++j) u[j] = acc[i][j];
+        if (EPI && g.bias) {
+#pragma unroll
+          for (int j = 0; j < FO; ++j) {
+            const int cb = cw + j * 16 + lq * 4;
+            const u32x2 b = *reinterpret_cast<const u32x2*>((const uint16_t*)g.bias +
+                                                            (int64_t)job.e * g.n + (cb < g.n ? cb : 0));
+            u[j] += f32x4{bf16_lo(b[0]), bf16_hi(b[0]), bf16_lo(b[1]), bf16_hi(b[1])};
+          }
+        }
+        if (EPI && g.Z) {
+#pragma unroll
+          for (int j = 0; j < FO; ++j) v[j] = pack4(u[j]);
+          put(g.Z, v);
+        }
+        if (!EPI || g.Y) {
+          if (EPI && g.act != kActNone) act_rows<FO>(g.act, u);
+#pragma unroll
+          for (int j = 0; j < FO; ++j) {
+#pragma unroll
+            for (int q = 0; q < 4; ++q) u[j][q] = odd(u[j][q]);
+            v[j] = pack4(u[j]);
+          }
+          put(g.Y, v);
+          if (g.Ylo) {
+            // 16 rows of FO * 16 bytes: lane l holds 16 columns of row l / FO
+#pragma unroll
+            for (int j = 0; j < FO; ++j)
+              *reinterpret_cast<uint32_t*>(buf + lrow * (FO * 16) + ((j ^ (lrow >> 1 & (FO - 1))) << 4) +
+                                           lq * 4) = next_bytes(u[j]);
+            wave_sync();
+            const int r = l / FO & 15, cl = cw + l % FO * 16;
+            const u32x4 lo = *reinterpret_cast<const u32x4*>(buf + r * (FO * 16) +
+                                                             (((l % FO) ^ (r >> 1 & (FO - 1))) << 4));
+            wave_sync();
+            const bool inl = r0 + r < job.rows && cl < g.n && l < 16 * FO;
+            char* d = (char*)g.Ylo + (int64_t)prow[r0 + r] * g.n + cl;
+            // (n is a multiple of 8: so are the bytes' addresses)
+            *reinterpret_cast<u32x2*>(inl ? d : dump) = u32x2{lo[0], lo[1]};
+            *reinterpret_cast<u32x2*>(inl && cl + 8 < g.n ? d + 8 : dump) = u32x2{lo[2], lo[3]};
+            stores += 2;
+          }
+        }
       }
     }
-    __syncthreads();
-    for (int u = threadIdx.x; u < ROWS * QR; u += C::NT) {
-      const int r = u / QR, c = u % QR * V;
-      const int row = (r >> 5) * C::TM + i0 * 16 + (r & 31);  // row of the tile
-      if (row >= job.rows || job.n0 + c >= g.n) continue;
-      auto sums = [&](int col) {
-        Vec<BF16> x;
+  }
+  return stores;
+}
+
+// The operand fragments of a stage (32 k in bf16): 16 bytes per lane each.
+template <class C>
+struct Frags {
+  u32x4 a[C::FM], b[C::FN];
+  // ao, bo: the lane's offsets of fragment 0 (the swizzle is the same 16 rows on)
+  __device__ __forceinline__ void read(const char* stage, int ao, int bo) {
 #pragma unroll
-        for (int q = 0; q < V / 4; ++q) {
-          const f32x4 y = *reinterpret_cast<const f32x4*>(buf + r * RB + (((col / 4 + q) ^ (r & 15)) << 4));
+    for (int j = 0; j < C::FN; ++j) b[j] = *reinterpret_cast<const u32x4*>(stage + C::SA + bo + j * 1024);
 #pragma unroll
-          for (int j = 0; j < 4; ++j) x.v[4 * q + j] = y[j];
-        }
-        return x;
-      };
-      emit<BF16, GLU>(g, job.e, job.m0 + row, prow[row], job.n0 + c, sums(c), sums(GLU ? BNO + c : c));
-    }
+    for (int i = 0; i < C::FM; ++i) a[i] = *reinterpret_cast<const u32x4*>(stage + ao + i * 1024);
+  }
+  // rows [I0, I1) of the fragments
+  template <bool BF16, int I0, int I1>
+  __device__ __forceinline__ void multiply(f32x4 (&acc)[C::FM][C::FN]) const {
+#pragma unroll
+    for (int i = I0; i < I1; ++i)
+#pragma unroll
+      for (int j = 0; j < C::FN; ++j) acc[i][j] = mma<BF16>(b[j], a[i], acc[i][j]);
+  }
+};
+
+// The next k-tile's LDS reads spread over the first half of this one's products.
+template <class C, bool BF16>
+__device__ __forceinline__ void interleave() {
+  constexpr int reads = C::FM + C::FN, mmas = C::FM / 2 * C::FN * (BF16 ? 1 : 4);
+  constexpr int per = mmas / reads > 0 ? mmas / reads : 1;
+#pragma unroll
+  for (int q = 0; q < reads; ++q) {
+    __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);    // an LDS read
+    __builtin_amdgcn_sched_group_barrier(0x008, per, 0);  // MFMAs
   }
 }
 
-template <class C, bool BF16, bool GLU>
+// Where the loads stand: a tile, its k-tile and what the next load takes.
+template <class C>
+struct FwdFeed {
+  FwdJob job;
+  int k;
+  dma_rsrc a, w0, w1;  // the operands' rows from k = 0, to their ends
+  int off[C::QA];
+};
+
+template <class C, bool BF16, bool GLU, bool EPI>
 __global__ __launch_bounds__(C::NT, 2) void k_fwd_tile(FwdGemmArgs g) {
-  constexpr int ES = BF16 ? 2 : 4, KT = 128 / ES;  // k per stage
-  constexpr int BNO = GLU ? C::BN / 2 : C::BN;     // output columns of a tile
-  constexpr int HN = C::TN / 2;                    // GLU: a wave's columns of each product
-  __shared__ __attribute__((aligned(1024))) char lds[2 * C::SS];
-  __shared__ int prow[2][C::BM];  // pair of every row of the tile
+  constexpr int ES = BF16 ? 2 : 4, KT = 64 / ES;  // k per stage
+  constexpr int BNO = GLU ? C::BN / 2 : C::BN;    // output columns of a tile
+  constexpr int HN = C::TN / 2;                   // GLU: a wave's columns of each product
+  constexpr int L = C::QA + C::QB;                // loads of a stage, per wave
+  __shared__ __attribute__((aligned(1024))) char lds[kStages * C::SS];
+  __shared__ __attribute__((aligned(16))) char sbuf[BF16 ? C::NW * kStoreBytes : 16];
+  __shared__ __attribute__((aligned(16))) int prow[4][C::BM];  // pair of every row, by tile
+  __shared__ __attribute__((aligned(16))) int xrow[2][C::BM];  // its row of X
   const int nc = (g.n + BNO - 1) / BNO;
   const int ntiles = ld_table(g.mt_off, g.E) * nc;
   const int x = blockIdx.x & 7, nb = gridDim.x >> 3;
@@ -247,132 +451,138 @@ __global__ __launch_bounds__(C::NT, 2) void k_fwd_tile(FwdGemmArgs g) {
   if (t >= tend) return;
   const int w = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6)), l = lane_id();
   const int wm = w / C::WGN, wn = w % C::WGN;
-  const int nk = (g.K + KT - 1) / KT;
+  // k-tiles of a tile, zeros past K: an even number, and at least six, so that
+  // the feed is never more than one tile ahead and the rows of the next tile,
+  // asked for when the feed enters this one, are there when it leaves it
+  const int nk = max(((g.K + KT - 1) / KT + 1) & ~1, 6);
   const int64_t kb = (int64_t)g.K * ES;  // bytes of a weight row
 
-  // this lane's granule of the 1 KB blocks that its wave loads
-  const int lr = l >> 3;  // row inside a block
-  int agran[C::QA], bgran[C::QB], boff[C::QB];
-#pragma unroll
-  for (int q = 0; q < C::QA; ++q)
-    agran[q] = ((l & 7) ^ lds_swz((w * C::QA + q) * 8 + lr)) * 16;
+  // this lane's place in the 1 KB blocks (16 rows) that its wave loads
+  const int lr = l >> 2, gran = ((l & 3) ^ swz64(lr)) * 16;
+  int boff[C::QB];
 #pragma unroll
   for (int q = 0; q < C::QB; ++q) {
-    const int r = (w * C::QB + q) * 8 + lr;
-    bgran[q] = ((l & 7) ^ lds_swz(r)) * 16;
-    const int in = r % C::TN;
+    const int r = (w * C::QB + q) * 16 + lr, in = r % C::TN;
     const int col = GLU ? (r / C::TN) * HN + in % HN : r;
-    boff[q] = (int)(col * kb) + bgran[q];
+    boff[q] = (int)(col * kb) + gran;
   }
-  // fragment offsets: row bits 4 and 5 flip granule bits 0 and 2
-  const int fa = wm * C::TM + (l & 15), fb = wn * C::TN + (l & 15);
-  int ao[4], bo[4];
-#pragma unroll
-  for (int v = 0; v < 4; ++v) {
-    const int flip = (v & 1) | (v & 2) << 1;
-    ao[v] = fa * 128 + ((((l >> 4) ^ lds_swz(fa)) ^ flip) << 4);
-    bo[v] = fb * 128 + ((((l >> 4) ^ lds_swz(fb)) ^ flip) << 4);
-  }
+  // and in the fragments that it multiplies
+  const int fr = l & 15, fo = fr * 64 + (((l >> 4) ^ swz64(fr)) << 4);
+  const int ao = wm * C::TM * 64 + fo, bo = wn * C::TN * 64 + fo;
 
-  FwdJob cur = fwd_job(g, t, nc, find_expert(g.mt_off, g.E, t / nc), C::BM, BNO), nxt = cur;
-  bool more = false;
-  int aoff[C::QA], noff[C::QA], np[C::QA], npr = 0;
-  // rows of a tile, in two dependent steps
-  auto rows1 = [&](const FwdJob& j) {
+  int vm = 0;  // memory instructions of this wave so far
+  FwdFeed<C> f;
+  FwdJob next, cur;   // the tile after the feed's; the one being multiplied
+  bool more = true;   // `next` is a tile
+  int entered = -1;   // tiles that the feed has entered, less one
+  auto look = [&]() {  // the rows of `next`, straight into LDS
+    if (w * 64 < C::BM) {
+      const int at = next.m0 + w * 64, slot = entered + 1;
+      dma4(uniform(make_dma_rsrc((const char*)(g.kept + at), (int64_t)(g.N - at) * 4)),
+           &prow[slot & 3][w * 64], l * 4);
+      dma4(uniform(make_dma_rsrc((const char*)(g.rows + at), (int64_t)(g.N - at) * 4)),
+           &xrow[slot & 1][w * 64], l * 4);
+      vm += 2;
+    }
+  };
+  auto enter = [&]() {  // the feed moves on to `next`
+    ++entered;
+    f.job = next;
+    f.k = 0;
+    const char* xa = (const char*)g.X + (g.gather ? 0 : (int64_t)next.m0 * g.ldx * ES);
+    f.a = uniform(make_dma_rsrc(xa, g.gather ? g.x_bytes
+                                             : ((int64_t)(next.rows - 1) * g.ldx + g.K) * ES));
+    const int64_t wat = (int64_t)next.e * g.w_stride * ES + next.n0 * kb;
+    const int64_t wleft = min<int64_t>((g.n - next.n0) * kb, kOobOff);
+    f.w0 = uniform(make_dma_rsrc((const char*)g.W0 + wat, wleft));
+    if constexpr (GLU) f.w1 = uniform(make_dma_rsrc((const char*)g.W1 + wat, wleft));
 #pragma unroll
     for (int q = 0; q < C::QA; ++q) {
-      const int r = (w * C::QA + q) * 8 + lr;
-      np[q] = g.gather && r < j.rows ? g.kept[j.m0 + r] : 0;
+      const int r = (w * C::QA + q) * 16 + lr;
+      const int row = g.gather ? xrow[entered & 1][r] : r;
+      f.off[q] = r < next.rows ? row * (int)(g.ldx * ES) + gran : kOobOff;
     }
-    if ((int)threadIdx.x < C::BM) npr = (int)threadIdx.x < j.rows ? g.kept[j.m0 + threadIdx.x] : 0;
-  };
-  auto rows2 = [&](const FwdJob& j, int par) {
-#pragma unroll
-    for (int q = 0; q < C::QA; ++q) {
-      const int r = (w * C::QA + q) * 8 + lr;
-      const int64_t row = g.gather ? (g.x_pair ? np[q] : g.token[np[q]]) : r;
-      noff[q] = r < j.rows ? (int)(row * g.ldx * ES) + agran[q] : kOobOff;
+    t += nb;
+    more = t < tend;
+    if (more) {
+      next = fwd_job(g, t, nc, next.e, C::BM, BNO);
+      look();
     }
-    if ((int)threadIdx.x < C::BM) prow[par][threadIdx.x] = npr;
   };
-  // stage s <- k-tile k of tile j with row offsets off
-  auto issue = [&](const FwdJob& j, const int (&off)[C::QA], int k, int s) {
-    const int kbyte = k * 128;
-    const char* abase = (const char*)g.X + (g.gather ? 0 : (int64_t)j.m0 * g.ldx * ES) + kbyte;
-    const int64_t abytes = g.gather ? g.x_bytes : ((int64_t)(j.rows - 1) * g.ldx + g.K) * ES;
-    const int64_t wat = (int64_t)j.e * g.w_stride * ES + j.n0 * kb + kbyte;
-    const int64_t wbytes = min<int64_t>((g.n - j.n0) * kb - kbyte, kOobOff);
-    const dma_rsrc ra = uniform(make_dma_rsrc(abase, abytes - kbyte));
-    const dma_rsrc r0 = uniform(make_dma_rsrc((const char*)g.W0 + wat, wbytes));
-    dma_rsrc r1 = r0;
-    if constexpr (GLU) r1 = uniform(make_dma_rsrc((const char*)g.W1 + wat, wbytes));
+  bool fed = false;  // the feed is past the last tile
+  auto feed = [&](int s) {  // stage s <- the feed's k-tile
+    if (fed) return;
     char* base = lds + s * C::SS;
-    const bool tail = kbyte + 128 > kb;
+    const int at = f.k * 64, left = (int)kb - at;  // bytes of a row before and from this k-tile
+    auto load = [&](auto tail) {
+      const bool out = tail && gran >= left;  // past K
 #pragma unroll
-    for (int q = 0; q < C::QA; ++q)
-      dma16(ra, reinterpret_cast<uint16_t*>(base + (w * C::QA + q) * 1024),
-            tail && kbyte + agran[q] >= kb ? kOobOff : off[q]);
+      for (int q = 0; q < C::QA; ++q)
+        dma16(f.a, reinterpret_cast<uint16_t*>(base + (w * C::QA + q) * 1024),
+              out ? kOobOff : f.off[q], at);
 #pragma unroll
-    for (int q = 0; q < C::QB; ++q) {
-      const bool up = GLU && (w * C::QB + q) * 8 % C::TN >= HN;
-      dma16(up ? r1 : r0, reinterpret_cast<uint16_t*>(base + C::SA + (w * C::QB + q) * 1024),
-            tail && kbyte + bgran[q] >= kb ? kOobOff : boff[q]);
+      for (int q = 0; q < C::QB; ++q) {
+        const bool up = GLU && (w * C::QB + q) * 16 % C::TN >= HN;
+        dma16(up ? f.w1 : f.w0, reinterpret_cast<uint16_t*>(base + C::SA + (w * C::QB + q) * 1024),
+              out ? kOobOff : boff[q], at);
+      }
+    };
+    if (left >= 64)
+      load(std::false_type());
+    else
+      load(std::true_type());
+    vm += L;
+    if (++f.k == nk) {
+      fed = !more;
+      if (more) enter();
     }
   };
 
-  rows1(cur);
-  rows2(cur, 0);
+  next = fwd_job(g, t, nc, find_expert(g.mt_off, g.E, t / nc), C::BM, BNO);
+  look();
+  stage_barrier<L>(0);
+  cur = next;
+  enter();
+  // mk[s]: vm just after the loads of the s-th oldest k-tile in flight
+  int mk[kStages];
 #pragma unroll
-  for (int q = 0; q < C::QA; ++q) aoff[q] = noff[q];
-  issue(cur, aoff, 0, 0);
-  int st = 0, par = 0;
-  for (;;) {
+  for (int s = 0; s < kStages; ++s) {
+    feed(s);
+    mk[s] = vm;
+  }
+  stage_barrier<L>(vm - mk[0]);
+  Frags<C> f0, f1;
+  f0.read(lds, ao, bo);
+  int st = 0;
+  for (int done = 0;; ++done) {
     f32x4 acc[C::FM][C::FN];
 #pragma unroll
     for (int i = 0; i < C::FM; ++i)
 #pragma unroll
       for (int j = 0; j < C::FN; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
-    for (int k = 0; k < nk; ++k) {
-      stage_barrier();
-      if (k == 0) {
-        t += nb;
-        more = t < tend;
-        if (more) {
-          nxt = fwd_job(g, t, nc, cur.e, C::BM, BNO);
-          rows1(nxt);
-        }
-      }
-      if (k == (nk > 1 ? 1 : 0) && more) rows2(nxt, par ^ 1);
-      if (k + 1 < nk)
-        issue(cur, aoff, k + 1, st ^ 1);
-      else if (more)
-        issue(nxt, noff, 0, st ^ 1);
-      const char* As = lds + st * C::SS;
-      const char* Bs = As + C::SA;
+    // A wave enters with the k-tile's fragments read (or on their way).  Past
+    // the barrier every wave has them, so the stage takes the k-tile four on,
+    // and the next k-tile's loads have arrived.
+    auto step = [&](const Frags<C>& now, Frags<C>& then) {
+      stage_barrier<L>(vm - mk[1]);
+      const int free = st;
+      st = (st + 1) & (kStages - 1);
+      then.read(lds + st * C::SS, ao, bo);
+      now.template multiply<BF16, 0, C::FM / 2>(acc);
+      interleave<C, BF16>();
+      feed(free);
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        u32x4 af[C::FM], bf[C::FN];
-#pragma unroll
-        for (int j = 0; j < C::FN; ++j)
-          bf[j] = *reinterpret_cast<const u32x4*>(Bs + bo[(j & 1) | ((((j >> 1) & 1) ^ h) << 1)] + j * 2048);
-#pragma unroll
-        for (int i = 0; i < C::FM; ++i)
-          af[i] = *reinterpret_cast<const u32x4*>(As + ao[(i & 1) | ((((i >> 1) & 1) ^ h) << 1)] + i * 2048);
-#pragma unroll
-        for (int i = 0; i < C::FM; ++i)
-#pragma unroll
-          for (int j = 0; j < C::FN; ++j) acc[i][j] = mma<BF16>(bf[j], af[i], acc[i][j]);
-      }
-      st ^= 1;
+      for (int s = 0; s < kStages - 1; ++s) mk[s] = mk[s + 1];
+      mk[kStages - 1] = vm;
+      now.template multiply<BF16, C::FM / 2, C::FM>(acc);
+    };
+    for (int k = 0; k < nk; k += 2) {
+      step(f0, f1);
+      step(f1, f0);
     }
-    // lane l of fragment (i, j): row 16 i + (l & 15), columns 16 j + 4 (l >> 4)
-    // .. + 3 of the wave's sub-tile
-    fwd_store<C, BF16, GLU>(g, cur, acc, lds + (st ^ 1) * C::SS, prow[par], w, l);
-    if (!more) break;
-    cur = nxt;
-    par ^= 1;
-#pragma unroll
-    for (int q = 0; q < C::QA; ++q) aoff[q] = noff[q];
+    vm += fwd_store<C, BF16, GLU, EPI>(g, cur, acc, sbuf + (BF16 ? w * kStoreBytes : 0), prow[done & 3], w, l);
+    if (done == entered) break;
+    cur = f.job;
   }
 }
 
@@ -381,8 +591,7 @@ __global__ __launch_bounds__(C::NT, 2) void k_fwd_tile(FwdGemmArgs g) {
 __global__ __launch_bounds__(256) void k_fwd_pack(FwdGemmArgs g, char* out) {
   const int m = blockIdx.x * 4 + (threadIdx.x >> 6);
   if (m >= g.offsets[g.E]) return;
-  const int p = g.kept[m];
-  const int64_t es = g.bf16 ? 2 : 4, row = g.x_pair ? p : g.token[p];
+  const int64_t es = g.bf16 ? 2 : 4, row = g.rows[m];
   const u32x4* src = reinterpret_cast<const u32x4*>((const char*)g.X + row * g.ldx * es);
   u32x4* dst = reinterpret_cast<u32x4*>(out + (int64_t)m * g.K * es);
   for (int c = lane_id(); c < g.K * es / 16; c += kWave) dst[c] = src[c];
@@ -451,26 +660,32 @@ __global__ __launch_bounds__(256) void k_fwd_join(FwdJoinArgs a) {
 
 namespace {
 
-typedef FwdCfg<256, 256, 2, 4> FwdL;
-typedef FwdCfg<128, 128, 2, 2> FwdM;
-typedef FwdCfg<64, 128, 1, 4> FwdS;
+// Rows x columns, and waves: a GLU wave holds half as many output columns, so
+// its sub-tile is wider (64 output columns a wave, 128 bytes a row, for L).
+template <bool GLU> using FwdL = FwdCfg<256, 256, GLU ? 4 : 2, GLU ? 2 : 4>;
+template <bool GLU> using FwdM = FwdCfg<128, 128, 2, 2>;
+template <bool GLU> using FwdS = FwdCfg<64, 128, GLU ? 2 : 1, GLU ? 2 : 4>;
 
-template <class C, bool BF16, bool GLU>
+template <class C, bool BF16, bool GLU, bool EPI>
 hipError_t launch_tiles(const FwdGemmArgs& g, hipStream_t s) {
   constexpr int bno = GLU ? C::BN / 2 : C::BN;
   const int64_t tiles = ((int64_t)g.N / C::BM + g.E) * ((g.n + bno - 1) / bno);
   if (tiles > 0x7fffffffll) return hipErrorInvalidValue;
-  const int cap = grid_cap_of<k_fwd_tile<C, BF16, GLU>, C::NT>() & ~7;
+  const int cap = grid_cap_of<k_fwd_tile<C, BF16, GLU, EPI>, C::NT>() & ~7;
   const int64_t want = (tiles + 7) & ~7ll;
   const int grid = (int)(want < cap ? want : cap < 8 ? 8 : cap);
-  LRM_LAUNCH(grid, C::NT, 0, s, k_fwd_tile<C, BF16, GLU>)(g);
+  LRM_LAUNCH(grid, C::NT, 0, s, k_fwd_tile<C, BF16, GLU, EPI>)(g);
   return hipGetLastError();
 }
 
-template <class C>
+template <template <bool> class C>
 hipError_t launch_cfg(const FwdGemmArgs& g, hipStream_t s) {
-  if (g.bf16) return g.glu ? launch_tiles<C, true, true>(g, s) : launch_tiles<C, true, false>(g, s);
-  return g.glu ? launch_tiles<C, false, true>(g, s) : launch_tiles<C, false, false>(g, s);
+  if (g.glu)
+    return g.bf16 ? launch_tiles<C<true>, true, true, false>(g, s)
+                  : launch_tiles<C<true>, false, true, false>(g, s);
+  if (!g.bf16) return launch_tiles<C<false>, false, false, true>(g, s);
+  return g.bias || g.Z || g.act != kActNone ? launch_tiles<C<false>, true, false, true>(g, s)
+                                            : launch_tiles<C<false>, true, false, false>(g, s);
 }
 
 }  // namespace

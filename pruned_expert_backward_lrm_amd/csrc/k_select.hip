@@ -273,7 +273,8 @@ __global__ __launch_bounds__(64) void k_bucket_scatter(int N, int T, int E, int 
                                                        const float* __restrict__ score,
                                                        int32_t* __restrict__ cand,
                                                        uint32_t* __restrict__ keys,
-                                                       int32_t* __restrict__ pos, int keep_all) {
+                                                       int32_t* __restrict__ pos, int keep_all,
+                                                       int32_t* __restrict__ tokens) {
   LRM_DYN_SHARED(int, run);  // [E]
   const int l = lane_id();
   const int64_t p0 = (int64_t)blockIdx.x * chunk;
@@ -323,6 +324,7 @@ __global__ __launch_bounds__(64) void k_bucket_scatter(int N, int T, int E, int 
         cand[dst] = (int32_t)p;
         if (keys) keys[dst] = __float_as_uint(sv[u]);
         if (keep_all) pos[p] = dst;
+        if (tokens) tokens[dst] = tv[u];
         if (rank == 0) run[e] += __popcll(m);
       } else if (in) {
         pos[p] = -1;
@@ -758,7 +760,8 @@ hipError_t launch_bucket(const BucketArgs& a, hipStream_t s) {
   if (a.N > 0) {
     LRM_LAUNCH(nblk, 64, a.E * sizeof(int), s, k_bucket_scatter)(a.N, a.T, a.E, chunk, a.token,
                                                          a.expert, a.blkcnt, a.cand_off, a.score,
-                                                         a.cand, a.keys, a.pos, a.keep_all);
+                                                         a.cand, a.keys, a.pos, a.keep_all,
+                                                         a.tokens);
   }
   return hipGetLastError();
 }

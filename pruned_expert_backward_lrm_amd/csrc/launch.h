@@ -59,6 +59,7 @@ struct BucketArgs {
   int32_t* cand;         // [N]
   uint32_t* keys;        // [N] or nullptr
   int32_t* pos;          // [N]
+  int32_t* tokens;       // [N] token of every candidate (keep_all), or nullptr
   int keep_all;          // pos written here (every valid pair kept, cand = kept)
   uint32_t* err;         // one word: the error bits of this call
   uint32_t* blkerr;      // [bucket_blocks(N)] per-block error bits (scratch)
@@ -286,25 +287,26 @@ hipError_t launch_pair_grad(const PairGradArgs& a, hipStream_t s);
 // ------------------------------------------------------- experts forward
 // One grouped product of the forward pass over the packed rows of all experts
 // (offsets [E+1], kept [N], mt_off [E+1] the prefix of row tiles of
-// fwd_tile_rows rows).  The A operand's row of packed row m is row m of X
-// (gather 0), or the row of pair kept[m]: itself (x_pair) or its token's.
+// fwd_tile_rows rows).  The A operand's row of packed row m is row m of X, or
+// with gather row rows[m] of it.
 //   glu: u = W0_e x, v = W1_e x: A[p] = u, B[p] = v (either may be null),
-//        H[m] = silu(u) v
+//        H[m] = silu(u) v, for p = kept[m]
 //   else: z = W0_e x + bias_e: Z[p] = z, Y[p] = act(z) (either may be null);
 //        Ylo[p]: the 8 bits below bf16 of Y (bf16; null: not wanted)
 // All outputs have n dense columns.
 struct FwdGemmArgs {
-  int N, E, bf16, K, n, glu, act, gather, x_pair;
+  int N, E, bf16, K, n, glu, act, gather;
   const int32_t* offsets;
   const int32_t* kept;
+  const int32_t* rows;
   const int32_t* mt_off;
-  const int32_t* token;
   const void* X; int64_t ldx;
   int64_t x_bytes;  // gather: from the first row of X to the end of the last one
   const void* W0; const void* W1; int64_t w_stride;  // [E][n][K]
   const void* bias;  // [E][n] or null
   void* A; void* B; void* H;
   void* Z; void* Y; int8_t* Ylo;
+  void* dump;  // 1 KB of scratch that lanes outside a tile store to
 };
 // The most x_bytes a gathering product takes (32-bit byte offsets, below the
 // one that stands for "outside"); larger inputs are packed first.  (The

@@ -362,6 +362,8 @@ inline V4 ds_read_tr16(const V4* p) {
 // the hardware exp2 and reciprocal, modelled correctly rounded
 #define __builtin_amdgcn_exp2f(x) ::exp2f(x)
 #define __builtin_amdgcn_rcpf(x) (1.0f / (x))
+// (instruction order is the compiler's business)
+#define __builtin_amdgcn_sched_group_barrier(mask, n, id) ((void)0)
 // memory operations complete at once here: waits have nothing to wait for
 #define __builtin_amdgcn_s_waitcnt(imm) ((void)(imm))
 #define __builtin_amdgcn_s_barrier() ::emu::syncthreads()
