@@ -316,6 +316,7 @@ struct FwdGemmArgs {
 #endif
 constexpr int64_t kFwdGatherMax = LRM_FWD_GATHER_MAX;
 int fwd_tile_rows(const FwdGemmArgs& g);
+int fwd_tile_forced();  // the row tile that LRM_FWD_TILE asks for, or 0
 // out[m] = the A operand's row of packed row m, K dense columns
 hipError_t launch_fwd_pack(const FwdGemmArgs& g, void* out, hipStream_t s);
 hipError_t launch_fwd_gemm(const FwdGemmArgs& g, hipStream_t s);
@@ -333,5 +334,34 @@ struct FwdJoinArgs {
   void* out;
 };
 hipError_t launch_fwd_join(const FwdJoinArgs& a, hipStream_t s);
+
+// The forward products of few pairs (N <= kFewPairs, T <= 65535), from the
+// pairs themselves.  The A operand's row of pair p is row p of X (x_pair) or
+// its token's; outputs are rows of p.
+//   launch_fwd_few: A, B, H (glu) or Z, Y, Yf (fp32) of every present pair;
+//     err (or null): the pairs' index error bits
+//   launch_fwd_few_join: y_p = W0 X[p], Y (or null), out[t] = R[t] + sum of w_p y_p
+//   launch_fwd_few_sum: out[t] = R[t] + sum of w_p Yf[p]
+struct FwdFewArgs {
+  int N, T, E, bf16, K, n, glu, act, x_pair;
+  int by_pair;  // a block's expert is that of its pair (N at most E)
+  const int32_t* token;
+  const int32_t* expert;
+  const float* weight;
+  const void* X; int64_t ldx;
+  const void* W0; const void* W1; int64_t w_stride;
+  const void* bias;
+  void* A; void* B; void* H;
+  void* Z; void* Y; float* Yf;
+  const void* R; int64_t ldr;
+  void* out;
+  uint32_t* err;
+};
+constexpr int kFewPairs = 64;  // a lane each
+constexpr int64_t kFewBlocks = 2048;
+hipError_t launch_fwd_few(const FwdFewArgs& g, hipStream_t s);
+hipError_t launch_fwd_few_sumsq(const FwdFewArgs& g, double* out, hipStream_t s);
+hipError_t launch_fwd_few_join(const FwdFewArgs& g, hipStream_t s);
+hipError_t launch_fwd_few_sum(const FwdFewArgs& g, hipStream_t s);
 
 }  // namespace lrm
