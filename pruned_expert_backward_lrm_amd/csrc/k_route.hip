@@ -7,8 +7,12 @@
 // per wave), each holding the NV experts i*NV .. i*NV + NV - 1 of its lane i:
 // lower lanes hold lower experts, so a tie between lanes goes to the lowest.
 // Keys are kept as unsigned integers that order like the floats (0: not
-// eligible); a round of the choice takes the maximum over the lanes with DPP
-// row rotations, then the minimum expert among the lanes that hold it.
+// eligible).  Up to 512 experts (8 a lane) a key carries its expert's
+// complement below it (16 bits of each for bf16 logits, 32 otherwise), so that
+// one maximum over the lanes decides key and tie; every lane sorts its 8 once
+// and a round only compares the lanes' heads (65536 tokens, 128 experts, top-8:
+// R_SORT us instead of 26 with a search of all 8 every round).  Larger rows and
+// fp64 keys take the maximum key, then the minimum expert among its holders.
 //
 // Order of the choice: without a bias the scores order like the logits, which
 // are exact.  With a bias, and for sums of two scores, the keys are first
@@ -80,6 +84,40 @@ __device__ __forceinline__ double ror(double v) {
   return __builtin_bit_cast(double, ror64<ROT>(__builtin_bit_cast(uint64_t, v)));
 }
 
+// The value in the other 16-lane row of a pair of rows, and in the other half
+// of the wave, beside the own one: (even row's, odd row's) and (low, high
+// half's), the same in both, so that a commutative op gives both the same bits.
+#ifdef LRM_CPU_EMU
+template <int DIST>
+__device__ __forceinline__ void both_of(uint32_t v, uint32_t& x, uint32_t& y) {
+  const uint32_t o = (uint32_t)__shfl_xor((int)v, DIST, kWave);
+  x = lane_id() & DIST ? o : v;
+  y = lane_id() & DIST ? v : o;
+}
+#else
+template <int DIST>
+__device__ __forceinline__ void both_of(uint32_t v, uint32_t& x, uint32_t& y) {
+  const auto r = DIST == 16 ? __builtin_amdgcn_permlane16_swap(v, v, false, false)
+                            : __builtin_amdgcn_permlane32_swap(v, v, false, false);
+  x = r[0];
+  y = r[1];
+}
+#endif
+template <int DIST, typename V, typename Op>
+__device__ __forceinline__ V across(V v, Op op) {
+  if constexpr (sizeof(V) == 4) {
+    uint32_t x, y;
+    both_of<DIST>(__builtin_bit_cast(uint32_t, v), x, y);
+    return op(__builtin_bit_cast(V, x), __builtin_bit_cast(V, y));
+  } else {
+    const uint64_t u = __builtin_bit_cast(uint64_t, v);
+    uint32_t xl, yl, xh, yh;
+    both_of<DIST>((uint32_t)u, xl, yl);
+    both_of<DIST>((uint32_t)(u >> 32), xh, yh);
+    return op(__builtin_bit_cast(V, (uint64_t)xh << 32 | xl), __builtin_bit_cast(V, (uint64_t)yh << 32 | yl));
+  }
+}
+
 // All lanes of the LPT-lane group get op over the group (op commutative; the
 // pairs of every step are the same two values in both lanes, so all lanes
 // hold the same bits).
@@ -89,8 +127,8 @@ __device__ __forceinline__ V group_all(V v, Op op) {
   v = op(v, ror<4>(v));
   v = op(v, ror<2>(v));
   v = op(v, ror<1>(v));
-  if constexpr (LPT >= 32) v = op(v, __shfl_xor(v, 16, kWave));
-  if constexpr (LPT >= 64) v = op(v, __shfl_xor(v, 32, kWave));
+  if constexpr (LPT >= 32) v = across<16>(v, op);
+  if constexpr (LPT >= 64) v = across<32>(v, op);
   return v;
 }
 struct OpMax {
@@ -143,12 +181,57 @@ __device__ __forceinline__ void load_row(const void* row, int bf16, bool vec, in
   }
 }
 
+// The same in two steps for 8 values, so that a row is on its way while the one
+// before it is worked on: fetched where the whole 8 lie inside an aligned row.
+struct RawRow {
+  u32x4 q[2];
+  __device__ __forceinline__ void fetch(const void* row, int bf16, bool vec, int c0, int E) {
+    if (!vec || c0 + 8 > E) return;
+    const u32x4* src = reinterpret_cast<const u32x4*>((const char*)row + (int64_t)c0 * (bf16 ? 2 : 4));
+    q[0] = src[0];
+    if (!bf16) q[1] = src[1];
+  }
+  __device__ __forceinline__ void values(const void* row, int bf16, bool vec, int c0, int E,
+                                         float (&z)[8]) const {
+    if (!vec || c0 + 8 > E) {
+      load_row<8>(row, bf16, false, c0, E, z);
+    } else if (bf16) {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        z[2 * j] = bf16_lo(q[0][j]);
+        z[2 * j + 1] = bf16_hi(q[0][j]);
+      }
+    } else {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        z[j] = __uint_as_float(q[0][j]);
+        z[4 + j] = __uint_as_float(q[1][j]);
+      }
+    }
+  }
+};
+
 __device__ __forceinline__ float load_one(const void* row, int bf16, int c) {
   return bf16 ? bf16_to_f32(((const uint16_t*)row)[c]) : ((const float*)row)[c];
 }
 
-__device__ __forceinline__ float exp_of(float x) { return expf(x); }
+// e^x in fp32 to about 2 units in the last place, from the hardware's exp2: the
+// rounding error of x log2(e) is put back.  x is held to [-150, 88], so that a
+// masked logit (-inf) gives 0 and no result is infinite.
+__device__ __forceinline__ float exp_of(float x) {
+  x = fminf(fmaxf(x, -150.f), 88.f);
+  const float t = x * 1.44269502f;  // log2(e) = 1.44269502 + 1.92596299e-8
+  const float r = fmaf(x, 1.92596299e-8f, fmaf(x, 1.44269502f, -t));
+  const float e = __builtin_amdgcn_exp2f(t);
+  return fmaf(e, r * 0.693147181f, e);
+}
 __device__ __forceinline__ double exp_of(double x) { return exp(x); }
+// 1 / x for x in [1, 2^127)
+__device__ __forceinline__ float inv_of(float x) {
+  const float r = __builtin_amdgcn_rcpf(x);
+  return fmaf(r, fmaf(-x, r, 1.f), r);
+}
+__device__ __forceinline__ double inv_of(double x) { return 1.0 / x; }
 
 // A bit per expert of the lane that takes part (NV <= 64).  Bits and selects,
 // not branches around single values: hipcc 7.2 drops the assignment of a
@@ -202,6 +285,146 @@ __device__ __forceinline__ bool choose(typename KeyOf<F>::type (&key)[NV], int i
     prev = top;
   }
   return close;
+}
+
+// Eight keys of a lane in descending order (Batcher's network).
+template <typename P>
+__device__ __forceinline__ void sort8(P (&s)[8]) {
+  auto ce = [&](int x, int y) {
+    const P lo = s[x] < s[y] ? s[x] : s[y];
+    s[x] = s[x] < s[y] ? s[y] : s[x];
+    s[y] = lo;
+  };
+  ce(0, 1); ce(2, 3); ce(4, 5); ce(6, 7);
+  ce(0, 2); ce(1, 3); ce(4, 6); ce(5, 7);
+  ce(1, 2); ce(5, 6);
+  ce(0, 4); ce(1, 5); ce(2, 6); ce(3, 7);
+  ce(2, 4); ce(3, 5);
+  ce(1, 2); ce(3, 4); ce(5, 6);
+}
+
+// k rounds of choice over packed keys (key above the expert's complement, all
+// different, 0: none): lane j of the group ends with the j-th in *got.  check
+// as in choose; key(p, q): whether the keys of p and the next one, q, are too
+// close to tell.
+template <int LPT, typename P, typename CLOSE>
+__device__ __forceinline__ bool choose_packed(P (&s)[8], int i, int k, bool check, P* got, CLOSE key) {
+  bool close = false;
+  P prev = 0;
+  *got = 0;
+  sort8(s);
+  const int rounds = check ? k + 1 : k;
+  if (rounds <= 9) {
+    // unrolled: after round r only 8 - r keys of a lane can still be asked for
+#pragma unroll
+    for (int r = 0; r < 9; ++r) {
+      if (r < rounds) {
+        const P top = group_all<LPT>(s[0], OpMax());
+        if (check && r > 0 && top != 0) close |= key(prev, top);
+        *got = i == r ? top : *got;
+        const bool mine = s[0] == top;
+#pragma unroll
+        for (int j = 0; j < 7; ++j)
+          if (j < 8 - r) s[j] = mine ? s[j + 1] : s[j];
+        if (r == 0) s[7] = mine ? 0 : s[7];
+        prev = top;
+      }
+    }
+    if (i >= k) *got = 0;
+    return close;
+  }
+  for (int r = 0; r < rounds; ++r) {
+    const P top = group_all<LPT>(s[0], OpMax());
+    if (check && r > 0 && top != 0) close |= key(prev, top);
+    if (i == r && r < k) *got = top;
+    const bool mine = s[0] == top;
+#pragma unroll
+    for (int j = 0; j < 7; ++j) s[j] = mine ? s[j + 1] : s[j];
+    s[7] = mine ? 0 : s[7];
+    prev = top;
+  }
+  return close;
+}
+
+// fp32 keys (scores, or scores plus bias) as fixed-point numbers above the
+// complement of an index below 512, in 32 bits: 23 bits from the least to the
+// largest that a key, or half a key or half a sum of two, can be for scores in
+// [0, 1] and the biases at hand.  What the fixed point or fp32 cannot tell apart
+// is chosen again in fp64.
+struct Fixed {
+  float base, scale;
+  uint32_t tol;
+  // least and largest bias
+  __device__ __forceinline__ Fixed(float lo, float hi) {
+    base = fminf(lo, 0.5f * lo);
+    scale = 8388000.f / (1.f + (fmaxf(hi, 0.5f * hi) - base));
+    // error of a key: see kKeyTol; two for the two roundings down
+    const float big = fmaxf(fabsf(lo), fabsf(hi)) + 1.f;
+    const float t = kKeyTol * (1.f + 0.125f * big) * scale + 2.f;
+    tol = t < 8388607.f ? (uint32_t)t : 8388607u;  // (a NaN or infinite bias: all too close)
+  }
+  __device__ __forceinline__ uint32_t pack(float c, int i) const {
+    const float q = fminf(fmaxf((c - base) * scale, 0.f), 8388600.f);
+    return ((uint32_t)q + 1u) << 9 | (511u - (uint32_t)i);
+  }
+  __device__ __forceinline__ bool near(uint32_t p, uint32_t q) const { return (p >> 9) - (q >> 9) <= tol; }
+  __device__ __forceinline__ static int index(uint32_t p) { return (int)(511u - (p & 511u)); }
+};
+
+// Value of v in the lane of the other half of 2 DIST lanes (DIST 1, 2, 4, 8), as
+// far as the lanes of a half hold the same value.
+template <int DIST>
+__device__ __forceinline__ float other_half(float v) {
+  constexpr int ctrl = DIST == 1 ? 0xB1 : DIST == 2 ? 0x4E : DIST == 4 ? 0x141 : 0x140;
+  return __uint_as_float(
+      (uint32_t)__builtin_amdgcn_update_dpp(0, (int)__float_as_uint(v), ctrl, 0xf, 0xf, false));
+}
+
+// keep_groups for groups of whole lanes, GL = 1, 2, 4, 8 or 16 of them (8
+// experts a lane), without LDS: the two best of a lane, then of the group's
+// lanes, then rounds of choice over the groups.
+template <int LPT>
+__device__ __forceinline__ uint64_t keep_groups8(const RouteArgs& a, const float (&val)[8], int i, int GL,
+                                                 const Fixed& fx, bool check, bool* close) {
+  const float inf = __builtin_inff();
+  float one = -inf, two = -inf;
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    two = fmaxf(two, fminf(one, val[j]));
+    one = fmaxf(one, val[j]);
+  }
+  auto merge = [&](float o1, float o2) {
+    two = fmaxf(fmaxf(two, o2), fminf(one, o1));
+    one = fmaxf(one, o1);
+  };
+  if (GL > 1) merge(other_half<1>(one), other_half<1>(two));
+  if (GL > 2) merge(other_half<2>(one), other_half<2>(two));
+  if (GL > 4) merge(other_half<4>(one), other_half<4>(two));
+  if (GL > 8) merge(other_half<8>(one), other_half<8>(two));
+  const int g = i / GL;
+  const bool rep = i % GL == 0 && g < a.n_group && one > -inf;
+  const float sc = a.group_top2 && two > -inf ? one + two : one;
+  uint64_t kept = 0;
+  const int rounds = check ? a.topk_group + 1 : a.topk_group;
+  if (check) {
+    // (half of a sum, or of the only key; the range reaches down to half keys)
+    uint32_t key = rep ? fx.pack(a.group_top2 ? 0.5f * sc : sc, g) : 0u, prev = 0;
+    for (int r = 0; r < rounds; ++r) {
+      const uint32_t top = group_all<LPT>(key, OpMax());
+      if (r > 0 && top != 0 && fx.near(prev, top)) *close = true;
+      if (r < a.topk_group && top != 0) kept |= 1ull << (Fixed::index(top) & 63);
+      key = key == top ? 0u : key;
+      prev = top;
+    }
+    return kept;
+  }
+  uint64_t key = rep ? (uint64_t)ord_of(sc) << 32 | (0xffffffffu - (uint32_t)g) : 0ull;
+  for (int r = 0; r < rounds; ++r) {
+    const uint64_t top = group_all<LPT>(key, OpMax());
+    if (top != 0) kept |= 1ull << ((0xffffffffu - (uint32_t)top) & 63u);
+    if (key == top) key = 0;
+  }
+  return kept;
 }
 
 // The groups that stay: a bit per group, from the values val (F; -inf where
@@ -287,33 +510,50 @@ __device__ __forceinline__ void scores(const RouteArgs& a, const float (&z)[NV],
     for (int j = 0; j < NV; ++j) s[j] *= inv;
   } else {
 #pragma unroll
-    for (int j = 0; j < NV; ++j) s[j] = (F)1 / ((F)1 + exp_of(-(F)z[j]));
+    for (int j = 0; j < NV; ++j) s[j] = inv_of((F)1 + exp_of(-(F)z[j]));
   }
 }
 
-// The choice of one token with keys in F.  exact: the keys' order is certain.
-template <int LPT, int NV, typename F>
-__device__ __forceinline__ bool choose_token(const RouteArgs& a, const float (&z)[NV], float top, int i,
-                                             F* row, int* got) {
+// The choice of one token with keys in F; true: fp32 keys leave it uncertain.
+// SCORED: with a bias or sums of two scores (else the logits are the keys).
+template <int LPT, int NV, typename F, bool SCORED>
+__device__ __forceinline__ bool choose_token(const RouteArgs& a, const float (&z)[NV],
+                                             const float (&bias)[NV], const Fixed& fx, float top,
+                                             int i, F* row, int* got, float* zgot) {
   typedef typename KeyOf<F>::type K;
   const F inf = (F)__builtin_inff();
-  const bool by_score = a.bias != nullptr;
-  const bool two = a.n_group > 1 && a.group_top2;
+  const bool by_score = SCORED && a.bias != nullptr;
+  const bool two = SCORED && a.n_group > 1 && a.group_top2;
   F s[NV];
   bool close = false;
   if (by_score || two) {
     scores<LPT, NV, F>(a, z, top, !by_score, s);
     if (by_score) {
 #pragma unroll
-      for (int j = 0; j < NV; ++j)
-        if (i * NV + j < a.E) s[j] += (F)a.bias[i * NV + j];
+      for (int j = 0; j < NV; ++j) s[j] += (F)bias[j];
     }
 #pragma unroll
-    for (int j = 0; j < NV; ++j)
-      if (!(z[j] > -__builtin_inff()) && z[j] == z[j]) s[j] = -inf;
+    for (int j = 0; j < NV; ++j) s[j] = z[j] == -__builtin_inff() ? -inf : s[j];
   }
   uint64_t kept = ~0ull;
-  if (a.n_group > 1) {
+  const int per = a.E / a.n_group;
+  if constexpr (NV == 8 && sizeof(F) == 4) {
+    // groups of whole lanes
+    const int GL = per / 8;
+    if (a.n_group > 1 && per % 8 == 0 && GL <= 16 && (GL & (GL - 1)) == 0) {
+      const bool sc = by_score || two;
+      float v[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[j] = sc ? s[j] : z[j];
+      kept = keep_groups8<LPT>(a, v, i, GL, fx, sc, &close);
+      kept = (kept >> (i / GL & 63)) & 1 ? ~0ull : 0ull;
+    } else if (a.n_group > 1) {
+      float v[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[j] = by_score || two ? s[j] : z[j];
+      kept = keep_groups<LPT, NV, F>(a, v, i, row, by_score || two, &close);
+    }
+  } else if (a.n_group > 1) {
     if (by_score || two) {
       kept = keep_groups<LPT, NV, F>(a, s, i, row, true, &close);
     } else {
@@ -324,7 +564,6 @@ __device__ __forceinline__ bool choose_token(const RouteArgs& a, const float (&z
     }
   }
   K key[NV];
-  const int per = a.E / a.n_group;
   int g = i * NV / per, c = i * NV - g * per;  // group and place of the lane's first expert
 #pragma unroll
   for (int j = 0; j < NV; ++j) {
@@ -336,7 +575,35 @@ __device__ __forceinline__ bool choose_token(const RouteArgs& a, const float (&z
       ++g;
     }
   }
-  close |= choose<LPT, NV, F>(key, i, a.k, by_score, got);
+  if constexpr (NV == 8 && sizeof(F) == 4) {
+    const uint32_t below = 0xffffffffu - (uint32_t)(i * 8);
+    if (by_score) {
+      uint32_t s32[8], w;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) s32[j] = key[j] ? fx.pack(s[j], i * 8 + j) : 0u;
+      close |= choose_packed<LPT>(s32, i, a.k, true, &w,
+                                  [&](uint32_t p, uint32_t q) { return fx.near(p, q); });
+      *got = w ? Fixed::index(w) : -1;
+    } else if (a.bf16) {
+      uint32_t s32[8], w;
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        s32[j] = key[j] ? (key[j] & 0xffff0000u) | ((below - j) & 0xffffu) : 0u;
+      choose_packed<LPT>(s32, i, a.k, false, &w, [](uint32_t, uint32_t) { return false; });
+      *got = w ? (int)(0xffffu - (w & 0xffffu)) : -1;
+      *zgot = unord(w & 0xffff0000u);  // (the low bits of a bf16 key are zero, or ones under a sign)
+      *zgot = __uint_as_float(__float_as_uint(*zgot) & 0xffff0000u);
+    } else {
+      uint64_t s64[8], w;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) s64[j] = key[j] ? (uint64_t)key[j] << 32 | (below - j) : 0ull;
+      choose_packed<LPT>(s64, i, a.k, false, &w, [](uint64_t, uint64_t) { return false; });
+      *got = w ? (int)(0xffffffffu - (uint32_t)w) : -1;
+      *zgot = unord((uint32_t)(w >> 32));
+    }
+  } else {
+    close |= choose<LPT, NV, F>(key, i, a.k, by_score, got);
+  }
   return close;
 }
 
@@ -345,13 +612,37 @@ __device__ __forceinline__ bool choose_token(const RouteArgs& a, const float (&z
 template <int NV>
 constexpr int route_threads() { return NV > 8 ? kWave : kRouteThreads; }
 
-template <int LPT, int NV>
-__global__ __launch_bounds__(route_threads<NV>()) void k_route(RouteArgs a) {
+// (the registers of the fp64 keys would halve the waves of the other tokens:
+// at least four a SIMD for rows of up to 512 experts)
+template <int LPT, int NV, bool SCORED>
+__global__ __launch_bounds__(route_threads<NV>(), NV > 8 ? 1 : 4) void k_route(RouteArgs a) {
   LRM_DYN_SHARED(double, dyn);  // [tokens of a block][E] rows (groups), then int hist[E] (counts)
   constexpr int NT = route_threads<NV>(), tpb = NT / LPT;
   const int i = threadIdx.x & (LPT - 1);
   const int sub = threadIdx.x / LPT;
   const uint64_t bits = expert_bits<NV>(a, i * NV);
+  float bias[NV];
+#pragma unroll
+  for (int j = 0; j < NV; ++j) {
+    const int c = i * NV + j < a.E ? i * NV + j : 0;
+    bias[j] = SCORED && a.bias ? a.bias[c] : 0.f;
+  }
+  // the range of the keys (see Fixed), over the biases of all lanes
+  float blo = 0.f, bhi = 0.f;
+  if (SCORED && a.bias) {
+    blo = bhi = bias[0];
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      blo = fminf(blo, bias[j]);
+      bhi = fmaxf(bhi, bias[j]);
+    }
+    blo = group_all<LPT>(blo, OpMin());
+    bhi = group_all<LPT>(bhi, OpMax());
+  }
+  const Fixed fx(blo, bhi);
+  // bf16 logits as they are, whole lanes of 8: keys straight from the words
+  const bool direct = !SCORED && NV == 8 && a.bf16 && a.n_group == 1 && a.vec && a.E % 8 == 0 &&
+                      (!a.softmax || a.renorm);
   double* row64 = a.n_group > 1 ? dyn + (int64_t)sub * a.E : nullptr;
   int* hist = reinterpret_cast<int*>(dyn + (a.n_group > 1 ? (int64_t)tpb * a.E : 0));
   if (a.counts) {
@@ -359,30 +650,76 @@ __global__ __launch_bounds__(route_threads<NV>()) void k_route(RouteArgs a) {
     __syncthreads();
   }
   const int nrow = (a.T - 1) / tpb + 1;
+  auto row_of = [&](int64_t t) { return (const char*)a.logits + t * a.ld * (a.bf16 ? 2 : 4); };
+  RawRow raw;
+  if constexpr (NV == 8) {
+    const int64_t t0 = (int64_t)blockIdx.x * tpb + sub;
+    raw.fetch(row_of(t0 < a.T ? t0 : 0), a.bf16, a.vec != 0, i * 8, a.E);
+  }
   for (int rb = blockIdx.x; rb < nrow; rb += gridDim.x) {
     const int64_t t = (int64_t)rb * tpb + sub;
     const bool in = t < a.T;
-    const char* lrow = (const char*)a.logits + (in ? t : 0) * a.ld * (a.bf16 ? 2 : 4);
+    const char* lrow = row_of(in ? t : 0);
     const bool on = in && (a.token_mask ? a.token_mask[in ? t : 0] != 0 : true);
-    float z[NV];
-    load_row<NV>(lrow, a.bf16, a.vec != 0, i * NV, a.E, z);
-    mask_row<NV>(on ? bits : 0, z);
-    float top = -__builtin_inff();
-    if (a.softmax && (!a.renorm || a.bias || a.n_group > 1)) {
+    float z[NV], top = -__builtin_inff(), zc = 0.f;  // zc: the choice's logit
+    int e = -1;
+    bool chosen = false;
+    if constexpr (NV == 8 && !SCORED) {
+      if (direct) {
+        uint32_t s32[8], w = 0;
+        const uint32_t below = 0xffffu - (uint32_t)(i * 8);
+        const uint32_t open = on && i * 8 < a.E ? 0xffffffffu : 0u;
 #pragma unroll
-      for (int j = 0; j < NV; ++j) top = z[j] > top ? z[j] : top;
-      top = group_all<LPT>(top, OpMax());
+        for (int j = 0; j < 4; ++j) {
+          const uint32_t x = raw.q[0][j];
+          // both halves: flip the sign of positive values, all bits of others
+          const uint32_t neg = (x >> 15) & 0x00010001u;
+          const uint32_t y = x ^ (((neg << 15) - neg) | 0x80008000u);
+          s32[2 * j] = (y << 16 | (below - 2 * j)) & open;
+          s32[2 * j + 1] = ((y & 0xffff0000u) | (below - 2 * j - 1)) & open;
+        }
+        if (a.expert_mask) {
+#pragma unroll
+          for (int j = 0; j < 8; ++j) s32[j] = (bits >> j) & 1 ? s32[j] : 0u;
+        }
+        const int64_t tn = t + (int64_t)gridDim.x * tpb;
+        if (tn < a.T) raw.fetch(row_of(tn), 1, true, i * 8, a.E);
+        choose_packed<LPT>(s32, i, a.k, false, &w, [](uint32_t, uint32_t) { return false; });
+        // (-inf has key 0x007f: such a choice is none)
+        if (w >= 0x00800000u) e = (int)(0xffffu - (w & 0xffffu));
+        zc = __uint_as_float(__float_as_uint(unord(w & 0xffff0000u)) & 0xffff0000u);
+        chosen = true;
+      }
     }
-    int e;
-    const bool close = choose_token<LPT, NV, float>(a, z, top, i, (float*)row64, &e);
-    if (__ballot(close)) {  // the whole wave again, in fp64
-      int e2;
-      choose_token<LPT, NV, double>(a, z, top, i, row64, &e2);
-      e = e2;
+    if (!chosen) {
+      if constexpr (NV == 8) {
+        raw.values(lrow, a.bf16, a.vec != 0, i * 8, a.E, z);
+        const int64_t tn = t + (int64_t)gridDim.x * tpb;
+        if (tn < a.T) raw.fetch(row_of(tn), a.bf16, a.vec != 0, i * 8, a.E);
+      } else {
+        load_row<NV>(lrow, a.bf16, a.vec != 0, i * NV, a.E, z);
+      }
+      mask_row<NV>(on ? bits : 0, z);
+      if (a.softmax && (!a.renorm || a.bias || a.n_group > 1)) {
+#pragma unroll
+        for (int j = 0; j < NV; ++j) top = z[j] > top ? z[j] : top;
+        top = group_all<LPT>(top, OpMax());
+      }
+      const bool close =
+          choose_token<LPT, NV, float, SCORED>(a, z, bias, fx, top, i, (float*)row64, &e, &zc);
+      if constexpr (SCORED) {
+        if (__ballot(close)) {  // the whole wave again, in fp64
+          int e2;
+          float z2;
+          choose_token<LPT, NV, double, true>(a, z, bias, fx, top, i, row64, &e2, &z2);
+          e = e2;
+        }
+      }
     }
     // weights: lane j holds choice j
     const bool has = i < a.k && e >= 0 && e < a.E;
-    const float ze = has ? load_one(lrow, a.bf16, e) : -__builtin_inff();
+    if (SCORED || NV > 8) zc = load_one(lrow, a.bf16, has ? e : 0);
+    const float ze = has ? zc : -__builtin_inff();
     float w = 0.f;
     if (a.renorm) {
       // softmax: exp(z - m) with m the largest chosen logit.  sigmoid: both
@@ -393,20 +730,20 @@ __global__ __launch_bounds__(route_threads<NV>()) void k_route(RouteArgs a) {
       float f = 0.f;
       if (has) {
         if (a.softmax)
-          f = expf(ze - m);
+          f = exp_of(ze - m);
         else
-          f = ze <= 0.f ? expf(ze - m) / (1.f + expf(ze)) : 1.f / (1.f + expf(-ze));
+          f = ze <= 0.f ? exp_of(ze - m) * inv_of(1.f + exp_of(ze)) : inv_of(1.f + exp_of(-ze));
       }
       const float sum = group_all<LPT>(f, OpAdd());
-      w = has ? a.scale * (f / sum) : 0.f;
+      w = has ? a.scale * (f * (sum >= 1.f ? inv_of(sum) : 1.f / sum)) : 0.f;
     } else if (a.softmax) {
       float sum = 0.f;
 #pragma unroll
-      for (int j = 0; j < NV; ++j) sum += top > -__builtin_inff() ? expf(z[j] - top) : 0.f;
+      for (int j = 0; j < NV; ++j) sum += top > -__builtin_inff() ? exp_of(z[j] - top) : 0.f;
       sum = group_all<LPT>(sum, OpAdd());
-      w = has ? a.scale * (expf(ze - top) / sum) : 0.f;
+      w = has ? a.scale * (exp_of(ze - top) / sum) : 0.f;
     } else {
-      w = has ? a.scale * (1.f / (1.f + expf(-ze))) : 0.f;
+      w = has ? a.scale * inv_of(1.f + exp_of(-ze)) : 0.f;
     }
     if (in && i < a.k) {
       const int64_t at = t * a.k + i;
@@ -422,20 +759,30 @@ __global__ __launch_bounds__(route_threads<NV>()) void k_route(RouteArgs a) {
   }
 }
 
-// counts[e] = sum over the blocks of part[b][e]
-__global__ __launch_bounds__(256) void k_route_counts(int nblk, int E, const int32_t* part,
-                                                      int32_t* counts) {
-  __shared__ int lds[256];
+// counts[e] = sum over the blocks of part[b][e]: 32 experts a block, 32 rows of
+// part at a time, eight loads in flight a thread.
+__global__ __launch_bounds__(1024) void k_route_counts(int nblk, int E, const int32_t* part,
+                                                       int32_t* counts) {
+  __shared__ int lds[32][33];
   const int c = threadIdx.x & 31, r = threadIdx.x >> 5;
-  const int e = blockIdx.x * 32 + c;
+  const int e = blockIdx.x * 32 + c, ec = e < E ? e : 0;
   int s = 0;
-  if (e < E)
-    for (int b = r; b < nblk; b += 8) s += part[(int64_t)b * E + e];
-  lds[threadIdx.x] = s;
+  for (int b0 = r; b0 < nblk; b0 += 256) {
+    int v[8];
+#pragma unroll
+    for (int q = 0; q < 8; ++q) {
+      const int b = b0 + q * 32;
+      v[q] = part[(int64_t)(b < nblk ? b : 0) * E + ec];
+      v[q] = b < nblk ? v[q] : 0;
+    }
+#pragma unroll
+    for (int q = 0; q < 8; ++q) s += v[q];
+  }
+  lds[r][c] = s;
   __syncthreads();
   if (r == 0 && e < E) {
 #pragma unroll
-    for (int q = 1; q < 8; ++q) s += lds[q * 32 + c];
+    for (int q = 1; q < 32; ++q) s += lds[q][c];
     counts[e] = s;
   }
 }
@@ -479,10 +826,10 @@ __global__ __launch_bounds__(kRouteThreads) void k_route_bwd(RouteArgs a, const 
       float f = 0.f, q = 1.f;
       if (has) {
         if (a.softmax) {
-          f = expf(ze - m);
+          f = exp_of(ze - m);
         } else {
-          q = 1.f / (1.f + expf(ze));  // 1 - sigmoid
-          f = ze <= 0.f ? expf(ze - m) * q : 1.f / (1.f + expf(-ze));
+          q = inv_of(1.f + exp_of(ze));  // 1 - sigmoid
+          f = ze <= 0.f ? exp_of(ze - m) * q : inv_of(1.f + exp_of(-ze));
         }
       }
       const float sum = group_all<LPT>(f, OpAdd());
@@ -498,17 +845,17 @@ __global__ __launch_bounds__(kRouteThreads) void k_route_bwd(RouteArgs a, const 
       top = group_all<LPT>(top, OpMax());
 #pragma unroll
       for (int j = 0; j < NV; ++j) {
-        p[j] = top > -__builtin_inff() ? expf(p[j] - top) : 0.f;
+        p[j] = top > -__builtin_inff() ? exp_of(p[j] - top) : 0.f;
         sum += p[j];
       }
       sum = group_all<LPT>(sum, OpAdd());
       const float inv = sum > 0.f ? 1.f / sum : 0.f;
 #pragma unroll
       for (int j = 0; j < NV; ++j) p[j] *= inv;
-      d = has ? expf(ze - top) * inv * v : 0.f;
+      d = has ? exp_of(ze - top) * inv * v : 0.f;
       dot = group_all<LPT>(d, OpAdd());
     } else if (has) {
-      d = v * (1.f / (1.f + expf(-ze))) * (1.f / (1.f + expf(ze)));
+      d = v * inv_of(1.f + exp_of(-ze)) * inv_of(1.f + exp_of(ze));
     }
     slots[threadIdx.x] = Slot{e, d};
     wave_sync();
@@ -608,9 +955,12 @@ hipError_t route_launch(const RouteArgs& a, int32_t* counts, hipStream_t s) {
   const size_t sh = (a.n_group > 1 ? (size_t)tpb * a.E * 8 : 0) + (counts ? (size_t)a.E * 4 : 0);
   RouteArgs b = a;
   b.counts = counts ? (grid == 1 ? counts : a.counts) : nullptr;
-  LRM_LAUNCH(grid, nt, sh, s, k_route<LPT, NV>)(b);
+  if (a.bias || (a.n_group > 1 && a.group_top2))
+    LRM_LAUNCH(grid, nt, sh, s, k_route<LPT, NV, true>)(b);
+  else
+    LRM_LAUNCH(grid, nt, sh, s, k_route<LPT, NV, false>)(b);
   if (counts && grid > 1)
-    LRM_LAUNCH((a.E + 31) / 32, 256, 0, s, k_route_counts)(grid, a.E, a.counts, counts);
+    LRM_LAUNCH((a.E + 31) / 32, 1024, 0, s, k_route_counts)(grid, a.E, a.counts, counts);
   return hipGetLastError();
 }
 

@@ -248,7 +248,7 @@ struct RouteArgs {
   int32_t* token;   // or nullptr
   int32_t* counts;  // scratch [kRouteBlocks][E] (needed when counts are wanted)
 };
-constexpr int kRouteBlocks = 2048;  // persistent blocks of the routing kernel, at most
+constexpr int kRouteBlocks = 1024;  // persistent blocks of the routing kernel, at most
 hipError_t launch_route(const RouteArgs& a, int32_t* counts, hipStream_t s);
 hipError_t launch_route_bwd(const RouteArgs& a, const int32_t* expert, const float* dweight,
                             void* dlogits, int64_t ldd, int vec_out, hipStream_t s);

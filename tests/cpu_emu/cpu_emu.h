@@ -299,7 +299,8 @@ typedef ::emu::BufRsrc __amdgpu_buffer_rsrc_t;
 
 namespace emu {
 // DPP model for the controls the kernels use: row_shr:n (0x110 + n),
-// row_ror:n (0x120 + n), row_bcast:15 (0x142), row_bcast:31 (0x143);
+// row_ror:n (0x120 + n), quad_perm (below 0x100), row_mirror (0x140),
+// row_half_mirror (0x141), row_bcast:15 (0x142), row_bcast:31 (0x143);
 // bound_ctrl off (lanes without a valid source, or in rows outside row_mask,
 // get old).
 inline int update_dpp(int old, int src, int ctrl, int row_mask) {
@@ -311,6 +312,12 @@ inline int update_dpp(int old, int src, int ctrl, int row_mask) {
   } else if (ctrl > 0x120 && ctrl < 0x130) {
     const int n = ctrl - 0x120;
     from = 16 * row + ((i - n) & 15);
+  } else if (ctrl < 0x100) {  // quad_perm
+    from = (lane & ~3) | ((ctrl >> (2 * (lane & 3))) & 3);
+  } else if (ctrl == 0x140) {  // row_mirror
+    from = 16 * row + 15 - i;
+  } else if (ctrl == 0x141) {  // row_half_mirror
+    from = (lane & ~7) + 7 - (lane & 7);
   } else if (ctrl == 0x142) {
     if (row >= 1) from = 16 * row - 1;
   } else if (ctrl == 0x143) {
