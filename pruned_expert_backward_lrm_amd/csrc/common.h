@@ -93,34 +93,66 @@ __device__ __forceinline__ int64_t pair_row(int rows_is_pair, const int32_t* tok
 // SiLU pieces in fp32 (accurate expf).
 __device__ __forceinline__ float sigmoidf_acc(float a) { return 1.0f / (1.0f + expf(-a)); }
 
-// Activations of the forward pass (lrm_act) in fp32 and their derivatives.
-// GELU is z * Phi(z), Phi the normal distribution function.
-constexpr int kActNone = 0, kActRelu = 1, kActGelu = 2, kActSilu = 3;
-template <int ACT>
-__device__ __forceinline__ float act_of(float z) {
-  if constexpr (ACT == kActRelu) return z > 0.f ? z : 0.f;
-  if constexpr (ACT == kActGelu) return 0.5f * z * (1.f + erff(z * 0.70710678118654752f));
-  if constexpr (ACT == kActSilu) return z * sigmoidf_acc(z);
-  return z;
+// 1 / (1 + e^-a) from the hardware's exp2 and reciprocal with one Newton step:
+// relative error about (|a| + 2) 2^-24; e^-a is held below 2^126.
+__device__ __forceinline__ float sigmoid_of(float a) {
+  const float d = 1.f + __builtin_amdgcn_exp2f(fminf(a * -1.44269504f, 126.f));
+  const float r = __builtin_amdgcn_rcpf(d);
+  return fmaf(r, fmaf(-d, r, 1.f), r);
 }
+
+// Phi(z), the normal distribution function, and e = e^(-z^2/2), which both GELU
+// and its derivative need: erfc(x) = t (a1 + t (a2 + .. a5 t^4)) e^(-x^2) with
+// t = 1 / (1 + p x), x = |z| / sqrt 2 (Abramowitz and Stegun 7.1.26).  In a
+// float32 model: absolute error of Phi up to 3e-7, z Phi(z) and its derivative
+// to 5 2^-24 (1 + |z|), relative error of Phi up to 0.4% at z = -6.  For bf16
+// data, whose rounding is of that size; fp32 data take erff.
+__device__ __forceinline__ float normal_cdf(float z, float& e) {
+  e = __builtin_amdgcn_exp2f(z * z * -0.72134752f);
+  const float d = fmaf(fabsf(z), 0.231641888f, 1.f);  // p / sqrt 2
+  float t = __builtin_amdgcn_rcpf(d);
+  t = fmaf(t, fmaf(-d, t, 1.f), t);
+  float q = fmaf(t, 1.061405429f, -1.453152027f);
+  q = fmaf(t, q, 1.421413741f);
+  q = fmaf(t, q, -0.284496736f);
+  q = fmaf(t, q, 0.254829592f);
+  const float tail = 0.5f * t * q * e;  // Phi(-|z|)
+  return z > 0.f ? 1.f - tail : tail;
+}
+
+// Activations of the forward pass (lrm_act) in fp32 and their derivatives.
+// GELU is z * Phi(z), Phi the normal distribution function.  FAST: bf16 data.
+constexpr int kActNone = 0, kActRelu = 1, kActGelu = 2, kActSilu = 3;
 // act(z) in y and act'(z) in g
-template <int ACT>
+template <int ACT, bool FAST>
 __device__ __forceinline__ void act_both(float z, float& y, float& g) {
   if constexpr (ACT == kActRelu) {
     y = z > 0.f ? z : 0.f;
     g = z > 0.f ? 1.f : 0.f;
   } else if constexpr (ACT == kActGelu) {
-    const float phi = 0.5f * (1.f + erff(z * 0.70710678118654752f));
+    float e, phi;
+    if constexpr (FAST) {
+      phi = normal_cdf(z, e);
+    } else {
+      phi = 0.5f * (1.f + erff(z * 0.70710678118654752f));
+      e = expf(-0.5f * z * z);
+    }
     y = z * phi;
-    g = phi + z * 0.39894228040143268f * expf(-0.5f * z * z);
+    g = fmaf(z * 0.39894228040143268f, e, phi);
   } else if constexpr (ACT == kActSilu) {
-    const float s = sigmoidf_acc(z);
+    const float s = FAST ? sigmoid_of(z) : sigmoidf_acc(z);
     y = z * s;
     g = s * (1.f + z * (1.f - s));
   } else {
     y = z;
     g = 1.f;
   }
+}
+template <int ACT, bool FAST>
+__device__ __forceinline__ float act_of(float z) {
+  float y, g;
+  act_both<ACT, FAST>(z, y, g);
+  return y;
 }
 
 // Device error bits (written into the first word of a workspace).

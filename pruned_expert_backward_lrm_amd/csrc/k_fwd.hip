@@ -20,9 +20,9 @@ namespace {
 
 __device__ __forceinline__ float act_rt(int act, float z) {
   switch (act) {
-    case kActRelu: return act_of<kActRelu>(z);
-    case kActGelu: return act_of<kActGelu>(z);
-    case kActSilu: return act_of<kActSilu>(z);
+    case kActRelu: return act_of<kActRelu, false>(z);
+    case kActGelu: return act_of<kActGelu, false>(z);
+    case kActSilu: return act_of<kActSilu, false>(z);
   }
   return z;
 }
@@ -46,7 +46,7 @@ __device__ __forceinline__ float join_bits(uint32_t hi16, int lo8) {
 }
 
 // act of a wave's row of fragments; one loop over registers for each kind
-template <int FO>
+template <int FO, bool FAST>
 __device__ __forceinline__ void act_rows(int act, f32x4 (&u)[FO]) {
   auto all = [&](auto f) {
 #pragma unroll
@@ -55,11 +55,11 @@ __device__ __forceinline__ void act_rows(int act, f32x4 (&u)[FO]) {
       for (int q = 0; q < 4; ++q) u[j][q] = f(u[j][q]);
   };
   if (act == kActRelu)
-    all([](float z) { return act_of<kActRelu>(z); });
+    all([](float z) { return act_of<kActRelu, FAST>(z); });
   else if (act == kActGelu)
-    all([](float z) { return act_of<kActGelu>(z); });
+    all([](float z) { return act_of<kActGelu, FAST>(z); });
   else
-    all([](float z) { return act_of<kActSilu>(z); });
+    all([](float z) { return act_of<kActSilu, FAST>(z); });
 }
 
 // silu for results that are rounded to bf16: the hardware's exp2 and reciprocal
@@ -358,7 +358,7 @@ __device__ __forceinline__ int fwd_store(const FwdGemmArgs& g, const FwdJob& job
           put(g.Z, v);
         }
         if (!EPI || g.Y) {
-          if (EPI && g.act != kActNone) act_rows<FO>(g.act, u);
+          if (EPI && g.act != kActNone) act_rows<FO, true>(g.act, u);
 #pragma unroll
           for (int j = 0; j < FO; ++j) {
 #pragma unroll
@@ -560,6 +560,8 @@ __global__ __launch_bounds__(C::NT, 2) void k_fwd_tile(FwdGemmArgs g) {
     for (int i = 0; i < C::FM; ++i)
 #pragma unroll
       for (int j = 0; j < C::FN; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
+    // (a wave whose rows lie past the expert's end only keeps step)
+    const bool live = wm * C::TM < cur.rows;
     // A wave enters with the k-tile's fragments read (or on their way).  Past
     // the barrier every wave has them, so the stage takes the k-tile four on,
     // and the next k-tile's loads have arrived.
@@ -567,14 +569,19 @@ __global__ __launch_bounds__(C::NT, 2) void k_fwd_tile(FwdGemmArgs g) {
       stage_barrier<L>(vm - mk[1]);
       const int free = st;
       st = (st + 1) & (kStages - 1);
-      then.read(lds + st * C::SS, ao, bo);
-      now.template multiply<BF16, 0, C::FM / 2>(acc);
-      interleave<C, BF16>();
+      const char* stage = lds + st * C::SS;
+      if (live) {
+        then.read(stage, ao, bo);
+        now.template multiply<BF16, 0, C::FM / 2>(acc);
+        interleave<C, BF16>();
+      } else {
+        then.read(stage, ao, bo);
+      }
       feed(free);
 #pragma unroll
       for (int s = 0; s < kStages - 1; ++s) mk[s] = mk[s + 1];
       mk[kStages - 1] = vm;
-      now.template multiply<BF16, C::FM / 2, C::FM>(acc);
+      if (live) now.template multiply<BF16, C::FM / 2, C::FM>(acc);
     };
     for (int k = 0; k < nk; k += 2) {
       step(f0, f1);

@@ -119,9 +119,9 @@ __device__ __forceinline__ float get1(const void* base, int64_t at) {
 __device__ __forceinline__ f32x4 act4(int act, f32x4 z) {
 #pragma unroll
   for (int q = 0; q < 4; ++q)
-    z[q] = act == kActRelu   ? act_of<kActRelu>(z[q])
-           : act == kActGelu ? act_of<kActGelu>(z[q])
-           : act == kActSilu ? act_of<kActSilu>(z[q])
+    z[q] = act == kActRelu   ? act_of<kActRelu, false>(z[q])
+           : act == kActGelu ? act_of<kActGelu, false>(z[q])
+           : act == kActSilu ? act_of<kActSilu, false>(z[q])
                              : z[q];
   return z;
 }

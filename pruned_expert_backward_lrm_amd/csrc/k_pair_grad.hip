@@ -45,8 +45,8 @@ __device__ __forceinline__ void store8(void* row, int c, int d, const float (&v)
   if constexpr (BF16) {
     if (c < d)
       *reinterpret_cast<u32x4*>((uint16_t*)row + c) =
-          u32x4{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]),
-                pack_bf16x2(v[6], v[7])};
+          u32x4{cvt_pk_bf16(v[0], v[1]), cvt_pk_bf16(v[2], v[3]), cvt_pk_bf16(v[4], v[5]),
+                cvt_pk_bf16(v[6], v[7])};
   } else {
     if (c < d) *reinterpret_cast<f32x4*>((float*)row + c) = f32x4{v[0], v[1], v[2], v[3]};
     if (c + 4 < d) *reinterpret_cast<f32x4*>((float*)row + c + 4) = f32x4{v[4], v[5], v[6], v[7]};
@@ -80,7 +80,7 @@ __global__ __launch_bounds__(256) void k_pair_grad(PairGradArgs a) {
       g8[j] = 0.f;
       if (there) {
         float act, der;
-        act_both<ACT>(z8[j], act, der);
+        act_both<ACT, BF16>(z8[j], act, der);
         sum = fmaf(y8[j], act, sum);
         g8[j] = y8[j] * der;
       }
@@ -123,7 +123,7 @@ __global__ __launch_bounds__(256) void k_pair_grad_bias(PairGradArgs a) {
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
         float act, der;
-        act_both<ACT>(z8[j], act, der);
+        act_both<ACT, BF16>(z8[j], act, der);
         sum = fmaf(y8[j], act, sum);
         g8[j] = y8[j] * der;
         acc[q][j] = fmaf(wt, g8[j], acc[q][j]);
@@ -152,7 +152,13 @@ __global__ __launch_bounds__(256) void k_pair_grad_join(PairGradArgs a, int S) {
   const int64_t step = (int64_t)gridDim.x * 256;
   for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n; i += step) {
     float v = 0.f;
-    for (int s = 0; s < S; ++s) v += a.part[s * n + i];
+    for (int s0 = 0; s0 < S; s0 += 8) {
+      float x[8];
+#pragma unroll
+      for (int q = 0; q < 8; ++q) x[q] = a.part[(s0 + q < S ? s0 + q : 0) * n + i];
+#pragma unroll
+      for (int q = 0; q < 8; ++q) v += s0 + q < S ? x[q] : 0.f;
+    }
     a.dbias[i] = v;
   }
   for (int64_t p = (int64_t)blockIdx.x * 256 + threadIdx.x; p < a.N; p += step) {

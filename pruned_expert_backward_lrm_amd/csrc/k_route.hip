@@ -11,7 +11,8 @@
 // complement below it (16 bits of each for bf16 logits, 32 otherwise), so that
 // one maximum over the lanes decides key and tie; every lane sorts its 8 once
 // and a round only compares the lanes' heads (65536 tokens, 128 experts, top-8:
-// R_SORT us instead of 26 with a search of all 8 every round).  Larger rows and
+// 11.3 us, and 3.9 for the counts, instead of 26 with a search of all 8 every
+// round; 273 vector instructions for four tokens bound it).  Larger rows and
 // fp64 keys take the maximum key, then the minimum expert among its holders.
 //
 // Order of the choice: without a bias the scores order like the logits, which
@@ -612,6 +613,89 @@ __device__ __forceinline__ bool choose_token(const RouteArgs& a, const float (&z
 template <int NV>
 constexpr int route_threads() { return NV > 8 ? kWave : kRouteThreads; }
 
+// The weight of a lane's choice from the logits of the token's choices alone
+// (zc of the lanes that have one): renormalised, or a sigmoid.
+template <int LPT>
+__device__ __forceinline__ float chosen_weight(const RouteArgs& a, bool has, float zc) {
+  const float ze = has ? zc : -__builtin_inff();
+  if (!a.renorm) return has ? a.scale * inv_of(1.f + exp_of(-ze)) : 0.f;
+  // softmax: exp(z - m) with m the largest chosen logit.  sigmoid: both
+  // numerator and sum times e^-m, m = min(largest chosen logit, 0), so that the
+  // sum cannot underflow.
+  float m = group_all<LPT>(ze, OpMax());
+  if (!a.softmax) m = m < 0.f ? m : 0.f;
+  float f = 0.f;
+  if (has)
+    f = a.softmax ? exp_of(ze - m)
+                  : (ze <= 0.f ? exp_of(ze - m) * inv_of(1.f + exp_of(ze)) : inv_of(1.f + exp_of(-ze)));
+  const float sum = group_all<LPT>(f, OpAdd());
+  return has ? a.scale * (f / sum) : 0.f;
+}
+
+// bf16 logits that are the keys as they are (no bias, no groups), in aligned
+// rows of whole lanes: keys straight from the words, weights from the keys.
+// (A kernel of its own: as a branch of k_route the scalar registers spill, and
+// the 65536-token call took 14.2 us instead of 11.3.)
+template <int LPT>
+__global__ __launch_bounds__(kRouteThreads) void k_route_direct(RouteArgs a) {
+  LRM_DYN_SHARED(int, hist);
+  constexpr int tpb = kRouteThreads / LPT;
+  const int i = threadIdx.x & (LPT - 1), sub = threadIdx.x / LPT;
+  const bool lane_on = i * 8 < a.E;
+  uint32_t bits = lane_on ? 0xffu : 0u;
+  if (a.expert_mask && lane_on) bits = (uint32_t)expert_bits<8>(a, i * 8);
+  if (a.counts) {
+    for (int e = threadIdx.x; e < a.E; e += kRouteThreads) hist[e] = 0;
+    __syncthreads();
+  }
+  const uint32_t below = 0xffffu - (uint32_t)(i * 8);
+  auto fetch = [&](int64_t t) {
+    return *reinterpret_cast<const u32x4*>((const uint16_t*)a.logits + t * a.ld + (lane_on ? i * 8 : 0));
+  };
+  const int nrow = (a.T - 1) / tpb + 1;
+  const int64_t t0 = (int64_t)blockIdx.x * tpb + sub;
+  u32x4 raw = fetch(t0 < a.T ? t0 : 0);
+  for (int rb = blockIdx.x; rb < nrow; rb += gridDim.x) {
+    const int64_t t = (int64_t)rb * tpb + sub, tn = t + (int64_t)gridDim.x * tpb;
+    const bool in = t < a.T;
+    const u32x4 x = raw;
+    if (rb + (int)gridDim.x < nrow) raw = fetch(tn < a.T ? tn : 0);
+    const bool on = in && (a.token_mask ? a.token_mask[in ? t : 0] != 0 : true);
+    const uint32_t open = on && lane_on ? 0xffffffffu : 0u;
+    uint32_t s32[8], w = 0;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      // both halves: flip the sign of positive values, all bits of others
+      const uint32_t neg = (x[j] >> 15) & 0x00010001u;
+      const uint32_t y = x[j] ^ (((neg << 15) - neg) | 0x80008000u);
+      s32[2 * j] = (y << 16 | (below - 2 * j)) & open;
+      s32[2 * j + 1] = ((y & 0xffff0000u) | (below - 2 * j - 1)) & open;
+    }
+    if (a.expert_mask) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) s32[j] = (bits >> j) & 1 ? s32[j] : 0u;
+    }
+    choose_packed<LPT>(s32, i, a.k, false, &w, [](uint32_t, uint32_t) { return false; });
+    // (-inf has key 0x007f: such a choice is none)
+    const bool has = i < a.k && w >= 0x00800000u;
+    const int e = (int)(0xffffu - (w & 0xffffu));
+    const float zc = __uint_as_float(__float_as_uint(unord(w & 0xffff0000u)) & 0xffff0000u);
+    const float wt = chosen_weight<LPT>(a, has, zc);
+    if (in && i < a.k) {
+      const int64_t at = t * a.k + i;
+      a.expert[at] = has ? e : -1;
+      a.weight[at] = wt;
+      if (a.token) a.token[at] = (int32_t)t;
+      if (a.counts && has) atomicAdd(&hist[e], 1);
+    }
+  }
+  if (a.counts) {
+    __syncthreads();
+    for (int e = threadIdx.x; e < a.E; e += kRouteThreads)
+      a.counts[(int64_t)blockIdx.x * a.E + e] = hist[e];
+  }
+}
+
 // (the registers of the fp64 keys would halve the waves of the other tokens:
 // at least four a SIMD for rows of up to 512 experts)
 template <int LPT, int NV, bool SCORED>
@@ -640,9 +724,6 @@ __global__ __launch_bounds__(route_threads<NV>(), NV > 8 ? 1 : 4) void k_route(R
     bhi = group_all<LPT>(bhi, OpMax());
   }
   const Fixed fx(blo, bhi);
-  // bf16 logits as they are, whole lanes of 8: keys straight from the words
-  const bool direct = !SCORED && NV == 8 && a.bf16 && a.n_group == 1 && a.vec && a.E % 8 == 0 &&
-                      (!a.softmax || a.renorm);
   double* row64 = a.n_group > 1 ? dyn + (int64_t)sub * a.E : nullptr;
   int* hist = reinterpret_cast<int*>(dyn + (a.n_group > 1 ? (int64_t)tpb * a.E : 0));
   if (a.counts) {
@@ -663,87 +744,41 @@ __global__ __launch_bounds__(route_threads<NV>(), NV > 8 ? 1 : 4) void k_route(R
     const bool on = in && (a.token_mask ? a.token_mask[in ? t : 0] != 0 : true);
     float z[NV], top = -__builtin_inff(), zc = 0.f;  // zc: the choice's logit
     int e = -1;
-    bool chosen = false;
-    if constexpr (NV == 8 && !SCORED) {
-      if (direct) {
-        uint32_t s32[8], w = 0;
-        const uint32_t below = 0xffffu - (uint32_t)(i * 8);
-        const uint32_t open = on && i * 8 < a.E ? 0xffffffffu : 0u;
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const uint32_t x = raw.q[0][j];
-          // both halves: flip the sign of positive values, all bits of others
-          const uint32_t neg = (x >> 15) & 0x00010001u;
-          const uint32_t y = x ^ (((neg << 15) - neg) | 0x80008000u);
-          s32[2 * j] = (y << 16 | (below - 2 * j)) & open;
-          s32[2 * j + 1] = ((y & 0xffff0000u) | (below - 2 * j - 1)) & open;
-        }
-        if (a.expert_mask) {
-#pragma unroll
-          for (int j = 0; j < 8; ++j) s32[j] = (bits >> j) & 1 ? s32[j] : 0u;
-        }
-        const int64_t tn = t + (int64_t)gridDim.x * tpb;
-        if (tn < a.T) raw.fetch(row_of(tn), 1, true, i * 8, a.E);
-        choose_packed<LPT>(s32, i, a.k, false, &w, [](uint32_t, uint32_t) { return false; });
-        // (-inf has key 0x007f: such a choice is none)
-        if (w >= 0x00800000u) e = (int)(0xffffu - (w & 0xffffu));
-        zc = __uint_as_float(__float_as_uint(unord(w & 0xffff0000u)) & 0xffff0000u);
-        chosen = true;
-      }
+    if constexpr (NV == 8) {
+      raw.values(lrow, a.bf16, a.vec != 0, i * 8, a.E, z);
+      const int64_t tn = t + (int64_t)gridDim.x * tpb;
+      if (tn < a.T) raw.fetch(row_of(tn), a.bf16, a.vec != 0, i * 8, a.E);
+    } else {
+      load_row<NV>(lrow, a.bf16, a.vec != 0, i * NV, a.E, z);
     }
-    if (!chosen) {
-      if constexpr (NV == 8) {
-        raw.values(lrow, a.bf16, a.vec != 0, i * 8, a.E, z);
-        const int64_t tn = t + (int64_t)gridDim.x * tpb;
-        if (tn < a.T) raw.fetch(row_of(tn), a.bf16, a.vec != 0, i * 8, a.E);
-      } else {
-        load_row<NV>(lrow, a.bf16, a.vec != 0, i * NV, a.E, z);
-      }
-      mask_row<NV>(on ? bits : 0, z);
-      if (a.softmax && (!a.renorm || a.bias || a.n_group > 1)) {
+    mask_row<NV>(on ? bits : 0, z);
+    if (a.softmax && (!a.renorm || a.bias || a.n_group > 1)) {
 #pragma unroll
-        for (int j = 0; j < NV; ++j) top = z[j] > top ? z[j] : top;
-        top = group_all<LPT>(top, OpMax());
-      }
-      const bool close =
-          choose_token<LPT, NV, float, SCORED>(a, z, bias, fx, top, i, (float*)row64, &e, &zc);
-      if constexpr (SCORED) {
-        if (__ballot(close)) {  // the whole wave again, in fp64
-          int e2;
-          float z2;
-          choose_token<LPT, NV, double, true>(a, z, bias, fx, top, i, row64, &e2, &z2);
-          e = e2;
-        }
+      for (int j = 0; j < NV; ++j) top = z[j] > top ? z[j] : top;
+      top = group_all<LPT>(top, OpMax());
+    }
+    const bool close =
+        choose_token<LPT, NV, float, SCORED>(a, z, bias, fx, top, i, (float*)row64, &e, &zc);
+    if constexpr (SCORED) {
+      if (__ballot(close)) {  // the whole wave again, in fp64
+        int e2;
+        float z2;
+        choose_token<LPT, NV, double, true>(a, z, bias, fx, top, i, row64, &e2, &z2);
+        e = e2;
       }
     }
     // weights: lane j holds choice j
     const bool has = i < a.k && e >= 0 && e < a.E;
     if (SCORED || NV > 8) zc = load_one(lrow, a.bf16, has ? e : 0);
-    const float ze = has ? zc : -__builtin_inff();
-    float w = 0.f;
-    if (a.renorm) {
-      // softmax: exp(z - m) with m the largest chosen logit.  sigmoid: both
-      // numerator and sum times e^-m, m = min(largest chosen logit, 0), so
-      // that the sum cannot underflow.
-      float m = group_all<LPT>(ze, OpMax());
-      if (!a.softmax) m = m < 0.f ? m : 0.f;
-      float f = 0.f;
-      if (has) {
-        if (a.softmax)
-          f = exp_of(ze - m);
-        else
-          f = ze <= 0.f ? exp_of(ze - m) * inv_of(1.f + exp_of(ze)) : inv_of(1.f + exp_of(-ze));
-      }
-      const float sum = group_all<LPT>(f, OpAdd());
-      w = has ? a.scale * (f * (sum >= 1.f ? inv_of(sum) : 1.f / sum)) : 0.f;
-    } else if (a.softmax) {
+    float w;
+    if (a.softmax && !a.renorm) {
       float sum = 0.f;
 #pragma unroll
       for (int j = 0; j < NV; ++j) sum += top > -__builtin_inff() ? exp_of(z[j] - top) : 0.f;
       sum = group_all<LPT>(sum, OpAdd());
-      w = has ? a.scale * (exp_of(ze - top) / sum) : 0.f;
+      w = has ? a.scale * (exp_of(zc - top) / sum) : 0.f;
     } else {
-      w = has ? a.scale * inv_of(1.f + exp_of(-ze)) : 0.f;
+      w = chosen_weight<LPT>(a, has, zc);
     }
     if (in && i < a.k) {
       const int64_t at = t * a.k + i;
@@ -955,7 +990,11 @@ hipError_t route_launch(const RouteArgs& a, int32_t* counts, hipStream_t s) {
   const size_t sh = (a.n_group > 1 ? (size_t)tpb * a.E * 8 : 0) + (counts ? (size_t)a.E * 4 : 0);
   RouteArgs b = a;
   b.counts = counts ? (grid == 1 ? counts : a.counts) : nullptr;
-  if (a.bias || (a.n_group > 1 && a.group_top2))
+  const bool direct = NV == 8 && a.bf16 && a.vec && a.E % 8 == 0 && !a.bias && a.n_group == 1 &&
+                      (a.renorm || !a.softmax);
+  if (direct)
+    LRM_LAUNCH(grid, kRouteThreads, sh, s, k_route_direct<LPT>)(b);
+  else if (a.bias || (a.n_group > 1 && a.group_top2))
     LRM_LAUNCH(grid, nt, sh, s, k_route<LPT, NV, true>)(b);
   else
     LRM_LAUNCH(grid, nt, sh, s, k_route<LPT, NV, false>)(b);
