@@ -560,8 +560,6 @@ __global__ __launch_bounds__(C::NT, 2) void k_fwd_tile(FwdGemmArgs g) {
     for (int i = 0; i < C::FM; ++i)
 #pragma unroll
       for (int j = 0; j < C::FN; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
-    // (a wave whose rows lie past the expert's end only keeps step)
-    const bool live = wm * C::TM < cur.rows;
     // A wave enters with the k-tile's fragments read (or on their way).  Past
     // the barrier every wave has them, so the stage takes the k-tile four on,
     // and the next k-tile's loads have arrived.
@@ -569,19 +567,14 @@ __global__ __launch_bounds__(C::NT, 2) void k_fwd_tile(FwdGemmArgs g) {
       stage_barrier<L>(vm - mk[1]);
       const int free = st;
       st = (st + 1) & (kStages - 1);
-      const char* stage = lds + st * C::SS;
-      if (live) {
-        then.read(stage, ao, bo);
-        now.template multiply<BF16, 0, C::FM / 2>(acc);
-        interleave<C, BF16>();
-      } else {
-        then.read(stage, ao, bo);
-      }
+      then.read(lds + st * C::SS, ao, bo);
+      now.template multiply<BF16, 0, C::FM / 2>(acc);
+      interleave<C, BF16>();
       feed(free);
 #pragma unroll
       for (int s = 0; s < kStages - 1; ++s) mk[s] = mk[s + 1];
       mk[kStages - 1] = vm;
-      if (live) now.template multiply<BF16, C::FM / 2, C::FM>(acc);
+      now.template multiply<BF16, C::FM / 2, C::FM>(acc);
     };
     for (int k = 0; k < nk; k += 2) {
       step(f0, f1);
