@@ -131,21 +131,26 @@ __device__ __forceinline__ void emit(const FwdGemmArgs& g, int e, int m, int p, 
 //
 // Output tiles of BM packed rows of one expert x BN weight rows (GLU: BN/2 of
 // W0 and the same BN/2 of W1, so that a lane holds a and b of the same
-// elements).  Both operands have k contiguous in memory: 64-byte pieces of
-// their rows (32 k in bf16, 16 in fp32) go straight from memory into LDS
+// elements).  Both operands have k contiguous in memory: 128-byte pieces of
+// their rows (64 k in bf16, 32 in fp32) go straight from memory into LDS
 // (dma16), kStages deep; a row gathered through the pairs costs nothing more,
 // since every lane brings its own offset.  Lanes past an expert's rows, past
 // the columns or past K take an offset outside the bound and write zeros.
-// Granule G (16 bytes) of row r sits at G ^ swz64(r): the four 16-lane passes
-// of a 16-byte LDS read then hit 16 distinct slots of the banks each.
+// Granule G (16 bytes) of row r sits at G ^ swz128(r): the four 16-lane passes
+// of a 16-byte LDS read then hit 16 distinct slots of the banks each.  Whole
+// lines of 128 bytes matter: the loads alone take 445 us for the gate/up
+// product of 131072 rows, 2048 x 2 x 768, and 580 in pieces of 64 bytes.
 //
-// Pipeline: while the products of k-tile k run from registers, the fragments
-// of k + 1 are read from LDS and the loads of k + 2 .. k + 4 are in flight.
-// Depth decides: with two stages of 64 k (one k-tile in flight) the same
-// products took 857 us instead of 592 when the loads were left out (Qwen3
-// gate/up, 131072 rows, without stores).  Waits name how many younger memory
-// instructions may stand (the counter retires in order), so that neither the
-// loads behind a k-tile nor a finished tile's stores are waited for.
+// Pipeline: a stage is multiplied in four quarters (half of the wave's rows x
+// half of k); each quarter reads from LDS what the next one multiplies.  A part
+// of a stage is loaded again as soon as every wave has its fragments: B and the
+// first half of A after the first quarter, the second half of A after the third,
+// 1.5 stages before they are needed (96 KB in flight per CU).  Waits name how
+// many younger memory instructions may stand (the counter retires in order), so
+// that neither the loads behind a part nor a finished tile's stores are waited
+// for.  The down product (768 x 2048, 131072 rows) takes 546 us, with four
+// stages of 64 bytes it took 647; 200 us of it go to 805 MB of stores that the
+// loads of the next tile cannot pass in that counter.
 //
 // Persistent blocks: each XCD (block b runs on XCD b mod 8) owns a contiguous
 // eighth of the tiles, in which an expert's tiles lie 8 row tiles high, column
@@ -155,18 +160,19 @@ __device__ __forceinline__ void emit(const FwdGemmArgs& g, int e, int m, int p, 
 // fp32 runs v_mfma_f32_16x16x4: a lane's 16-byte granule holds four k, and
 // step s multiplies the s-th of every lane.  Which k those are is the same for
 // both operands, so every k is met once.
-constexpr int kStages = 4;
+constexpr int kStages = 2;
 
 template <int BM_, int BN_, int WGM_, int WGN_>
 struct FwdCfg {
   static constexpr int BM = BM_, BN = BN_, WGM = WGM_, WGN = WGN_, NW = WGM * WGN, NT = 64 * NW;
   static constexpr int TM = BM / WGM, TN = BN / WGN, FM = TM / 16, FN = TN / 16;
-  static constexpr int QA = BM / 16 / NW, QB = BN / 16 / NW;  // 1 KB loads per wave and stage
-  static constexpr int SA = BM * 64, SS = (BM + BN) * 64;     // bytes of a stage
-  static_assert(BM % (16 * NW) == 0 && BN % (16 * NW) == 0 && TN % 32 == 0 && TM % 32 == 0, "tile");
+  static constexpr int QA = BM / 16 / NW, QB = BN / 8 / NW;  // 1 KB loads per wave: half of A, B
+  static constexpr int L = 2 * QA + QB;                      // and of a stage
+  static constexpr int SA = BM * 128, SS = (BM + BN) * 128;  // bytes of a stage
+  static_assert(BM % (16 * NW) == 0 && BN % (8 * NW) == 0 && TN % 32 == 0 && TM % 32 == 0, "tile");
 };
 
-__device__ __forceinline__ int swz64(int r) { return (4 - ((r >> 2) & 3)) & 3; }
+__device__ __forceinline__ int swz128(int r) { return (r >> 1) & 7; }
 
 struct FwdJob {
   int e, m0, rows, n0;
@@ -213,13 +219,12 @@ __device__ __forceinline__ f32x4 mma(u32x4 b, u32x4 a, f32x4 c) {
 template <int L>
 __device__ __forceinline__ void stage_barrier(int n) {
   asm volatile("" ::: "memory");
-  if (n == 2 * L) wait_vm<2 * L>();
+  if (n == L) wait_vm<L>();
   else if (n >= 56) wait_vm<56>();
   else if (n >= 40) wait_vm<40>();
   else if (n >= 32) wait_vm<32>();
   else if (n >= 24) wait_vm<24>();
   else if (n >= 16) wait_vm<16>();
-  else if (n >= 2 * L) wait_vm<2 * L>();
   else if (n >= L) wait_vm<L>();
   else wait_vm<0>();
   __builtin_amdgcn_s_barrier();
@@ -238,7 +243,7 @@ __device__ __forceinline__ void stage_barrier(int n) {
 // their number, which the function returns, is known to the waits.
 //
 // fp32 lanes hold 16 bytes of a row and store them directly (not counted: 0).
-constexpr int kStoreBytes = 3072;
+constexpr int kStoreBytes = 2048;
 
 // 16 rows of FO * 16 bf16 columns from the MFMA layout (v: four columns a
 // fragment) to granules: lane l then holds granule l % (2 FO) of rows
@@ -246,6 +251,7 @@ constexpr int kStoreBytes = 3072;
 template <int FO>
 struct Piece {
   static constexpr int GR = 2 * FO, NQ = FO > 1 ? FO / 2 : 1, STEP = 64 / GR;
+  static_assert(16 * GR * 16 <= kStoreBytes, "the piece of LDS holds 16 rows");
   __device__ __forceinline__ static int row(int l, int q) { return (l / GR + q * STEP) & 15; }
   __device__ __forceinline__ static void pass(char* buf, int l, const u32x2 (&v)[FO], u32x4 (&out)[NQ]) {
     const int lrow = l & 15, lq = l >> 4;
@@ -379,10 +385,14 @@ __device__ __forceinline__ int fwd_store(const FwdGemmArgs& g, const FwdJob& job
             wave_sync();
             const bool inl = r0 + r < job.rows && cl < g.n && l < 16 * FO;
             char* d = (char*)g.Ylo + (int64_t)prow[r0 + r] * g.n + cl;
-            // (n is a multiple of 8: so are the bytes' addresses)
-            *reinterpret_cast<u32x2*>(inl ? d : dump) = u32x2{lo[0], lo[1]};
-            *reinterpret_cast<u32x2*>(inl && cl + 8 < g.n ? d + 8 : dump) = u32x2{lo[2], lo[3]};
-            stores += 2;
+            if (g.n % 16 == 0) {
+              *reinterpret_cast<u32x4*>(inl ? d : dump) = lo;
+              ++stores;
+            } else {  // n is a multiple of 8: so are the bytes' addresses
+              *reinterpret_cast<u32x2*>(inl ? d : dump) = u32x2{lo[0], lo[1]};
+              *reinterpret_cast<u32x2*>(inl && cl + 8 < g.n ? d + 8 : dump) = u32x2{lo[2], lo[3]};
+              stores += 2;
+            }
           }
         }
       }
@@ -391,36 +401,42 @@ __device__ __forceinline__ int fwd_store(const FwdGemmArgs& g, const FwdJob& job
   return stores;
 }
 
-// The operand fragments of a stage (32 k in bf16): 16 bytes per lane each.
+// The operand fragments of a stage, 16 bytes per lane each: k half h (32 k in
+// bf16) of the wave's columns (b) and of the upper and the lower half of its
+// rows (a[0], a[1]).
 template <class C>
 struct Frags {
-  u32x4 a[C::FM], b[C::FN];
-  // ao, bo: the lane's offsets of fragment 0 (the swizzle is the same 16 rows on)
-  __device__ __forceinline__ void read(const char* stage, int ao, int bo) {
+  static constexpr int HM = C::FM / 2;
+  u32x4 a[2][2][HM], b[2][C::FN];
+  // o: the lane's offset of fragment 0 in k half 0 (the swizzle is the same 16
+  // rows on, and the other half of k 4 granules off)
+  __device__ __forceinline__ void read_a(const char* stage, int o, int half, int h) {
 #pragma unroll
-    for (int j = 0; j < C::FN; ++j) b[j] = *reinterpret_cast<const u32x4*>(stage + C::SA + bo + j * 1024);
-#pragma unroll
-    for (int i = 0; i < C::FM; ++i) a[i] = *reinterpret_cast<const u32x4*>(stage + ao + i * 1024);
+    for (int i = 0; i < HM; ++i)
+      a[half][h][i] = *reinterpret_cast<const u32x4*>(stage + (o ^ h * 64) + (half * HM + i) * 2048);
   }
-  // rows [I0, I1) of the fragments
-  template <bool BF16, int I0, int I1>
-  __device__ __forceinline__ void multiply(f32x4 (&acc)[C::FM][C::FN]) const {
+  __device__ __forceinline__ void read_b(const char* stage, int o, int h) {
 #pragma unroll
-    for (int i = I0; i < I1; ++i)
+    for (int j = 0; j < C::FN; ++j)
+      b[h][j] = *reinterpret_cast<const u32x4*>(stage + C::SA + (o ^ h * 64) + j * 2048);
+  }
+  template <bool BF16>
+  __device__ __forceinline__ void multiply(f32x4 (&acc)[C::FM][C::FN], int half, int h) const {
 #pragma unroll
-      for (int j = 0; j < C::FN; ++j) acc[i][j] = mma<BF16>(b[j], a[i], acc[i][j]);
+    for (int i = 0; i < HM; ++i)
+#pragma unroll
+      for (int j = 0; j < C::FN; ++j)
+        acc[half * HM + i][j] = mma<BF16>(b[h][j], a[half][h][i], acc[half * HM + i][j]);
   }
 };
 
-// The next k-tile's LDS reads spread over the first half of this one's products.
-template <class C, bool BF16>
+// LDS reads one by one between the products that run meanwhile.
+template <int READS, bool BF16>
 __device__ __forceinline__ void interleave() {
-  constexpr int reads = C::FM + C::FN, mmas = C::FM / 2 * C::FN * (BF16 ? 1 : 4);
-  constexpr int per = mmas / reads > 0 ? mmas / reads : 1;
 #pragma unroll
-  for (int q = 0; q < reads; ++q) {
-    __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);    // an LDS read
-    __builtin_amdgcn_sched_group_barrier(0x008, per, 0);  // MFMAs
+  for (int q = 0; q < READS; ++q) {
+    __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);           // an LDS read
+    __builtin_amdgcn_sched_group_barrier(0x008, BF16 ? 1 : 4, 0);  // MFMAs
   }
 }
 
@@ -430,15 +446,14 @@ struct FwdFeed {
   FwdJob job;
   int k;
   dma_rsrc a, w0, w1;  // the operands' rows from k = 0, to their ends
-  int off[C::QA];
+  int off[2][C::QA];
 };
 
 template <class C, bool BF16, bool GLU, bool EPI>
 __global__ __launch_bounds__(C::NT, 2) void k_fwd_tile(FwdGemmArgs g) {
-  constexpr int ES = BF16 ? 2 : 4, KT = 64 / ES;  // k per stage
+  constexpr int ES = BF16 ? 2 : 4, KT = 128 / ES;  // k per stage
   constexpr int BNO = GLU ? C::BN / 2 : C::BN;    // output columns of a tile
   constexpr int HN = C::TN / 2;                   // GLU: a wave's columns of each product
-  constexpr int L = C::QA + C::QB;                // loads of a stage, per wave
   __shared__ __attribute__((aligned(1024))) char lds[kStages * C::SS];
   __shared__ __attribute__((aligned(16))) char sbuf[BF16 ? C::NW * kStoreBytes : 16];
   __shared__ __attribute__((aligned(16))) int prow[4][C::BM];  // pair of every row, by tile
@@ -451,24 +466,30 @@ __global__ __launch_bounds__(C::NT, 2) void k_fwd_tile(FwdGemmArgs g) {
   if (t >= tend) return;
   const int w = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6)), l = lane_id();
   const int wm = w / C::WGN, wn = w % C::WGN;
-  // k-tiles of a tile, zeros past K: an even number, and at least six, so that
-  // the feed is never more than one tile ahead and the rows of the next tile,
-  // asked for when the feed enters this one, are there when it leaves it
-  const int nk = max(((g.K + KT - 1) / KT + 1) & ~1, 6);
+  // stages of a tile, zeros past K: three at least, so that the feed is never
+  // more than one tile ahead and the rows of the next tile, asked for when the
+  // feed enters this one, are there when it leaves it
+  const int nk = max((g.K + KT - 1) / KT, 3);
   const int64_t kb = (int64_t)g.K * ES;  // bytes of a weight row
 
-  // this lane's place in the 1 KB blocks (16 rows) that its wave loads
-  const int lr = l >> 2, gran = ((l & 3) ^ swz64(lr)) * 16;
+  // this lane's place in the 1 KB blocks (8 rows) that its wave loads
+  const int lr = l >> 3;
+  auto gran = [&](int r) { return ((l & 7) ^ swz128(r)) * 16; };
+  auto arow = [&](int half, int q) {  // the upper or lower half of every wave's rows
+    const int r = (w * C::QA + q) * 8, in = r % (C::TM / 2);
+    return r / (C::TM / 2) * C::TM + half * (C::TM / 2) + in;
+  };
+  auto brow = [&](int q) { return (w * C::QB + q) * 8; };
   int boff[C::QB];
 #pragma unroll
   for (int q = 0; q < C::QB; ++q) {
-    const int r = (w * C::QB + q) * 16 + lr, in = r % C::TN;
+    const int r = brow(q) + lr, in = r % C::TN;
     const int col = GLU ? (r / C::TN) * HN + in % HN : r;
-    boff[q] = (int)(col * kb) + gran;
+    boff[q] = (int)(col * kb) + gran(r);
   }
   // and in the fragments that it multiplies
-  const int fr = l & 15, fo = fr * 64 + (((l >> 4) ^ swz64(fr)) << 4);
-  const int ao = wm * C::TM * 64 + fo, bo = wn * C::TN * 64 + fo;
+  const int fr = l & 15, fo = fr * 128 + (((l >> 4) ^ swz128(fr)) << 4);
+  const int ao = wm * C::TM * 128 + fo, bo = wn * C::TN * 128 + fo;
 
   int vm = 0;  // memory instructions of this wave so far
   FwdFeed<C> f;
@@ -497,11 +518,13 @@ __global__ __launch_bounds__(C::NT, 2) void k_fwd_tile(FwdGemmArgs g) {
     f.w0 = uniform(make_dma_rsrc((const char*)g.W0 + wat, wleft));
     if constexpr (GLU) f.w1 = uniform(make_dma_rsrc((const char*)g.W1 + wat, wleft));
 #pragma unroll
-    for (int q = 0; q < C::QA; ++q) {
-      const int r = (w * C::QA + q) * 16 + lr;
-      const int row = g.gather ? xrow[entered & 1][r] : r;
-      f.off[q] = r < next.rows ? row * (int)(g.ldx * ES) + gran : kOobOff;
-    }
+    for (int half = 0; half < 2; ++half)
+#pragma unroll
+      for (int q = 0; q < C::QA; ++q) {
+        const int r = arow(half, q) + lr;
+        const int row = g.gather ? xrow[entered & 1][r] : r;
+        f.off[half][q] = r < next.rows ? row * (int)(g.ldx * ES) + gran(r) : kOobOff;
+      }
     t += nb;
     more = t < tend;
     if (more) {
@@ -510,29 +533,35 @@ __global__ __launch_bounds__(C::NT, 2) void k_fwd_tile(FwdGemmArgs g) {
     }
   };
   bool fed = false;  // the feed is past the last tile
-  auto feed = [&](int s) {  // stage s <- the feed's k-tile
+  // stage s <- the feed's k-tile, B and the first half of A or the second half
+  auto feed = [&](int s, auto second) {
     if (fed) return;
     char* base = lds + s * C::SS;
-    const int at = f.k * 64, left = (int)kb - at;  // bytes of a row before and from this k-tile
+    const int at = f.k * 128, left = (int)kb - at;  // bytes of a row before and from this k-tile
     auto load = [&](auto tail) {
-      const bool out = tail && gran >= left;  // past K
+      constexpr int half = second;
 #pragma unroll
-      for (int q = 0; q < C::QA; ++q)
-        dma16(f.a, reinterpret_cast<uint16_t*>(base + (w * C::QA + q) * 1024),
-              out ? kOobOff : f.off[q], at);
+      for (int q = 0; q < C::QA; ++q) {
+        const int r = arow(half, q);
+        dma16(f.a, reinterpret_cast<uint16_t*>(base + r * 128),
+              tail && gran(r + lr) >= left ? kOobOff : f.off[half][q], at);
+      }
+      if constexpr (!half) {
 #pragma unroll
-      for (int q = 0; q < C::QB; ++q) {
-        const bool up = GLU && (w * C::QB + q) * 16 % C::TN >= HN;
-        dma16(up ? f.w1 : f.w0, reinterpret_cast<uint16_t*>(base + C::SA + (w * C::QB + q) * 1024),
-              out ? kOobOff : boff[q], at);
+        for (int q = 0; q < C::QB; ++q) {
+          const int r = brow(q);
+          const bool up = GLU && r % C::TN >= HN;
+          dma16(up ? f.w1 : f.w0, reinterpret_cast<uint16_t*>(base + C::SA + r * 128),
+                tail && gran(r + lr) >= left ? kOobOff : boff[q], at);
+        }
       }
     };
-    if (left >= 64)
+    if (left >= 128)
       load(std::false_type());
     else
       load(std::true_type());
-    vm += L;
-    if (++f.k == nk) {
+    vm += second ? C::QA : C::QA + C::QB;
+    if (second && ++f.k == nk) {
       fed = !more;
       if (more) enter();
     }
@@ -540,19 +569,30 @@ __global__ __launch_bounds__(C::NT, 2) void k_fwd_tile(FwdGemmArgs g) {
 
   next = fwd_job(g, t, nc, find_expert(g.mt_off, g.E, t / nc), C::BM, BNO);
   look();
-  stage_barrier<L>(0);
+  stage_barrier<C::L>(0);
   cur = next;
   enter();
-  // mk[s]: vm just after the loads of the s-th oldest k-tile in flight
-  int mk[kStages];
-#pragma unroll
-  for (int s = 0; s < kStages; ++s) {
-    feed(s);
-    mk[s] = vm;
-  }
-  stage_barrier<L>(vm - mk[0]);
-  Frags<C> f0, f1;
-  f0.read(lds, ao, bo);
+  std::false_type first;
+  std::true_type second;
+  // mk[i]: vm just after the loads of the i-th oldest half stage in flight
+  int mk[3];
+  feed(0, first);
+  const int m0 = vm;
+  feed(0, second);
+  mk[0] = vm;
+  feed(1, first);
+  mk[1] = vm;
+  feed(1, second);
+  mk[2] = vm;
+  auto shift = [&]() {
+    mk[0] = mk[1];
+    mk[1] = mk[2];
+    mk[2] = vm;
+  };
+  stage_barrier<C::L>(vm - m0);
+  Frags<C> f01;
+  f01.read_a(lds, ao, 0, 0);
+  f01.read_b(lds, bo, 0);
   int st = 0;
   for (int done = 0;; ++done) {
     f32x4 acc[C::FM][C::FN];
@@ -560,27 +600,37 @@ __global__ __launch_bounds__(C::NT, 2) void k_fwd_tile(FwdGemmArgs g) {
     for (int i = 0; i < C::FM; ++i)
 #pragma unroll
       for (int j = 0; j < C::FN; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
-    // A wave enters with the k-tile's fragments read (or on their way).  Past
-    // the barrier every wave has them, so the stage takes the k-tile four on,
-    // and the next k-tile's loads have arrived.
-    auto step = [&](const Frags<C>& now, Frags<C>& then) {
-      stage_barrier<L>(vm - mk[1]);
-      const int free = st;
-      st = (st + 1) & (kStages - 1);
-      then.read(lds + st * C::SS, ao, bo);
-      now.template multiply<BF16, 0, C::FM / 2>(acc);
-      interleave<C, BF16>();
-      feed(free);
-#pragma unroll
-      for (int s = 0; s < kStages - 1; ++s) mk[s] = mk[s + 1];
-      mk[kStages - 1] = vm;
-      now.template multiply<BF16, C::FM / 2, C::FM>(acc);
-    };
-    for (int k = 0; k < nk; k += 2) {
-      step(f0, f1);
-      step(f1, f0);
+    // Four quarters, each reading what the next one multiplies.  A wave enters
+    // with the first one's fragments read (or on their way).
+    for (int k = 0; k < nk; ++k) {
+      const char* stage = lds + st * C::SS;
+      f01.read_a(stage, ao, 0, 1);
+      f01.read_b(stage, bo, 1);
+      f01.template multiply<BF16>(acc, 0, 0);
+      interleave<C::FM / 2 + C::FN, BF16>();
+      // every wave has B and the first half of A; the second half is there
+      stage_barrier<C::L>(vm - mk[0]);
+      f01.read_a(stage, ao, 1, 0);
+      feed(st, first);
+      shift();
+      f01.template multiply<BF16>(acc, 0, 1);
+      interleave<C::FM / 2, BF16>();
+      f01.read_a(stage, ao, 1, 1);
+      f01.template multiply<BF16>(acc, 1, 0);
+      interleave<C::FM / 2, BF16>();
+      // every wave has the second half; the next stage's B and first half are there
+      stage_barrier<C::L>(vm - mk[0]);
+      const char* behind = lds + (st ^ 1) * C::SS;
+      f01.read_a(behind, ao, 0, 0);
+      f01.read_b(behind, bo, 0);
+      feed(st, second);
+      shift();
+      f01.template multiply<BF16>(acc, 1, 1);
+      interleave<C::FM / 2 + C::FN, BF16>();
+      st ^= 1;
     }
-    vm += fwd_store<C, BF16, GLU, EPI>(g, cur, acc, sbuf + (BF16 ? w * kStoreBytes : 0), prow[done & 3], w, l);
+    vm += fwd_store<C, BF16, GLU, EPI>(g, cur, acc, sbuf + (BF16 ? w * kStoreBytes : 0), prow[done & 3], w,
+                                         l + opaque_uniform(0));
     if (done == entered) break;
     cur = f.job;
   }
@@ -618,7 +668,9 @@ __global__ __launch_bounds__(256) void k_fwd_sumsq(FwdGemmArgs g, double* out) {
   if (lane_id() == 0) out[g.kept[m]] = s;
 }
 
-// One wave per token and 512 (bf16) or 256 (fp32) columns.
+// One wave per token and 512 (bf16) or 256 (fp32) columns.  Bound by memory: 16384
+// tokens of 8 pairs, 2048 columns, take 186 us for 872 MB, the rate of a large
+// copy; asking for four pairs' rows at once changed nothing.
 template <bool BF16>
 __global__ __launch_bounds__(256) void k_fwd_join(FwdJoinArgs a) {
   constexpr int V = BF16 ? 8 : 4, COLS = V * kWave;
@@ -696,11 +748,11 @@ int fwd_tile_forced() {
   return v == 64 || v == 128 || v == 256 ? v : 0;
 }
 
-// Rows of a tile: by the rows of an average expert.  bf16 (Qwen3-shaped layer,
-// 128 experts): 128 rows an expert 410 us with tiles of 128 and 439 with 256,
-// 256 rows 657 and 571; 64 rows 338 with 128 and 365 with 64.  fp32 (1024 x 1408,
-// 8 experts): 64 rows an expert 66 us with tiles of 64 and 101 with 128, 1024
-// rows 239 and 247, 2048 rows 517 and 480.
+// Rows of a tile: by the rows of an average expert.  bf16 (both products of a
+// Qwen3-shaped layer, 128 experts): 128 rows an expert 350 us with tiles of 128
+// and 377 with 256, 187 rows 420 and 417, 256 rows 560 and 502.  fp32 (1024 x
+// 1408, 8 experts): 128 rows an expert 55 us with tiles of 64 and 93 with 128,
+// 1024 rows 247 and 256, 2048 rows 469 and 453.
 int fwd_tile_rows(const FwdGemmArgs& g) {
   if (const int v = fwd_tile_forced()) return v;
   const int avg = g.N / g.E;
