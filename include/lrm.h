@@ -612,7 +612,7 @@ typedef struct lrm_forward {
 } lrm_forward;
 
 /* Outputs, device, dense, of the inputs' dtype (h_sumsq fp64); NULL: not
- * wanted, at least one is.  Rows of pairs that are absent (index out of range)
+ * wanted, at least one is unless N is 0.  Rows of pairs that are absent (index out of range)
  * are left as they were in the PAIR outputs and add nothing to Y. */
 typedef struct lrm_forward_outputs {
   void* Y;         /* [T][d_out] (SWIGLU: [T][H]); may be R itself when R.ld is its columns */
@@ -645,7 +645,7 @@ typedef struct lrm_pair_grad_problem {
   lrm_mat Z;     /* PAIR, d cols, d 1..2^20-1 */
 } lrm_pair_grad_problem;
 
-/* Outputs, device, NULL: not wanted, at least one is.  Absent pairs (index out
+/* Outputs, device, NULL: not wanted, at least one is unless N is 0.  Absent pairs (index out
  * of range) get 0 in dweight and G and add nothing to dbias; their Z rows are
  * not used. */
 typedef struct lrm_pair_grad_outputs {

@@ -135,7 +135,8 @@ lrm_status check_forward(const lrm_forward* f, const lrm_forward_outputs* out) {
   if (out) {
     const bool glu = f->kind == LRM_SWIGLU;
     if (glu ? out->Z != nullptr : (out->A || out->B || out->h_sumsq)) return LRM_ERR_UNSUPPORTED;
-    if (!out->Y && !out->Yp && !out->Z && !out->A && !out->B && !out->h_sumsq)
+    // (outputs of no rows may be null)
+    if (p->N > 0 && !out->Y && !out->Yp && !out->Z && !out->A && !out->B && !out->h_sumsq)
       return LRM_ERR_NULL;
     if (f->R.ptr && !out->Y) return LRM_ERR_UNSUPPORTED;
     if (!aligned16(out->Y) || !aligned16(out->Yp) || !aligned16(out->Z) || !aligned16(out->A) ||
@@ -289,7 +290,7 @@ lrm_status check_pair_grad(const lrm_pair_grad_problem* g, const lrm_pair_grad_o
   LRM_TRY(check_mat(&g->Z, &g->pairs, g->dtype, -1, LRM_ROWS_PAIR));
   LRM_TRY(check_mat(&g->dY, &g->pairs, g->dtype, g->Z.cols, -1));
   if (out) {
-    if (!out->dweight && !out->G && !out->dbias) return LRM_ERR_NULL;
+    if (g->pairs.N > 0 && !out->dweight && !out->G && !out->dbias) return LRM_ERR_NULL;
     if (!aligned4(out->dweight) || !aligned16(out->G) || !aligned4(out->dbias))
       return LRM_ERR_ALIGN;
   }

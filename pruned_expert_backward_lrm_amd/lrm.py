@@ -481,6 +481,7 @@ class Router:
                 raise ValueError(f"{name} must be a contiguous {dts[0]} tensor of {n} entries "
                                  "on the logits' device")
         self.T, self.E, self.k = int(T), int(E), int(k)
+        self.device = logits.device
         self.keep = [logits, bias, expert_mask, token_mask]
         ld = logits.stride(0) if T > 1 else max(logits.stride(0), E)
         self.c = lrm_router(self.T, self.E, self.k, SCORES[score],
@@ -490,20 +491,22 @@ class Router:
         self.ws_bytes = int(_lib.lrm_route_workspace_size(C.byref(self.c)))
 
 
-def _slots(name, t, n, dtype):
-    """A dense device array of at least n entries of a type, or None."""
-    if t is not None and (t.dtype != dtype or t.numel() < n or not t.is_contiguous()):
-        raise ValueError(f"{name} must be a contiguous {dtype} tensor of at least {n} entries")
+def _slots(name, t, n, dtype, device):
+    """A dense array of at least n entries of a type on a device, or None."""
+    if t is not None and (t.dtype != dtype or t.numel() < n or not t.is_contiguous()
+                          or t.device != device):
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor of at least {n} entries "
+                         f"on {device}")
 
 
 def lrm_route(r: Router, expert, weight, token=None, counts=None, ws=None, stream=None):
     """The k experts of every token (int32 [T*k], -1 in empty slots) and their
     weights (fp32 [T*k]); optionally the slots' tokens and the experts' counts."""
-    n = r.T * r.k
-    _slots("expert", expert, n, torch.int32)
-    _slots("weight", weight, n, torch.float32)
-    _slots("token", token, n, torch.int32)
-    _slots("counts", counts, r.E, torch.int32)
+    n, on = r.T * r.k, r.device
+    _slots("expert", expert, n, torch.int32, on)
+    _slots("weight", weight, n, torch.float32, on)
+    _slots("token", token, n, torch.int32, on)
+    _slots("counts", counts, r.E, torch.int32, on)
     if counts is not None:
         ws = _ws(r.ws_bytes, counts.device, ws)
     _check(_lib.lrm_route(C.byref(r.c), _ptr(expert), _ptr(weight), _ptr(token), _ptr(counts),
@@ -515,11 +518,12 @@ def lrm_route_bwd(r: Router, expert, dweight, dlogits: torch.Tensor, stream=None
     """Gradient of the logits (their dtype, [T][E]) from the gradient of the
     weights (fp32 [T*k]) of a choice (int32 [T*k])."""
     n = r.T * r.k
-    _slots("expert", expert, n, torch.int32)
-    _slots("dweight", dweight, n, torch.float32)
+    _slots("expert", expert, n, torch.int32, r.device)
+    _slots("dweight", dweight, n, torch.float32, r.device)
     if dlogits.shape != (r.T, r.E) or (r.E > 1 and dlogits.stride(1) != 1) or \
-            dtype_code(dlogits) != r.c.dtype:
-        raise ValueError("dlogits must be [T][E] of the logits' dtype with unit column stride")
+            dtype_code(dlogits) != r.c.dtype or dlogits.device != r.device:
+        raise ValueError("dlogits must be [T][E] of the logits' dtype with unit column stride "
+                         "on the logits' device")
     ldd = dlogits.stride(0) if r.T > 1 else max(dlogits.stride(0), r.E)
     _check(_lib.lrm_route_bwd(C.byref(r.c), _ptr(expert), _ptr(dweight), _ptr(dlogits), ldd,
                               _stream(stream)), "lrm_route_bwd")
@@ -535,7 +539,7 @@ def lrm_route_share(T: int, k: int, expert, weight, e0: int, E: int, out_token, 
                            ("out_expert", out_expert, n, torch.int32),
                            ("out_weight", out_weight, n, torch.float32),
                            ("out_slot", out_slot, n, torch.int32), ("out_n", out_n, 1, torch.int32)):
-        _slots(name, t, m, dt)
+        _slots(name, t, m, dt, out_n.device)
     ws = _ws(_lib.lrm_route_share_workspace_size(int(T), int(k)), out_n.device, ws)
     _check(_lib.lrm_route_share(int(T), int(k), _ptr(expert), _ptr(weight), int(e0), int(E),
                                 _ptr(out_token), _ptr(out_expert), _ptr(out_weight),
@@ -548,6 +552,8 @@ class Forward:
     """An lrm_forward plus the objects that keep its memory alive."""
 
     def __init__(self, kind: int, pairs: Pairs, X, x_rows, residual, act: str = "none"):
+        _rows("X", X, x_rows, pairs)
+        _rows("residual", residual, "token", pairs)
         self.pairs = pairs
         self.keep = [pairs, X, residual]
         self.c = lrm_forward()
@@ -556,7 +562,18 @@ class Forward:
         self.c.R = mat(residual, "token")
 
 
-def _dense(name, t, shape, dtype):
+def _rows(name, t, rows, pairs):
+    """A row of t for every token or pair, on the pairs' device."""
+    if t is None:
+        return
+    need = pairs.T if rows in ("token", ROWS["token"]) else pairs.N
+    if t.shape[0] < need or t.device != pairs.token.device:
+        raise ValueError(f"{name} must have at least {need} rows on the pairs' device")
+
+
+def _dense(name, t, shape, dtype, device):
+    if t.device != device:
+        raise ValueError(f"{name} must be on the pairs' device")
     if tuple(t.shape) != tuple(shape) or t.dtype != dtype or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)}")
 
@@ -564,16 +581,20 @@ def _dense(name, t, shape, dtype):
 def linear_forward(pairs: Pairs, X, x_rows, W, act="none", bias=None, residual=None) -> Forward:
     """y_p = act(W_e x_p + bias_e) with W [E][d_out][d_in], bias [E][d_out]."""
     if W.dim() != 3 or W.shape[0] != pairs.E or W.dtype != X.dtype or W.stride(2) != 1 or \
-            W.stride(1) != W.shape[2] or W.shape[2] != X.shape[1]:
-        raise ValueError("W must be [E][d_out][d_in] of X's dtype, dense inside an expert")
+            W.stride(1) != W.shape[2] or W.shape[2] != X.shape[1] or \
+            W.device != pairs.token.device:
+        raise ValueError("W must be [E][d_out][d_in] of X's dtype, dense inside an expert, "
+                         "on the pairs' device")
     if bias is not None:
-        _dense("bias", bias, W.shape[:2], X.dtype)
+        _dense("bias", bias, W.shape[:2], X.dtype, pairs.token.device)
     f = Forward(LRM_LINEAR, pairs, X, x_rows, residual, act)
     f.keep += [W, bias]
     c = f.c
     c.W, c.w_stride = _ptr(W), max(W.stride(0), W.shape[1] * W.shape[2])
     c.bias = _ptr(bias)
     c.d_in, c.d_out = W.shape[2], W.shape[1]
+    f.sizes = {"Y": (X.dtype, pairs.T * c.d_out), "Yp": (X.dtype, pairs.N * c.d_out),
+               "Z": (X.dtype, pairs.N * c.d_out)}
     return f
 
 
@@ -582,12 +603,15 @@ def swiglu_forward(pairs: Pairs, X, W_gate, W_up, W_down, residual=None) -> Forw
     H, I = X.shape[1], W_gate.shape[1]  # noqa: E741
     for name, w, shape in (("W_gate", W_gate, (pairs.E, I, H)), ("W_up", W_up, (pairs.E, I, H)),
                            ("W_down", W_down, (pairs.E, H, I))):
-        _dense(name, w, shape, X.dtype)
+        _dense(name, w, shape, X.dtype, pairs.token.device)
     f = Forward(LRM_SWIGLU, pairs, X, "token", residual)
     f.keep += [W_gate, W_up, W_down]
     c = f.c
     c.W_gate, c.W_up, c.W_down = _ptr(W_gate), _ptr(W_up), _ptr(W_down)
     c.H, c.I = H, I
+    f.sizes = {"Y": (X.dtype, pairs.T * H), "Yp": (X.dtype, pairs.N * H),
+               "A": (X.dtype, pairs.N * I), "B": (X.dtype, pairs.N * I),
+               "h_sumsq": (torch.float64, pairs.N)}
     return f
 
 
@@ -597,12 +621,26 @@ def lrm_forward_workspace_size(f: Forward) -> int:
 
 def _marshal(struct, outputs: dict):
     o = struct()
+    o._fits = None  # the problem whose sizes were checked last
     o._tensors = dict(outputs)  # the descriptor keeps its memory alive
     for k, v in outputs.items():
         if v is not None and not v.is_contiguous():
             raise ValueError(f"output {k} must be contiguous")
         setattr(o, k, _ptr(v))
     return o
+
+
+def _check_outputs(o, problem):
+    """The outputs have the problem's types, sizes and device."""
+    if o._fits is problem:
+        return
+    for k, t in o._tensors.items():
+        if t is None or k not in problem.sizes:  # (the call refuses what its kind does not have)
+            continue
+        dtype, n = problem.sizes[k]
+        if t.dtype != dtype or t.numel() != n or t.device != problem.pairs.token.device:
+            raise ValueError(f"output {k} must be {n} elements of {dtype} on the pairs' device")
+    o._fits = problem
 
 
 def forward_outputs(outputs: dict) -> lrm_forward_outputs:
@@ -622,6 +660,7 @@ def _grown(ws, need, device):
 def lrm_expert_forward(f: Forward, outputs, ws=None, stream=None):
     """The experts' forward pass; outputs: a dict or forward_outputs(dict)."""
     o = forward_outputs(outputs) if isinstance(outputs, dict) else outputs
+    _check_outputs(o, f)
     if ws is None:
         ws = _grown(ws, lrm_forward_workspace_size(f), f.pairs.token.device)
     _check(_lib.lrm_expert_forward(C.byref(f.c), C.byref(o), _ptr(ws),
@@ -635,8 +674,13 @@ class PairGrad:
     """An lrm_pair_grad_problem plus the objects that keep its memory alive."""
 
     def __init__(self, pairs: Pairs, dY, dy_rows, Z, act: str):
+        _rows("dY", dY, dy_rows, pairs)
+        _rows("Z", Z, "pair", pairs)
         self.pairs = pairs
         self.keep = [pairs, dY, Z]
+        d = Z.shape[1]
+        self.sizes = {"dweight": (torch.float32, pairs.N), "G": (Z.dtype, pairs.N * d),
+                      "dbias": (torch.float32, pairs.E * d)}
         self.c = lrm_pair_grad_problem(ACTS[act], dtype_code(Z), pairs.c, mat(dY, dy_rows),
                                        mat(Z, "pair"))
 
@@ -658,6 +702,7 @@ def lrm_pair_grad(g: PairGrad, outputs, ws=None, stream=None):
     """Gradients of the routing weights, the projection's output and the bias;
     outputs: a dict or pair_grad_outputs(dict)."""
     o = pair_grad_outputs(outputs) if isinstance(outputs, dict) else outputs
+    _check_outputs(o, g)
     if ws is None:
         ws = _grown(ws, lrm_pair_grad_workspace_size(g), g.pairs.token.device)
     _check(_lib.lrm_pair_grad(C.byref(g.c), C.byref(o), _ptr(ws),

@@ -176,7 +176,7 @@ def judge_route_bwd(c, e, dw, dlogits):
 def _f(kind, T, E, k, d_in, d, dtype="bf16", **kw):
     c = dict(kind=kind, T=T, E=E, k=k, d_in=d_in, d=d, dtype=dtype, act="none", bias=False,
              residual=False, x_rows="token", drop=0.0, skew=0.0, empty=0.0, bad=False, ldx=0,
-             outs=None)
+             twice=False, outs=None)
     c.update(kw)
     return c
 
@@ -205,6 +205,10 @@ FORWARD_CASES = {
     "glu_y_only": _f("swiglu", 40, 5, 2, 72, 40, outs=("Y",), residual=True),
     "glu_bad": _f("swiglu", 40, 6, 2, 64, 40, bad=True),
     "glu_bad_t1": _f("swiglu", 2, 16, 4, 64, 40, bad=True, residual=True),
+    "lin_no_tokens": _f("linear", 0, 4, 2, 64, 64, residual=True, bias=True),
+    "glu_no_tokens": _f("swiglu", 0, 4, 2, 64, 40, residual=True),
+    "lin_twice": _f("linear", 40, 3, 3, 64, 72, twice=True, act="gelu", residual=True),
+    "glu_twice": _f("swiglu", 5, 8, 4, 64, 40, twice=True, residual=True),
 }
 
 
@@ -218,6 +222,8 @@ def build_forward(case, name):
     g = gen("fwd", name)
     c["pairs"] = p = make_pairs(T, E, c["k"], 5 + len(name), c["drop"], c["skew"], c["empty"])
     N = c["N"] = p["token"].size
+    if c["twice"]:  # every token names one expert twice
+        p["expert"][1::c["k"]] = p["expert"][0::c["k"]]
     if c["bad"] and N > 3:  # experts out of range: absent, reported
         p["expert"][1] = -1
         p["expert"][N // 2] = E

@@ -176,7 +176,7 @@ def emu_forward(driver, tmp_path, c, env_extra=None):
 
 
 SMALL_FORWARD = ["lin_one", "lin_one_f32", "lin_odd", "lin_none", "lin_bad", "glu_t1", "glu_t3",
-                 "glu_small", "glu_small_f32", "glu_pairs_only", "glu_bad_t1"]
+                 "glu_small", "glu_small_f32", "glu_pairs_only", "glu_bad_t1", "lin_no_tokens", "glu_no_tokens", "glu_twice"]
 
 
 @pytest.mark.parametrize("name", list(FC.FORWARD_CASES) if FULL else SMALL_FORWARD)
@@ -190,6 +190,11 @@ def test_emu_forward_tiles(driver, tmp_path, name, tile):
     """The larger tiles on cases small enough to emulate (one that packs its
     input first among them)."""
     emu_forward(driver, tmp_path, FC.forward_case(name), {"LRM_FWD_TILE": tile})
+
+
+@pytest.mark.parametrize("name", ["lin_none", "lin_no_tokens", "glu_no_tokens", "glu_twice"])
+def test_emu_forward_tiles_of_little(driver, tmp_path, name):
+    emu_forward(driver, tmp_path, FC.forward_case(name), {"LRM_FWD_TILE": "64"})
 
 
 @pytest.mark.parametrize("name", list(FC.PAIR_GRAD_CASES) if FULL else

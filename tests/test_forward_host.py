@@ -298,3 +298,44 @@ def test_binding_refuses_bad_tensors():
         L.linear_forward(pr, z, "token", torch.zeros(2, 8, 8), bias=torch.zeros(2, 7))
     with pytest.raises(ValueError):
         L.swiglu_forward(pr, z, torch.zeros(2, 4, 8), torch.zeros(2, 4, 8), torch.zeros(2, 4, 8))
+
+
+def test_binding_refuses_outputs_that_do_not_fit():
+    i, f = torch.zeros(8, dtype=torch.int32), torch.zeros(8)
+    pr = L.Pairs(i, i, f, 4, 2)
+    X, W = torch.zeros(4, 8), torch.zeros(2, 12, 8)
+    with pytest.raises(ValueError):
+        L.linear_forward(pr, X[:3], "token", W)
+    with pytest.raises(ValueError):
+        L.linear_forward(pr, X, "pair", W)
+    with pytest.raises(ValueError):
+        L.linear_forward(pr, X, "token", W, residual=torch.zeros(3, 12))
+    with pytest.raises(ValueError):
+        L.linear_forward(pr, X, "token", W.to("meta"))
+    lin = L.linear_forward(pr, X, "token", W)
+    for out in (dict(Y=torch.zeros(4, 11)), dict(Yp=torch.zeros(7, 12)),
+                dict(Y=torch.zeros(4, 12, dtype=torch.bfloat16)),
+                dict(Y=torch.zeros(4, 12), Z=torch.zeros(9, 12)),
+                dict(Y=torch.zeros(4, 12, device="meta"))):
+        with pytest.raises(ValueError):
+            L.lrm_expert_forward(lin, out)
+        with pytest.raises(ValueError):  # marshalled before
+            L.lrm_expert_forward(lin, L.forward_outputs(out))
+    glu = L.swiglu_forward(pr, X, torch.zeros(2, 4, 8), torch.zeros(2, 4, 8), torch.zeros(2, 8, 4))
+    for out in (dict(Y=torch.zeros(4, 4)), dict(A=torch.zeros(8, 8)), dict(h_sumsq=torch.zeros(8))):
+        with pytest.raises(ValueError):
+            L.lrm_expert_forward(glu, out)
+    with pytest.raises(ValueError):
+        L.pair_grad_problem(pr, X, "token", torch.zeros(7, 8))
+    with pytest.raises(ValueError):
+        L.pair_grad_problem(pr, X, "pair", torch.zeros(8, 8))
+    pg = L.pair_grad_problem(pr, X, "token", torch.zeros(8, 8))
+    for out in (dict(dweight=torch.zeros(7)), dict(G=torch.zeros(8, 4)), dict(dbias=torch.zeros(3, 8)),
+                dict(dweight=torch.zeros(8, dtype=torch.float64))):
+        with pytest.raises(ValueError):
+            L.lrm_pair_grad(pg, out)
+    r = L.Router(X, 2)
+    with pytest.raises(ValueError):
+        L.lrm_route(r, i.to("meta"), f)
+    with pytest.raises(ValueError):
+        L.lrm_route_bwd(r, i, f, torch.zeros(4, 8, device="meta"))

@@ -246,6 +246,15 @@ def test_forward_graph_replays(L):
                 assert torch.equal(got[k].view(torch.uint8), out[k].view(torch.uint8)), (name, k)
 
 
+@pytest.mark.parametrize("name", ["lin_none", "lin_no_tokens", "glu_no_tokens", "lin_twice",
+                                  "glu_twice"])
+def test_forward_tiles_of_little(L, monkeypatch, name):
+    monkeypatch.setenv("LRM_FWD_TILE", "64")
+    c = FC.forward_case(name)
+    out, before = run_forward(L, c)
+    FC.judge_forward(c, out, before)
+
+
 @pytest.mark.parametrize("name", list(FC.PAIR_GRAD_CASES))
 def test_pair_grad(L, name):
     c = FC.pair_grad_case(name)
@@ -361,3 +370,108 @@ def test_share_of_a_padded_batch_together(L):
     dref[torch.from_numpy(s2)] = ref_dw
     ref = OF.route_bwd(z, k, we, dref, token_mask=keep)
     assert float((dz.cpu().double() - ref).norm() / ref.norm()) < 1e-5
+
+
+def _bits(out):
+    return {k: v.clone().view(torch.uint8) for k, v in out.items()}
+
+
+def test_calls_of_a_layer_in_one_graph(L):
+    """Route, share, forward, both epilogue gradients and the routing gradient,
+    captured in one graph over one workspace: every replay, with the program's
+    own eager calls in the same workspace between, equals the eager calls."""
+    T, E, k, H, d = 130, 12, 3, 64, 72
+    g = FC.gen("graph")
+    i32, f32, bf = torch.int32, torch.float32, torch.bfloat16
+    n = T * k
+    z, X, dY = dev(FC.normal(g, T, E)), dev(FC.normal(g, T, H, dtype=bf)), \
+        dev(FC.normal(g, T, d, dtype=bf))
+    W, bias = dev(FC.normal(g, E, d, H, std=0.1, dtype=bf)), dev(FC.normal(g, E, d, dtype=bf))
+    out = dict(expert=filled((n,), i32), weight=filled((n,), f32), token=filled((n,), i32),
+               counts=filled((E,), i32), st=filled((n,), i32), se=filled((n,), i32),
+               sw=filled((n,), f32), ss=filled((n,), i32), sn=filled((1,), i32),
+               Y=filled((T, d), bf), Z=filled((n, d), bf), dweight=filled((n,), f32),
+               G=filled((n, d), bf), dbias=filled((E, d), f32), dz=filled((T, E), f32))
+    r = L.Router(z, k, score="sigmoid")
+    pairs = L.Pairs(out["token"], out["expert"], out["weight"], T, E)
+    f = L.linear_forward(pairs, X, "token", W, act="gelu", bias=bias)
+    pg = L.pair_grad_problem(pairs, dY, "token", out["Z"], act="gelu")
+    fo = L.forward_outputs(dict(Y=out["Y"], Z=out["Z"]))
+    po = L.pair_grad_outputs(dict(dweight=out["dweight"], G=out["G"], dbias=out["dbias"]))
+    ws = torch.empty(max(L.lrm_forward_workspace_size(f), L.lrm_pair_grad_workspace_size(pg), 1 << 16),
+                     dtype=torch.uint8, device=DEV)
+
+    def calls():
+        L.lrm_route(r, out["expert"], out["weight"], token=out["token"], counts=out["counts"], ws=ws)
+        L.lrm_route_share(T, k, out["expert"], out["weight"], 2, 6, out["st"], out["se"], out["sw"],
+                          out["sn"], out_slot=out["ss"], ws=ws)
+        L.lrm_expert_forward(f, fo, ws=ws)
+        L.lrm_pair_grad(pg, po, ws=ws)
+        L.lrm_route_bwd(r, out["expert"], out["dweight"], out["dz"])
+
+    calls()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        calls()
+    for step in range(4):
+        gs = FC.gen("graph", step)
+        z.copy_(FC.normal(gs, T, E))
+        X.copy_(FC.normal(gs, T, H).to(bf))
+        dY.copy_(FC.normal(gs, T, d).to(bf))
+        for v in out.values():
+            v.view(torch.uint8).fill_(0xCD)
+        graph.replay()
+        torch.cuda.synchronize()
+        got = _bits(out)
+        for v in out.values():
+            v.view(torch.uint8).fill_(0xCD)
+        calls()
+        torch.cuda.synchronize()
+        want = _bits(out)
+        for name in out:
+            assert torch.equal(got[name], want[name]), (step, name)
+        assert L.lrm_check_device_errors(ws) == L.LRM_OK
+
+
+def test_two_streams_at_once(L):
+    """Two calls on two streams, each with its own workspace and outputs."""
+    todo = []
+    for name in ("glu_mid", "lin_odd"):
+        c = FC.forward_case(name)
+        f = make_forward(L, c)
+        out = {k: filled(*v) for k, v in FC.forward_shapes(c).items()}
+        ws = torch.empty(L.lrm_forward_workspace_size(f), dtype=torch.uint8, device=DEV)
+        rc = FC.route_case("groups_top2")
+        r = make_router(L, rc)
+        ex, wt = filled((rc["T"] * rc["k"],), torch.int32), filled((rc["T"] * rc["k"],), torch.float32)
+        todo.append((c, f, out, ws, r, ex, wt, torch.cuda.Stream()))
+    torch.cuda.synchronize()
+    for _ in range(5):
+        for c, f, out, ws, r, ex, wt, s in todo:
+            L.lrm_expert_forward(f, out, ws=ws, stream=s)
+            L.lrm_route(r, ex, wt, stream=s)
+    torch.cuda.synchronize()
+    for c, f, out, ws, r, ex, wt, s in todo:
+        FC.judge_forward(c, out)
+        alone = {k: filled(*v) for k, v in FC.forward_shapes(c).items()}
+        ex1, wt1 = torch.empty_like(ex), torch.empty_like(wt)
+        L.lrm_expert_forward(f, alone)
+        L.lrm_route(r, ex1, wt1)
+        torch.cuda.synchronize()
+        for k in out:
+            assert torch.equal(out[k].view(torch.uint8), alone[k].view(torch.uint8)), k
+        assert torch.equal(ex, ex1) and torch.equal(wt, wt1)
+
+
+def test_pair_grad_without_tokens(L):
+    i32, f32, bf = torch.int32, torch.float32, torch.bfloat16
+    pairs = L.Pairs(filled((0,), i32), filled((0,), i32), filled((0,), f32), 0, 5)
+    out = dict(dweight=filled((0,), f32), G=filled((0, 72), bf), dbias=filled((5, 72), f32))
+    L.lrm_pair_grad(L.pair_grad_problem(pairs, filled((0, 72), bf), "token", filled((0, 72), bf),
+                                        act="gelu"), out)
+    torch.cuda.synchronize()
+    assert not out["dbias"].any()
+    L.lrm_pair_grad(L.pair_grad_problem(pairs, filled((0, 72), bf), "pair", filled((0, 72), bf)),
+                    dict(dweight=out["dweight"]))
+    torch.cuda.synchronize()
