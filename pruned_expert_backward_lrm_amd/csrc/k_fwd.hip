@@ -159,8 +159,11 @@ __device__ __forceinline__ void emit(const FwdGemmArgs& g, int e, int m, int p, 
 //
 // fp32 runs v_mfma_f32_16x16x4: a lane's 16-byte granule holds four k, and
 // step s multiplies the s-th of every lane.  Which k those are is the same for
-// both operands, so every k is met once.
-constexpr int kStages = 2;
+// both operands, so every k is met once.  Its sums restart every kRestart stages
+// (256 k) and are added up apart: the roundings of a long sum stay below those
+// of a library's split sums, for an addition in 64 products (bf16 inputs round
+// by far more).
+constexpr int kStages = 2, kRestart = 8;
 
 template <int BM_, int BN_, int WGM_, int WGN_>
 struct FwdCfg {
@@ -600,6 +603,7 @@ __global__ __launch_bounds__(C::NT, 2) void k_fwd_tile(FwdGemmArgs g) {
     for (int i = 0; i < C::FM; ++i)
 #pragma unroll
       for (int j = 0; j < C::FN; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
+    f32x4 total[BF16 ? 1 : C::FM][C::FN] = {};  // fp32: of the finished runs of stages
     // Four quarters, each reading what the next one multiplies.  A wave enters
     // with the first one's fragments read (or on their way).
     for (int k = 0; k < nk; ++k) {
@@ -628,6 +632,18 @@ __global__ __launch_bounds__(C::NT, 2) void k_fwd_tile(FwdGemmArgs g) {
       feed(st, second);
       shift();
       st ^= 1;
+      if constexpr (!BF16) {
+        if (k % kRestart == kRestart - 1 || k == nk - 1) {
+          const bool last = k == nk - 1;
+#pragma unroll
+          for (int i = 0; i < C::FM; ++i)
+#pragma unroll
+            for (int j = 0; j < C::FN; ++j) {
+              total[i][j] += acc[i][j];
+              acc[i][j] = last ? total[i][j] : f32x4{0.f, 0.f, 0.f, 0.f};
+            }
+        }
+      }
     }
     vm += fwd_store<C, BF16, GLU, EPI>(g, cur, acc, sbuf + (BF16 ? w * kStoreBytes : 0), prow[done & 3], w,
                                          l + opaque_uniform(0));
@@ -731,11 +747,14 @@ hipError_t launch_tiles(const FwdGemmArgs& g, hipStream_t s) {
 }
 
 template <template <bool> class C>
-hipError_t launch_cfg(const FwdGemmArgs& g, hipStream_t s) {
-  if (g.glu)
-    return g.bf16 ? launch_tiles<C<true>, true, true, false>(g, s)
-                  : launch_tiles<C<true>, false, true, false>(g, s);
-  if (!g.bf16) return launch_tiles<C<false>, false, false, true>(g, s);
+hipError_t launch_f32(const FwdGemmArgs& g, hipStream_t s) {
+  return g.glu ? launch_tiles<C<true>, false, true, false>(g, s)
+               : launch_tiles<C<false>, false, false, true>(g, s);
+}
+
+template <template <bool> class C>
+hipError_t launch_bf16(const FwdGemmArgs& g, hipStream_t s) {
+  if (g.glu) return launch_tiles<C<true>, true, true, false>(g, s);
   return g.bias || g.Z || g.act != kActNone ? launch_tiles<C<false>, true, false, true>(g, s)
                                             : launch_tiles<C<false>, true, false, false>(g, s);
 }
@@ -752,22 +771,24 @@ int fwd_tile_forced() {
 // Qwen3-shaped layer, 128 experts): 128 rows an expert 350 us with tiles of 128
 // and 377 with 256, 187 rows 420 and 417, 256 rows 560 and 502.  fp32 (1024 x
 // 1408, 8 experts): 128 rows an expert 55 us with tiles of 64 and 93 with 128,
-// 1024 rows 247 and 256, 2048 rows 469 and 453.
+// 1024 rows 251 and 250, 4096 rows 870 and 862.
 int fwd_tile_rows(const FwdGemmArgs& g) {
-  if (const int v = fwd_tile_forced()) return v;
-  const int avg = g.N / g.E;
-  if (!g.bf16) return avg >= 1536 ? 128 : 64;
+  const int v = fwd_tile_forced(), avg = g.N / g.E;
+  if (!g.bf16) return v ? (v < 128 ? v : 128) : avg >= 1536 ? 128 : 64;
+  if (v) return v;
   return avg >= 192 ? 256 : 128;
 }
 
 hipError_t launch_fwd_gemm(const FwdGemmArgs& g, hipStream_t s) {
   if (g.N <= 0) return hipSuccess;
   if (g.gather && g.x_bytes > kFwdGatherMax) return hipErrorInvalidValue;
-  switch (fwd_tile_rows(g)) {
-    case 256: return launch_cfg<FwdL>(g, s);
-    case 128: return launch_cfg<FwdM>(g, s);
+  const int rows = fwd_tile_rows(g);
+  if (!g.bf16) return rows == 128 ? launch_f32<FwdM>(g, s) : launch_f32<FwdS>(g, s);
+  switch (rows) {
+    case 256: return launch_bf16<FwdL>(g, s);
+    case 128: return launch_bf16<FwdM>(g, s);
   }
-  return launch_cfg<FwdS>(g, s);
+  return launch_bf16<FwdS>(g, s);
 }
 
 hipError_t launch_fwd_pack(const FwdGemmArgs& g, void* out, hipStream_t s) {
