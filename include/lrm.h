@@ -59,8 +59,8 @@
  *     results); LRM_FUSE_GATE_UP=0 runs the SwiGLU gate and up weight
  *     gradients as two launches where one would compute both (bit-identical
  *     results under the same tile configuration); LRM_FWD_TILE=64|128|256
- *     forces the row tile of the forward products (fp32: 128 at most).  Workspace sizes do not
- *     depend on them.
+ *     forces the row tile of the forward products (bf16: 128 at least, fp32:
+ *     128 at most).  Workspace sizes do not depend on them.
  */
 #ifndef LRM_H_
 #define LRM_H_

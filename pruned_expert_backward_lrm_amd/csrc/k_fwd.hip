@@ -769,13 +769,14 @@ int fwd_tile_forced() {
 
 // Rows of a tile: by the rows of an average expert.  bf16 (both products of a
 // Qwen3-shaped layer, 128 experts): 128 rows an expert 350 us with tiles of 128
-// and 377 with 256, 187 rows 420 and 417, 256 rows 560 and 502.  fp32 (1024 x
+// and 377 with 256, 187 rows 420 and 417, 256 rows 560 and 502 (tiles of 64 are
+// within 3 % of 128 from 1 to 32 rows an expert: there are none).  fp32 (1024 x
 // 1408, 8 experts): 128 rows an expert 55 us with tiles of 64 and 93 with 128,
 // 1024 rows 251 and 250, 4096 rows 870 and 862.
 int fwd_tile_rows(const FwdGemmArgs& g) {
   const int v = fwd_tile_forced(), avg = g.N / g.E;
   if (!g.bf16) return v ? (v < 128 ? v : 128) : avg >= 1536 ? 128 : 64;
-  if (v) return v;
+  if (v) return v < 128 ? 128 : v;
   return avg >= 192 ? 256 : 128;
 }
 
@@ -784,11 +785,7 @@ hipError_t launch_fwd_gemm(const FwdGemmArgs& g, hipStream_t s) {
   if (g.gather && g.x_bytes > kFwdGatherMax) return hipErrorInvalidValue;
   const int rows = fwd_tile_rows(g);
   if (!g.bf16) return rows == 128 ? launch_f32<FwdM>(g, s) : launch_f32<FwdS>(g, s);
-  switch (rows) {
-    case 256: return launch_bf16<FwdL>(g, s);
-    case 128: return launch_bf16<FwdM>(g, s);
-  }
-  return launch_bf16<FwdS>(g, s);
+  return rows == 256 ? launch_bf16<FwdL>(g, s) : launch_bf16<FwdM>(g, s);
 }
 
 hipError_t launch_fwd_pack(const FwdGemmArgs& g, void* out, hipStream_t s) {

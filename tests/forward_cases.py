@@ -207,6 +207,8 @@ FORWARD_CASES = {
     "glu_bad_t1": _f("swiglu", 2, 16, 4, 64, 40, bad=True, residual=True),
     "lin_many": _f("linear", 4500, 7, 2, 16, 24, skew=0.5, drop=0.02, empty=0.05, bad=True),
     "lin_one_block": _f("linear", 4096, 9, 2, 16, 24, skew=0.5, bad=True),
+    "lin_512_experts": _f("linear", 700, 512, 3, 16, 24, skew=0.3, bad=True),
+    "lin_513_experts": _f("linear", 700, 513, 3, 16, 24, skew=0.3, bad=True),
     "lin_no_tokens": _f("linear", 0, 4, 2, 64, 64, residual=True, bias=True),
     "glu_no_tokens": _f("swiglu", 0, 4, 2, 64, 40, residual=True),
     "lin_twice": _f("linear", 40, 3, 3, 64, 72, twice=True, act="gelu", residual=True),
