@@ -588,9 +588,10 @@ typedef enum lrm_act { LRM_ACT_NONE = 0, LRM_ACT_RELU = 1, LRM_ACT_GELU = 2, LRM
  *   SWIGLU: a_p = W_gate,e x_p, b_p = W_up,e x_p, y_p = W_down,e (silu(a_p) b_p)
  *   Y[t] = R[t] + sum over the pairs p of t of w_p y_p
  * with e the expert of p.  bf16 runs on MFMA with fp32 accumulation, fp32 in
- * fp32; silu(a) b is rounded to the inputs' dtype between the two products;
- * bias, activation, weights, the sum over pairs and the residual are fp32 and
- * rounded once. */
+ * fp32; silu(a) b is rounded to the inputs' dtype between the two products
+ * (held in fp32 where Y is wanted of one token's pairs, at most 64 of them, or of
+ * at most E / 4 pairs); bias, activation, weights, the sum over pairs and the
+ * residual are fp32 and rounded once. */
 typedef struct lrm_forward {
   int32_t kind;  /* lrm_kind */
   int32_t act;   /* lrm_act (LINEAR; NONE for SWIGLU) */

@@ -164,7 +164,7 @@ bool few_join(const lrm_pairs* p) { return p->T == 1 || (int64_t)p->N * 4 <= p->
 struct FwdWs {
   BucketWs b;
   float* Yf;     // few pairs: y in fp32, [N][d_out]
-  void* H;       // SWIGLU: packed silu(a) b, [N][I]
+  void* H;       // SWIGLU: packed silu(a) b, [N][I] (fp32 where few_join takes it)
   void* Yp;      // [N][d_out]
   int8_t* Ylo;   // bf16: [N][d_out]
   void* dump;    // 1 KB that lanes outside a tile store to
@@ -183,7 +183,8 @@ FwdWs carve_forward(Carve& c, const lrm_forward* f) {
   const bool glu = f->kind == LRM_SWIGLU;
   const int64_t d = glu ? f->H : f->d_out;
   w.b = carve_bucket(c, &f->pairs);
-  if (glu) w.H = c.take<char>(N * f->I * es);
+  const bool h32 = few_pairs(&f->pairs) && few_join(&f->pairs);
+  if (glu) w.H = c.take<char>(N * f->I * (h32 ? 4 : es));
   w.Yp = c.take<char>(N * d * es);
   if (f->dtype == LRM_BF16) w.Ylo = c.take<int8_t>(N * d);
   if (few_pairs(&f->pairs)) w.Yf = c.take<float>(N * d);
@@ -195,6 +196,7 @@ FwdWs carve_forward(Carve& c, const lrm_forward* f) {
 lrm_status run_few(const lrm_forward* f, const lrm_forward_outputs* out, void* ws, hipStream_t s) {
   const lrm_pairs* p = &f->pairs;
   const bool glu = f->kind == LRM_SWIGLU;
+  const bool joined = out->Y && glu && few_join(p);
   Carve c(ws);
   const FwdWs w = carve_forward(c, f);
   FwdFewArgs g{};
@@ -208,6 +210,7 @@ lrm_status run_few(const lrm_forward* f, const lrm_forward_outputs* out, void* w
     g.glu = 1; g.K = f->H; g.n = f->I;
     g.W0 = f->W_gate; g.W1 = f->W_up; g.w_stride = (int64_t)f->H * f->I;
     g.A = out->A; g.B = out->B; g.H = w.H;
+    g.h32 = joined;
     LRM_TRY_HIP(launch_fwd_few(g, s));
     if (out->h_sumsq) LRM_TRY_HIP(launch_fwd_few_sumsq(g, out->h_sumsq, s));
     g.glu = 0; g.K = f->I; g.n = f->H; g.X = w.H; g.ldx = f->I; g.x_pair = 1;
@@ -219,7 +222,7 @@ lrm_status run_few(const lrm_forward* f, const lrm_forward_outputs* out, void* w
   g.Y = out->Yp; g.out = out->Y; g.R = f->R.ptr; g.ldr = f->R.ld;
   // (the joining product reports no index errors: GLU's first product has, and
   // one projection without it takes the other way)
-  if (out->Y && glu && few_join(p)) {
+  if (joined) {
     LRM_TRY_HIP(launch_fwd_few_join(g, s));
     return LRM_OK;
   }

@@ -13,7 +13,9 @@
 // k_fwd_few_join: a block takes one token and 8 output columns; a wave takes a
 // pair of the token, and the weighted sum over them and the residual happen on
 // the way out, so that one decoded token needs two launches.  Every token
-// reads its experts' weights on its own.
+// reads its experts' weights on its own.  It multiplies in fp32, so silu(a) b
+// comes to it in fp32 too (h32; 24 KB for a token of 8 pairs, from the L2); the
+// MFMA products take it in the inputs' type.
 //
 // Sums are made in a fixed order.
 //
@@ -145,6 +147,21 @@ __device__ __forceinline__ float dot16(u32x4 x, u32x4 y) {
   return s;
 }
 
+// x: the same values' partners in fp32 (V / 4 vectors of four)
+template <bool BF16>
+__device__ __forceinline__ float dot16(u32x4 w, const f32x4* x, float s) {
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    if constexpr (BF16) {
+      s = fmaf(bf16_lo(w[k]), x[k >> 1][2 * (k & 1)], s);
+      s = fmaf(bf16_hi(w[k]), x[k >> 1][2 * (k & 1) + 1], s);
+    } else {
+      s = fmaf(__uint_as_float(w[k]), x[0][k], s);
+    }
+  }
+  return s;
+}
+
 // What becomes of four consecutive columns c .. of pair p: u = W0 x, v = W1 x.
 template <bool BF16, bool GLU>
 __device__ __forceinline__ void few_emit(const FwdFewArgs& g, int e, int p, int c, f32x4 u, f32x4 v) {
@@ -155,7 +172,10 @@ __device__ __forceinline__ void few_emit(const FwdFewArgs& g, int e, int p, int 
     f32x4 h;
 #pragma unroll
     for (int k = 0; k < 4; ++k) h[k] = u[k] * sigmoidf_acc(u[k]) * v[k];
-    put4<BF16>(g.H, at, h);
+    if (g.h32)
+      put4<false>(g.H, at, h);
+    else
+      put4<BF16>(g.H, at, h);
   } else {
     if (g.bias) {
 #pragma unroll
@@ -200,7 +220,7 @@ __global__ __launch_bounds__(256, 2) void k_fwd_few(FwdFewArgs g) {
   if (NF == 1 && M == 1) {
     // one pair: a wave takes four of the 16 weight rows, 1 KB of a row a load
     // (16 rows x 64 bytes a load, as the fragments have it: two tokens of the
-    // Qwen3-shaped layer 38 us instead of 32)
+    // Qwen3-shaped layer 38 us instead of 32), 16 KB of weights in flight
     constexpr int UB = 4;
     const int p = list[0], t = __shfl(pairs.t, p, kWave), G = kb / 16;
     const u32x4* x = reinterpret_cast<const u32x4*>((const char*)g.X +
@@ -269,13 +289,40 @@ __global__ __launch_bounds__(256, 2) void k_fwd_few(FwdFewArgs g) {
   }
 }
 
+// acc[r] += the granules i0 .. i0 + UB * kWave - 1 (those below G) of weight row
+// r times x, one a lane and step.  All loads are on their way before the first
+// product.
+template <bool BF16, int UB, int ROWS>
+__device__ __forceinline__ void join_step(const u32x4* const (&row)[ROWS], const f32x4* x, int i0,
+                                          int G, float (&acc)[ROWS]) {
+  constexpr int XV = BF16 ? 2 : 1;
+  u32x4 b[UB][ROWS];
+  f32x4 a[UB][XV];
+#pragma unroll
+  for (int q = 0; q < UB; ++q) {
+    const int i = i0 + q * kWave + lane_id(), ic = i < G ? i : G - 1;
+#pragma unroll
+    for (int r = 0; r < ROWS; ++r) b[q][r] = row[r][ic];
+#pragma unroll
+    for (int v = 0; v < XV; ++v) {
+      a[q][v] = x[ic * XV + v];
+      if (i >= G) a[q][v] = f32x4{0.f, 0.f, 0.f, 0.f};
+    }
+  }
+#pragma unroll
+  for (int q = 0; q < UB; ++q)
+#pragma unroll
+    for (int r = 0; r < ROWS; ++r) acc[r] = dot16<BF16>(b[q][r], a[q], acc[r]);
+}
+
 // The products of one token's pairs and their weighted sum: out[t] = R[t] +
-// sum of w_p W0 x_p, with x_p row p of X (the packed silu(a) b), and Y.  The
-// block's 8 weight rows lie one after the other in memory: a wave reads them
-// as one run, 1 KB a load, and adds each lane's 16 bytes to their row.
+// sum of w_p W0 x_p, with x_p row p of X (silu(a) b in fp32), and Y.  The
+// block's 8 weight rows lie one after the other in memory; a wave reads 1 KB of
+// each at a time, 16 KB in flight as in k_fwd_few (half of that for the last
+// granules, or rows of one KB at most), and holds x over the eight rows.
 template <bool BF16>
 __global__ __launch_bounds__(512, 2) void k_fwd_few_join(FwdFewArgs g) {
-  constexpr int ES = BF16 ? 2 : 4, COLS = 8, UB = 12;
+  constexpr int ES = BF16 ? 2 : 4, COLS = 8;
   __shared__ int lists[kJoinWaves][kWave];
   __shared__ float ys[kFewPairs][COLS];
   const int w = threadIdx.x >> 6, l = lane_id();
@@ -289,34 +336,22 @@ __global__ __launch_bounds__(512, 2) void k_fwd_few_join(FwdFewArgs g) {
   const int M = __popcll(m);
   int* list = lists[w];
   list_bits(m, list);
-  const int G = g.K * ES / 16;                     // granules of a row
-  const int TG = (n0 + COLS < g.n ? COLS : g.n - n0) * G;
+  const int G = g.K * ES / 16;  // granules of a row
   for (int j = w; j < M; j += kJoinWaves) {
     const int p = list[j], e = __shfl(pairs.e, p, kWave);
-    const u32x4* x = reinterpret_cast<const u32x4*>((const char*)g.X + (int64_t)p * g.ldx * ES);
-    const u32x4* W = reinterpret_cast<const u32x4*>(
-        (const char*)g.W0 + ((int64_t)e * g.w_stride + (int64_t)n0 * g.K) * ES);
+    const f32x4* x = reinterpret_cast<const f32x4*>((const float*)g.X + (int64_t)p * g.ldx);
+    const u32x4* row[COLS];
+#pragma unroll
+    for (int r = 0; r < COLS; ++r)
+      row[r] = reinterpret_cast<const u32x4*>(
+          (const char*)g.W0 +
+          ((int64_t)e * g.w_stride + (int64_t)(n0 + r < g.n ? n0 + r : g.n - 1) * g.K) * ES);
     float acc[COLS];
 #pragma unroll
     for (int r = 0; r < COLS; ++r) acc[r] = 0.f;
-    for (int i0 = 0; i0 < TG; i0 += UB * kWave) {
-      u32x4 a[UB], b[UB];
-      int row[UB];
-#pragma unroll
-      for (int q = 0; q < UB; ++q) {
-        const int i = i0 + q * kWave + l, ic = i < TG ? i : TG - 1;
-        row[q] = ic / G;
-        b[q] = W[ic];
-        a[q] = x[ic - row[q] * G];
-        if (i >= TG) row[q] = COLS;
-      }
-#pragma unroll
-      for (int q = 0; q < UB; ++q) {
-        const float d = dot16<BF16>(a[q], b[q]);
-#pragma unroll
-        for (int r = 0; r < COLS; ++r) acc[r] += row[q] == r ? d : 0.f;
-      }
-    }
+    int i0 = 0;
+    for (; i0 + kWave < G; i0 += 2 * kWave) join_step<BF16, 2, COLS>(row, x, i0, G, acc);
+    if (i0 < G) join_step<BF16, 1, COLS>(row, x, i0, G, acc);
 #pragma unroll
     for (int r = 0; r < COLS; ++r) acc[r] = wave_sum(acc[r]);
     if (l == 0) {
@@ -379,7 +414,7 @@ __global__ __launch_bounds__(256) void k_fwd_few_sum(FwdFewArgs g) {
   put4<BF16>(g.out, (int64_t)t * g.n + c, sum);
 }
 
-// |H[p]|^2 of every present pair: one wave each
+// |H[p]|^2 of every present pair: one wave each (BF16: H is of that type)
 template <bool BF16>
 __global__ __launch_bounds__(256) void k_fwd_few_sumsq(FwdFewArgs g, double* out) {
   const int p = blockIdx.x * 4 + (threadIdx.x >> 6);
@@ -420,7 +455,7 @@ hipError_t launch_fwd_few(const FwdFewArgs& g, hipStream_t s) {
 
 hipError_t launch_fwd_few_sumsq(const FwdFewArgs& g, double* out, hipStream_t s) {
   if (g.N <= 0) return hipSuccess;
-  if (g.bf16)
+  if (g.bf16 && !g.h32)
     LRM_LAUNCH((g.N + 3) / 4, 256, 0, s, k_fwd_few_sumsq<true>)(g, out);
   else
     LRM_LAUNCH((g.N + 3) / 4, 256, 0, s, k_fwd_few_sumsq<false>)(g, out);

@@ -340,11 +340,13 @@ hipError_t launch_fwd_join(const FwdJoinArgs& a, hipStream_t s);
 // its token's; outputs are rows of p.
 //   launch_fwd_few: A, B, H (glu) or Z, Y, Yf (fp32) of every present pair;
 //     err (or null): the pairs' index error bits
-//   launch_fwd_few_join: y_p = W0 X[p], Y (or null), out[t] = R[t] + sum of w_p y_p
+//   launch_fwd_few_join: y_p = W0 X[p], Y (or null), out[t] = R[t] + sum of w_p y_p;
+//     X is fp32 whatever the type
 //   launch_fwd_few_sum: out[t] = R[t] + sum of w_p Yf[p]
 struct FwdFewArgs {
   int N, T, E, bf16, K, n, glu, act, x_pair;
   int by_pair;  // a block's expert is that of its pair (N at most E)
+  int h32;      // H is fp32 whatever the type (for launch_fwd_few_join)
   const int32_t* token;
   const int32_t* expert;
   const float* weight;

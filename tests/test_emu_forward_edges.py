@@ -1,0 +1,35 @@
+"""Edge cases of the router, the experts' forward pass and the epilogue's
+backward pass on the unchanged kernels in the CPU emulation (see
+test_emu_forward)."""
+
+from __future__ import annotations
+
+import numpy as np
+import pytest
+import torch
+
+import forward_cases as FC
+import forward_edges as FE
+from test_emu_forward import call, driver, nbytes, router_nums, stored  # noqa: F401
+
+
+def emu(driver, tmp_path, c, expect=(0, 0), env_extra=None):  # noqa: F811
+    """The forward call's outputs by name."""
+    shapes = FC.forward_shapes(c)
+    order = ("Y", "Yp", "Z", "A", "B", "h_sumsq")
+    pr = c["pairs"]
+    nums = [3, c["T"], c["N"], c["E"], int(c["kind"] != "linear"), int(c["dtype"] == "bf16"),
+            ("none", "relu", "gelu", "silu").index(c["act"]), c["d_in"], c["d"],
+            int(c["x_rows"] == "pair"), c["ldx"], c["d_out"], c["d_in"] * c["d"]]
+    nums += [nbytes(*shapes[k]) if k in shapes else -1 for k in order]
+    w = [c["W"], c["bias_t"]] if c["kind"] == "linear" else [c["W_gate"], c["W_up"], c["W_down"]]
+    got = call(driver, tmp_path, nums,
+               [pr["token"], pr["expert"], pr["weight"], c["X_store"].reshape(-1), c["R"], *w],
+               [shapes[k] for k in order if k in shapes], expect=expect, env_extra=env_extra)
+    return dict(zip([k for k in order if k in shapes], got))
+
+
+@pytest.mark.parametrize("name", list(FE.ONE_TOKEN))
+def test_emu_one_token_keeps_its_hidden_values_in_fp32(driver, tmp_path, name):  # noqa: F811
+    c = FE.one_token_case(name)
+    FE.judge_one_token(c, emu(driver, tmp_path, c))
