@@ -30,12 +30,13 @@ namespace {
 constexpr int kRouteThreads = 256;
 
 // ---------------------------------------------------------- ordered keys
+// (-0 has the key of +0: adding +0 turns it into +0)
 __device__ __forceinline__ uint32_t ord_of(float f) {
-  const uint32_t u = __float_as_uint(f);
+  const uint32_t u = __float_as_uint(f + 0.f);
   return u ^ ((u & 0x80000000u) ? 0xffffffffu : 0x80000000u);
 }
 __device__ __forceinline__ uint64_t ord_of(double d) {
-  const uint64_t u = __builtin_bit_cast(uint64_t, d);
+  const uint64_t u = __builtin_bit_cast(uint64_t, d + 0.0);
   return u ^ ((u >> 63) ? ~0ull : (1ull << 63));
 }
 __device__ __forceinline__ float unord(uint32_t k) {
@@ -665,9 +666,10 @@ __global__ __launch_bounds__(kRouteThreads) void k_route_direct(RouteArgs a) {
     uint32_t s32[8], w = 0;
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-      // both halves: flip the sign of positive values, all bits of others
+      // both halves: 0x8000 plus the magnitude, or less it (-0 and +0 alike;
+      // no half carries into the other)
       const uint32_t neg = (x[j] >> 15) & 0x00010001u;
-      const uint32_t y = x[j] ^ (((neg << 15) - neg) | 0x80008000u);
+      const uint32_t y = (x[j] ^ (((neg << 15) - neg) | 0x80008000u)) + neg;
       s32[2 * j] = (y << 16 | (below - 2 * j)) & open;
       s32[2 * j + 1] = ((y & 0xffff0000u) | (below - 2 * j - 1)) & open;
     }
@@ -676,10 +678,11 @@ __global__ __launch_bounds__(kRouteThreads) void k_route_direct(RouteArgs a) {
       for (int j = 0; j < 8; ++j) s32[j] = (bits >> j) & 1 ? s32[j] : 0u;
     }
     choose_packed<LPT>(s32, i, a.k, false, &w, [](uint32_t, uint32_t) { return false; });
-    // (-inf has key 0x007f: such a choice is none)
-    const bool has = i < a.k && w >= 0x00800000u;
+    // (-inf has key 0x0080: such a choice is none)
+    const bool has = i < a.k && w >= 0x00810000u;
     const int e = (int)(0xffffu - (w & 0xffffu));
-    const float zc = __uint_as_float(__float_as_uint(unord(w & 0xffff0000u)) & 0xffff0000u);
+    const uint32_t hi = w & 0xffff0000u;
+    const float zc = __uint_as_float(hi & 0x80000000u ? hi ^ 0x80000000u : 0u - hi);
     const float wt = chosen_weight<LPT>(a, has, zc);
     if (in && i < a.k) {
       const int64_t at = t * a.k + i;

@@ -62,3 +62,50 @@ def judge_one_token(c, got):
         t, w = int(pr["token"][p]), abs(float(pr["weight"][p]))
         tY[t] += w * (ty[p] + (c["k"] + 4) * U * ref["Yp"][p].abs())
     FC.close("Y", got["Y"].cpu(), ref["Y"], tY + half * (ref["Y"].abs() + tY))
+
+
+# ------------------------------------------------------- zeros of both signs
+# -0 and +0 are equal logits: the border of the choice lies between them (z1 of
+# a row's zeros, the rest below), or between groups whose best are zeros.
+ZERO_TIES = {
+    "direct": dict(T=40, E=16, k=1, dtype="bf16"),
+    "direct_mid": dict(T=40, E=136, k=3, dtype="bf16"),
+    "direct_wide": dict(T=20, E=512, k=4, dtype="bf16"),
+    "not_renormed": dict(T=40, E=16, k=2, dtype="bf16", renorm=False),
+    "odd": dict(T=40, E=15, k=2, dtype="bf16"),
+    "sigmoid": dict(T=40, E=15, k=1, dtype="bf16", score="sigmoid"),
+    "f32": dict(T=40, E=16, k=2, dtype="f32"),
+    "f32_odd": dict(T=40, E=61, k=3, dtype="f32"),
+    "f32_wide": dict(T=12, E=600, k=2, dtype="f32"),
+    "wide": dict(T=12, E=600, k=2, dtype="bf16"),
+    "widest": dict(T=4, E=1100, k=2, dtype="f32"),
+    "bias": dict(T=40, E=24, k=2, dtype="f32", bias=True, score="sigmoid"),
+    "groups_lanes": dict(T=40, E=64, k=2, dtype="bf16", n_group=8, topk_group=1, group_rule="max"),
+    "groups_lanes_f32": dict(T=40, E=64, k=2, dtype="f32", n_group=4, topk_group=2,
+                             group_rule="max"),
+    "groups_odd": dict(T=40, E=60, k=2, dtype="f32", n_group=10, topk_group=2, group_rule="max"),
+    "groups_wide": dict(T=8, E=600, k=2, dtype="f32", n_group=50, topk_group=2, group_rule="max"),
+    "groups_top2": dict(T=40, E=64, k=3, dtype="f32", n_group=8, topk_group=2),
+    "masked": dict(T=40, E=16, k=2, dtype="bf16", emask=True),
+}
+
+
+def zero_case(name):
+    c = dict(score="softmax", renorm=True, scale=1.0, n_group=1, topk_group=1, group_rule="top2",
+             bias=False, emask=False)
+    c.update(ZERO_TIES[name])
+    T, E = c["T"], c["E"]
+    g = FC.gen("zeros", name)
+    z = -1.0 - torch.rand(T, E, generator=g)
+    rng = np.random.default_rng(T + E)
+    for t in range(T):
+        at = np.sort(rng.choice(E, size=min(E, c["k"] + 4), replace=False))
+        sign = rng.random(at.size) < 0.5
+        sign[0], sign[-1] = True, False  # the lowest is -0, the highest +0
+        z[t, torch.from_numpy(at)] = torch.from_numpy(np.where(sign, -0.0, 0.0).astype(np.float32))
+    c["bias_t"] = torch.zeros(E) if c["bias"] else None
+    c["tmask"] = None
+    c["emask"] = (torch.rand(E, generator=g) < 0.7).to(torch.uint8) if c["emask"] else None
+    c["logits"] = z.to(FC.DT[c["dtype"]])
+    c["ld"] = E
+    return c

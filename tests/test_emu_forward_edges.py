@@ -33,3 +33,16 @@ def emu(driver, tmp_path, c, expect=(0, 0), env_extra=None):  # noqa: F811
 def test_emu_one_token_keeps_its_hidden_values_in_fp32(driver, tmp_path, name):  # noqa: F811
     c = FE.one_token_case(name)
     FE.judge_one_token(c, emu(driver, tmp_path, c))
+
+
+def emu_route(driver, tmp_path, c):  # noqa: F811
+    n, i32 = c["T"] * c["k"], torch.int32
+    return call(driver, tmp_path, router_nums(0, c) + [4 * n, 4 * n, 4 * c["E"]],
+                [stored(c), c["bias_t"], c["emask"], c["tmask"]],
+                [((n,), i32), ((n,), torch.float32), ((n,), i32), ((c["E"],), i32)])
+
+
+@pytest.mark.parametrize("name", list(FE.ZERO_TIES))
+def test_emu_zeros_of_both_signs_tie(driver, tmp_path, name):  # noqa: F811
+    c = FE.zero_case(name)
+    FC.judge_route(c, *emu_route(driver, tmp_path, c))
