@@ -222,10 +222,19 @@ def mat(t: torch.Tensor | None, rows: str | int) -> lrm_mat:
     return m
 
 
-def _ws(nbytes: int, device, ws):
+def _scratch(nbytes: int, device, stream):
+    """Device scratch for a call on `stream`, allocated on that stream: freed with
+    its last reference, it goes to later work of the same stream only."""
+    if stream is None:
+        return torch.empty(nbytes, dtype=torch.uint8, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(nbytes, dtype=torch.uint8, device=device)
+
+
+def _ws(nbytes: int, device, ws, stream=None):
     if ws is not None:
         return ws
-    return torch.empty(max(int(nbytes), 256), dtype=torch.uint8, device=device)
+    return _scratch(max(int(nbytes), 256), device, stream)
 
 
 def _quota_arr(q):
@@ -241,7 +250,7 @@ def _quota_arr(q):
 # ---------------------------------------------------------------- the steps
 def lrm_score(pairs: Pairs, X: lrm_mat, G: lrm_mat, score: torch.Tensor, ws=None, stream=None):
     need = _lib.lrm_score_workspace_size(C.byref(pairs.c))
-    ws = _ws(need, score.device, ws)
+    ws = _ws(need, score.device, ws, stream)
     _check(_lib.lrm_score(C.byref(pairs.c), C.byref(X), C.byref(G), _ptr(score), _ptr(ws),
                           ws.numel(), _stream(stream)), "lrm_score")
 
@@ -249,7 +258,7 @@ def lrm_score(pairs: Pairs, X: lrm_mat, G: lrm_mat, score: torch.Tensor, ws=None
 def lrm_score_glu(pairs: Pairs, A: lrm_mat, B: lrm_mat, G: lrm_mat, score: torch.Tensor,
                   ws=None, stream=None):
     need = _lib.lrm_score_workspace_size(C.byref(pairs.c))
-    ws = _ws(need, score.device, ws)
+    ws = _ws(need, score.device, ws, stream)
     _check(_lib.lrm_score_glu(C.byref(pairs.c), C.byref(A), C.byref(B), C.byref(G),
                               _ptr(score), _ptr(ws), ws.numel(), _stream(stream)),
            "lrm_score_glu")
@@ -258,7 +267,7 @@ def lrm_score_glu(pairs: Pairs, A: lrm_mat, B: lrm_mat, G: lrm_mat, score: torch
 def lrm_select(pairs: Pairs, score, quota, pos, offsets, kept, flags=0, ws=None, stream=None,
                device=None):
     need = _lib.lrm_select_workspace_size(C.byref(pairs.c))
-    ws = _ws(need, device or offsets.device, ws)
+    ws = _ws(need, device or offsets.device, ws, stream)
     q = _quota_arr(quota) if quota is not None else None
     _check(_lib.lrm_select(C.byref(pairs.c), _ptr(score), _ptr(q), flags, _ptr(pos),
                            _ptr(offsets), _ptr(kept), _ptr(ws), ws.numel(), _stream(stream)),
@@ -297,7 +306,7 @@ def lrm_grouped_bwd(E: int, offsets, max_rows: int, Gp, Xp, W, d_in: int, d_out:
     if w_stride is None:
         w_stride = d_in * d_out
     need = _lib.lrm_grouped_bwd_workspace_size(int(E))
-    ws = _ws(need, offsets.device, ws)
+    ws = _ws(need, offsets.device, ws, stream)
     _check(_lib.lrm_grouped_bwd(int(E), _ptr(offsets), int(max_rows), dt, _ptr(Gp), _ptr(Xp),
                                 _ptr(W), int(w_stride), int(d_in), int(d_out), _ptr(dW),
                                 _ptr(dXp), _ptr(ws), ws.numel(), _stream(stream)),
@@ -306,7 +315,7 @@ def lrm_grouped_bwd(E: int, offsets, max_rows: int, Gp, Xp, W, d_in: int, d_out:
 
 def lrm_unpermute(pairs: Pairs, pos, dXp, d_in: int, out_rows, dX, ws=None, stream=None):
     need = _lib.lrm_unpermute_workspace_size(C.byref(pairs.c))
-    ws = _ws(need, dX.device, ws)
+    ws = _ws(need, dX.device, ws, stream)
     r = ROWS[out_rows] if isinstance(out_rows, str) else int(out_rows)
     _check(_lib.lrm_unpermute(C.byref(pairs.c), _ptr(pos), _ptr(dXp), int(d_in), r, _ptr(dX),
                               _ptr(ws), ws.numel(), _stream(stream)), "lrm_unpermute")
@@ -333,7 +342,7 @@ def lrm_quota_waterfill_device(pairs: Pairs, budget: int, quota, counts=None, ws
     `quota`, from device counts [E] or (counts None) the pairs' own counts.
     Returns the workspace (its error word reports pairs out of range)."""
     need = _lib.lrm_quota_waterfill_device_workspace_size(C.byref(pairs.c))
-    ws = _ws(need, quota.device, ws)
+    ws = _ws(need, quota.device, ws, stream)
     _check(_lib.lrm_quota_waterfill_device(C.byref(pairs.c), _ptr(counts), int(budget),
                                            _ptr(quota), _ptr(ws), ws.numel(), _stream(stream)),
            "lrm_quota_waterfill_device")
@@ -367,7 +376,7 @@ def lrm_receiver_layout(offsets, assign, max_rows: int, ws=None, stream=None):
     send_off = torch.empty(G + 1, **i32)
     blk_off = torch.empty(G, E + 1, **i32)
     dst = torch.empty(max(int(max_rows), 1), **i32)
-    ws = _ws(_lib.lrm_receiver_layout_workspace_size(E, G), dev, ws)
+    ws = _ws(_lib.lrm_receiver_layout_workspace_size(E, G), dev, ws, stream)
     _check(_lib.lrm_receiver_layout(E, G, _ptr(offsets), _ptr(assign), int(max_rows),
                                     _ptr(send_off), _ptr(blk_off), _ptr(dst), _ptr(ws),
                                     ws.numel(), _stream(stream)), "lrm_receiver_layout")
@@ -431,18 +440,18 @@ def _outputs(outputs: dict) -> lrm_outputs:
     return o
 
 
-def _fused_ws(pb: Problem, ws):
+def _fused_ws(pb: Problem, ws, stream=None):
     if ws is not None:
         return ws
     n = lrm_workspace_size(pb)
     if n == 0:
         raise LrmError(2, "lrm_workspace_size")
-    return torch.empty(n, dtype=torch.uint8, device=pb.pairs.token.device)
+    return _scratch(n, pb.pairs.token.device, stream)
 
 
 def lrm_expert_backward(pb: Problem, outputs: dict, ws=None, stream=None):
     o = _outputs(outputs)
-    ws = _fused_ws(pb, ws)
+    ws = _fused_ws(pb, ws, stream)
     _check(_lib.lrm_expert_backward(C.byref(pb.c), C.byref(o), _ptr(ws), ws.numel(),
                                     _stream(stream)), "lrm_expert_backward")
     return ws
@@ -452,7 +461,7 @@ def lrm_expert_backward_events(pb: Problem, outputs: dict, events, ws=None, stre
     """The fused call recording torch.cuda.Event objects at stage boundaries
     (each event must have been recorded once so that its handle exists)."""
     o = _outputs(outputs)
-    ws = _fused_ws(pb, ws)
+    ws = _fused_ws(pb, ws, stream)
     arr = (C.c_void_p * len(events))(*[ev.cuda_event for ev in events])
     _check(_lib.lrm_expert_backward_events(C.byref(pb.c), C.byref(o), _ptr(ws), ws.numel(),
                                            _stream(stream), arr, len(events)),
@@ -508,7 +517,7 @@ def lrm_route(r: Router, expert, weight, token=None, counts=None, ws=None, strea
     _slots("token", token, n, torch.int32, on)
     _slots("counts", counts, r.E, torch.int32, on)
     if counts is not None:
-        ws = _ws(r.ws_bytes, counts.device, ws)
+        ws = _ws(r.ws_bytes, counts.device, ws, stream)
     _check(_lib.lrm_route(C.byref(r.c), _ptr(expert), _ptr(weight), _ptr(token), _ptr(counts),
                           _ptr(ws), ws.numel() if ws is not None else 0, _stream(stream)),
            "lrm_route")
@@ -540,7 +549,7 @@ def lrm_route_share(T: int, k: int, expert, weight, e0: int, E: int, out_token, 
                            ("out_weight", out_weight, n, torch.float32),
                            ("out_slot", out_slot, n, torch.int32), ("out_n", out_n, 1, torch.int32)):
         _slots(name, t, m, dt, out_n.device)
-    ws = _ws(_lib.lrm_route_share_workspace_size(int(T), int(k)), out_n.device, ws)
+    ws = _ws(_lib.lrm_route_share_workspace_size(int(T), int(k)), out_n.device, ws, stream)
     _check(_lib.lrm_route_share(int(T), int(k), _ptr(expert), _ptr(weight), int(e0), int(E),
                                 _ptr(out_token), _ptr(out_expert), _ptr(out_weight),
                                 _ptr(out_slot), _ptr(out_n), _ptr(ws), ws.numel(),
@@ -649,12 +658,8 @@ def forward_outputs(outputs: dict) -> lrm_forward_outputs:
     return _marshal(lrm_forward_outputs, outputs)
 
 
-def _grown(ws, need, device):
-    if ws is not None:
-        return ws
-    if need == 0:
-        return None
-    return torch.empty(need, dtype=torch.uint8, device=device)
+def _grown(need, device, stream):
+    return _scratch(need, device, stream) if need else None
 
 
 def lrm_expert_forward(f: Forward, outputs, ws=None, stream=None):
@@ -662,7 +667,7 @@ def lrm_expert_forward(f: Forward, outputs, ws=None, stream=None):
     o = forward_outputs(outputs) if isinstance(outputs, dict) else outputs
     _check_outputs(o, f)
     if ws is None:
-        ws = _grown(ws, lrm_forward_workspace_size(f), f.pairs.token.device)
+        ws = _grown(lrm_forward_workspace_size(f), f.pairs.token.device, stream)
     _check(_lib.lrm_expert_forward(C.byref(f.c), C.byref(o), _ptr(ws),
                                    ws.numel() if ws is not None else 0, _stream(stream)),
            "lrm_expert_forward")
@@ -704,7 +709,7 @@ def lrm_pair_grad(g: PairGrad, outputs, ws=None, stream=None):
     o = pair_grad_outputs(outputs) if isinstance(outputs, dict) else outputs
     _check_outputs(o, g)
     if ws is None:
-        ws = _grown(ws, lrm_pair_grad_workspace_size(g), g.pairs.token.device)
+        ws = _grown(lrm_pair_grad_workspace_size(g), g.pairs.token.device, stream)
     _check(_lib.lrm_pair_grad(C.byref(g.c), C.byref(o), _ptr(ws),
                               ws.numel() if ws is not None else 0, _stream(stream)),
            "lrm_pair_grad")

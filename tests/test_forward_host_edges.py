@@ -1,0 +1,81 @@
+"""CPU tests of the binding's edge cases: the router, the experts' forward pass
+and the epilogue's backward pass (see test_forward_host)."""
+
+import contextlib
+
+import pytest
+import torch
+
+from pruned_expert_backward_lrm_amd import lrm as L
+
+
+class FakeLibrary:
+    """Answers every call with LRM_OK and every size query with 4096."""
+
+    def __getattr__(self, name):
+        return lambda *a: 4096 if name.endswith("_workspace_size") else L.LRM_OK
+
+
+class FakeStream:
+    cuda_stream = 0
+
+
+def i32(*shape):
+    return torch.zeros(*shape, dtype=torch.int32)
+
+
+def every_call(stream):
+    """Every call that may allocate its workspace, on `stream`."""
+    N, T, E = 8, 4, 2
+    pr = L.Pairs(i32(N), i32(N), torch.zeros(N), T, E)
+    X, W = torch.zeros(T, 8), torch.zeros(E, 12, 8)
+    r = L.Router(X, 2)
+    f = L.linear_forward(pr, X, "token", W)
+    pg = L.pair_grad_problem(pr, X, "token", torch.zeros(N, 8))
+    pb = L.linear_problem(pr, X, "token", torch.zeros(T, 12), "token", W, [4, 4])
+    m = L.mat(X, "token")
+    return {
+        "lrm_route": lambda: L.lrm_route(r, i32(8), torch.zeros(8), counts=i32(8), stream=stream),
+        "lrm_route_share": lambda: L.lrm_route_share(T, 2, i32(8), torch.zeros(8), 0, E, i32(8), i32(8),
+                                                     torch.zeros(8), i32(1), stream=stream),
+        "lrm_expert_forward": lambda: L.lrm_expert_forward(f, dict(Y=torch.zeros(T, 12)),
+                                                           stream=stream),
+        "lrm_pair_grad": lambda: L.lrm_pair_grad(pg, dict(dweight=torch.zeros(N)), stream=stream),
+        "lrm_expert_backward": lambda: L.lrm_expert_backward(pb, {}, stream=stream),
+        "lrm_expert_backward_events": lambda: L.lrm_expert_backward_events(pb, {}, [], stream=stream),
+        "lrm_score": lambda: L.lrm_score(pr, m, m, torch.zeros(N), stream=stream),
+        "lrm_score_glu": lambda: L.lrm_score_glu(pr, m, m, m, torch.zeros(N), stream=stream),
+        "lrm_select": lambda: L.lrm_select(pr, torch.zeros(N), [4, 4], i32(N), i32(3), i32(N),
+                                           stream=stream),
+        "lrm_grouped_bwd": lambda: L.lrm_grouped_bwd(E, i32(3), N, X, X, W, 8, 12, W, X, stream=stream),
+        "lrm_unpermute": lambda: L.lrm_unpermute(pr, i32(N), X, 8, "token", X, stream=stream),
+        "lrm_quota_waterfill_device": lambda: L.lrm_quota_waterfill_device(pr, 4, i32(E),
+                                                                           stream=stream),
+        "lrm_receiver_layout": lambda: L.lrm_receiver_layout(i32(3), i32(E, 1), 4, stream=stream),
+    }
+
+
+@pytest.mark.parametrize("name", list(every_call(None)))
+def test_a_workspace_is_allocated_on_the_stream_that_uses_it(monkeypatch, name):
+    s, inside, scratch = FakeStream(), [], []
+
+    @contextlib.contextmanager
+    def on(stream):
+        inside.append(stream)
+        yield
+        inside.pop()
+
+    empty = torch.empty
+
+    def record(*a, **kw):
+        if kw.get("dtype") == torch.uint8:
+            scratch.append(inside[-1] if inside else None)
+        return empty(*a, **kw)
+
+    call = every_call(s)[name]
+    monkeypatch.setattr(torch.cuda, "stream", on)
+    monkeypatch.setattr(torch, "empty", record)
+    monkeypatch.setattr(L, "_lib", FakeLibrary())
+    monkeypatch.setattr(L, "_stream", lambda *a: 0)
+    call()
+    assert scratch == [s]
