@@ -594,12 +594,16 @@ def linear_forward(pairs: Pairs, X, x_rows, W, act="none", bias=None, residual=N
             W.device != pairs.token.device:
         raise ValueError("W must be [E][d_out][d_in] of X's dtype, dense inside an expert, "
                          "on the pairs' device")
+    # (the stride of one expert says nothing)
+    stride = W.stride(0) if pairs.E > 1 else W.shape[1] * W.shape[2]
+    if stride < W.shape[1] * W.shape[2]:
+        raise ValueError("the experts of W must not share memory (an expanded W: call contiguous)")
     if bias is not None:
         _dense("bias", bias, W.shape[:2], X.dtype, pairs.token.device)
     f = Forward(LRM_LINEAR, pairs, X, x_rows, residual, act)
     f.keep += [W, bias]
     c = f.c
-    c.W, c.w_stride = _ptr(W), max(W.stride(0), W.shape[1] * W.shape[2])
+    c.W, c.w_stride = _ptr(W), stride
     c.bias = _ptr(bias)
     c.d_in, c.d_out = W.shape[2], W.shape[1]
     f.sizes = {"Y": (X.dtype, pairs.T * c.d_out), "Yp": (X.dtype, pairs.N * c.d_out),

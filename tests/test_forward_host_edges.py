@@ -79,3 +79,20 @@ def test_a_workspace_is_allocated_on_the_stream_that_uses_it(monkeypatch, name):
     monkeypatch.setattr(L, "_stream", lambda *a: 0)
     call()
     assert scratch == [s]
+
+
+def test_experts_that_share_weights_are_refused():
+    """A W shared over the experts holds one expert's elements: described with
+    the stride of a dense W, the kernels would read past it."""
+    pr = L.Pairs(i32(8), i32(8), torch.zeros(8), 4, 4)
+    X, W = torch.zeros(4, 8), torch.zeros(12, 8)
+    with pytest.raises(ValueError):
+        L.linear_forward(pr, X, "token", W.expand(4, -1, -1))
+    store = torch.zeros(4 * 48 + 96)
+    with pytest.raises(ValueError):  # experts that overlap
+        L.linear_forward(pr, X, "token", store.as_strided((4, 12, 8), (48, 8, 1)))
+    wide = torch.zeros(4, 2, 12, 8)[:, 0]  # a gap between the experts
+    assert L.linear_forward(pr, X, "token", wide).c.w_stride == 192
+    one = L.Pairs(i32(8), i32(8), torch.zeros(8), 4, 1)  # of one expert any stride will do
+    assert L.linear_forward(one, X, "token", W.expand(1, -1, -1)).c.w_stride == 96
+    assert L.linear_forward(one, X, "token", store.as_strided((1, 12, 8), (7, 8, 1))).c.w_stride == 96
