@@ -668,7 +668,8 @@ size_t lrm_pair_grad_workspace_size(const lrm_pair_grad_problem* g);
  * a workspace used by lrm_select, lrm_expert_backward, lrm_receiver_layout,
  * lrm_expert_forward or lrm_pair_grad:
  * LRM_OK, or LRM_ERR_INDEX if an expert index was out of range or token[]
- * was out of range or decreasing (such pairs are treated as absent), or a
+ * was out of range (such pairs are treated as absent) or decreasing (the sums
+ * over a token's pairs, Y and a TOKEN dX, are then undefined), or a
  * replica assignment did not match the kept counts; otherwise
  * LRM_ERR_WORKSPACE if a selection kept more rows than the packed buffers of
  * the call were sized for (a captured call replayed with other quotas); and

@@ -66,12 +66,22 @@ __device__ bool scan_kept_capped(int E, int* mcount, int32_t* out, int64_t cap, 
 }
 
 // tok_off[t] for the tokens t that start at pair p (p in [0, N]): the first
-// pair whose token is >= t.
-__device__ __forceinline__ void token_offsets_at(int64_t p, int N, int T,
+// pair whose token is >= t.  Pairs whose token is out of range start none and are
+// passed over, so that every entry has one writer while the others do not
+// decrease (absent pairs may lie inside a token's run; readers skip them by pos).
+// own: token[p] (not looked at for p = N); before: token[p - 1] (-1 for p = 0).
+// A run of absent pairs is walked back by the pair behind it alone.
+__device__ __forceinline__ void token_offsets_at(int64_t p, int own, int before, int N, int T,
                                                  const int32_t* __restrict__ token,
                                                  int32_t* __restrict__ tok_off) {
-  const int lo = (p == 0) ? 0 : min(max(token[p - 1], -1), T - 1) + 1;
-  const int hi = (p == N) ? T : min(max(token[p], 0), T);
+  const auto in = [T](int t) { return (unsigned)t < (unsigned)T; };
+  const int hi = p == N ? T : own;
+  if (p < N && !in(hi)) return;
+  if (!in(before) && p > 1 && T > 0) {
+#pragma unroll 1
+    for (const int32_t* q = token + p - 1; q != token && !in(before);) before = *--q;
+  }
+  const int lo = in(before) ? before + 1 : 0;
   for (int t = lo; t <= hi; ++t) tok_off[t] = (int32_t)p;
 }
 
@@ -92,11 +102,13 @@ __global__ __launch_bounds__(256) void k_bucket_count(int N, int T, int E, int c
     const int t = token[p];
     if (e < 0 || e >= E) bad |= kErrExpertRange;
     if (t < 0 || t >= T) bad |= kErrTokenRange;
-    if (p > 0 && token[p - 1] > t) bad |= kErrTokenOrder;
+    const int before = p > 0 ? token[p - 1] : -1;
+    if (p > 0 && before > t) bad |= kErrTokenOrder;
     if (e >= 0 && e < E && t >= 0 && t < T) atomicAdd(&hist[e], 1);
-    if (tok_off) token_offsets_at(p, N, T, token, tok_off);
+    if (tok_off) token_offsets_at(p, t, before, N, T, token, tok_off);
   }
-  if (tok_off && p1 == N && threadIdx.x == 0) token_offsets_at(N, N, T, token, tok_off);
+  if (tok_off && p1 == N && threadIdx.x == 0)
+    token_offsets_at(N, T, N > 0 ? token[N - 1] : -1, N, T, token, tok_off);
   // this block's error bits: one word per block, written every call (no
   // zeroing pass); the scan kernel folds them into the call's error word
   __shared__ uint32_t berr;
@@ -354,13 +366,14 @@ __global__ __launch_bounds__(kSelThreads) void k_bucket_one(BucketArgs a) {
   const int tid = threadIdx.x, w = tid >> 6, l = lane_id();
   const int groups = (N + kSelThreads - 1) / kSelThreads;
   const int p0 = w * groups * kWave;
-  int ev[kOneGroups], tv[kOneGroups];
+  int ev[kOneGroups], tv[kOneGroups], pv[kOneGroups];
 #pragma unroll
   for (int u = 0; u < kOneGroups; ++u) {
     const int p = p0 + u * kWave + l;
     const bool in = u < groups && p < N;
     ev[u] = in ? a.expert[p] : -1;
     tv[u] = in ? a.token[p] : -1;
+    pv[u] = in && p > 0 ? a.token[p - 1] : -1;
   }
   for (int i = tid; i < NW * E; i += kSelThreads) cnt[i] = 0;
   if (tid == 0) eor = 0u;
@@ -374,11 +387,11 @@ __global__ __launch_bounds__(kSelThreads) void k_bucket_one(BucketArgs a) {
     const bool ein = ev[u] >= 0 && ev[u] < E, tin = tv[u] >= 0 && tv[u] < T;
     if (!ein) bad |= kErrExpertRange;
     if (!tin) bad |= kErrTokenRange;
-    if (p > 0 && a.token[p - 1] > tv[u]) bad |= kErrTokenOrder;
+    if (p > 0 && pv[u] > tv[u]) bad |= kErrTokenOrder;
     if (ein && tin) atomicAdd(&mine[ev[u]], 1);
-    if (a.tok_off) token_offsets_at(p, N, T, a.token, a.tok_off);
+    if (a.tok_off) token_offsets_at(p, tv[u], pv[u], N, T, a.token, a.tok_off);
   }
-  if (a.tok_off && tid == 0) token_offsets_at(N, N, T, a.token, a.tok_off);
+  if (a.tok_off && tid == 0) token_offsets_at(N, T, a.token[N - 1], N, T, a.token, a.tok_off);
   if (bad) atomicOr(&eor, bad);
   __syncthreads();
   for (int e = tid; e < E; e += kSelThreads) {
@@ -718,7 +731,7 @@ __global__ __launch_bounds__(kSelThreads) void k_select_small(SmallSelArgs a) {
       const bool in = r0 + u < R && p < N;
       exv[u] = in ? a.expert[p] : -1;
       tkv[u] = in ? a.token[p] : 0;
-      tpv[u] = (e == 0 && in && p > 0) ? a.token[p - 1] : 0;
+      tpv[u] = (e == 0 && in && p > 0) ? a.token[p - 1] : -1;
     }
 #pragma unroll
     for (int u = 0; u < kSmallBatch; ++u) {
@@ -736,7 +749,7 @@ __global__ __launch_bounds__(kSelThreads) void k_select_small(SmallSelArgs a) {
         if (valid) atomicAdd(&cnt[ex], 1);
         if (e == 0) {
           if (!valid) a.pos[p] = -1;
-          if (a.tok_off) token_offsets_at(p, N, T, a.token, a.tok_off);
+          if (a.tok_off) token_offsets_at(p, tk, tpv[u], N, T, a.token, a.tok_off);
         }
       }
       const bool hit = valid && ex == e;
@@ -745,7 +758,8 @@ __global__ __launch_bounds__(kSelThreads) void k_select_small(SmallSelArgs a) {
       mine |= (uint64_t)(hit ? 1 : 0) << r;
     }
   }
-  if (e == 0 && tid == 0 && a.tok_off) token_offsets_at(N, N, T, a.token, a.tok_off);
+  if (e == 0 && tid == 0 && a.tok_off)
+    token_offsets_at(N, T, N > 0 ? a.token[N - 1] : -1, N, T, a.token, a.tok_off);
   if (bad) atomicOr(&eor, bad);
   __syncthreads();
   // quotas: device array, or by value, or keep all
@@ -795,7 +809,7 @@ __global__ __launch_bounds__(256) void k_token_offsets(int N, int T,
                                                        int32_t* __restrict__ tok_off) {
   const int64_t p = (int64_t)blockIdx.x * 256 + threadIdx.x;
   if (p > N) return;
-  token_offsets_at(p, N, T, token, tok_off);
+  token_offsets_at(p, p < N ? token[p] : T, p > 0 ? token[p - 1] : -1, N, T, token, tok_off);
 }
 
 // mt_off[e] = sum over e' < e of ceil(M_e' / bm)  (row tiles of the dX GEMM)

@@ -109,3 +109,32 @@ def zero_case(name):
     c["logits"] = z.to(FC.DT[c["dtype"]])
     c["ld"] = E
     return c
+
+
+# ------------------------------------------------------ tokens out of range
+# where: the pairs whose token is out of range, as a share of the list
+BAD_TOKENS = {
+    "middle": (FC._f("linear", 20, 8, 2, 24, 16, residual=True), ((0.5, -1), (0.7, 1 << 20))),
+    "past_t": (FC._f("linear", 20, 8, 2, 24, 16), ((0.5, 20),)),
+    "ends": (FC._f("linear", 20, 8, 2, 24, 16, "f32", residual=True), ((0.0, -5), (0.999, -5))),
+    "runs": (FC._f("linear", 90, 5, 2, 16, 24), ((slice(0.2, 0.4), -1), (slice(0.7, 0.73), 90))),
+    "padded": (FC._f("linear", 90, 5, 2, 16, 24, residual=True), ((slice(0.6, 1.0), -1),)),
+    "padded_high": (FC._f("linear", 90, 5, 2, 16, 24), ((slice(0.6, 1.0), 90),)),
+    "all": (FC._f("linear", 40, 5, 2, 16, 24, residual=True), ((slice(0.0, 1.0), -1),)),
+    "swiglu": (FC._f("swiglu", 60, 5, 2, 24, 16, residual=True), ((0.3, -1), (slice(0.5, 0.6), 60))),
+    "swiglu_few": (FC._f("swiglu", 3, 64, 4, 24, 16), ((0.5, -1), (0.7, 3))),
+    "swiglu_sum": (FC._f("swiglu", 9, 8, 4, 24, 16), ((0.5, -1), (0.7, 9))),
+    "many_blocks": (FC._f("linear", 4500, 7, 2, 16, 8, empty=0.1), ((slice(0.3, 0.5), -1), (0.9, -2))),
+}
+
+
+def bad_token_case(name):
+    case, where = BAD_TOKENS[name]
+    c = FC.build_forward(case, "bad tokens " + name)
+    N, tok = c["N"], c["pairs"]["token"]
+    for at, t in where:
+        if isinstance(at, slice):
+            tok[int(at.start * N):max(int(at.stop * N), int(at.start * N) + 1)] = t
+        else:
+            tok[int(at * N)] = t
+    return c

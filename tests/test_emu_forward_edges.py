@@ -10,7 +10,7 @@ import torch
 
 import forward_cases as FC
 import forward_edges as FE
-from test_emu_forward import call, driver, nbytes, router_nums, stored  # noqa: F401
+from test_emu_forward import FULL, call, driver, held, nbytes, router_nums, stored  # noqa: F401
 
 
 def emu(driver, tmp_path, c, expect=(0, 0), env_extra=None):  # noqa: F811
@@ -46,3 +46,12 @@ def emu_route(driver, tmp_path, c):  # noqa: F811
 def test_emu_zeros_of_both_signs_tie(driver, tmp_path, name):  # noqa: F811
     c = FE.zero_case(name)
     FC.judge_route(c, *emu_route(driver, tmp_path, c))
+
+
+@pytest.mark.parametrize("name", [n for n in FE.BAD_TOKENS if FULL or n != "many_blocks"])
+@pytest.mark.parametrize("path", ["own", "tiles"])
+def test_emu_tokens_out_of_range_are_absent(driver, tmp_path, name, path):  # noqa: F811
+    c = FE.bad_token_case(name)
+    got = emu(driver, tmp_path, c, expect=(0, 8),
+              env_extra={"LRM_FWD_TILE": "64"} if path == "tiles" else None)
+    FC.judge_forward(c, got, {k: held(*v) for k, v in FC.forward_shapes(c).items()})

@@ -64,3 +64,43 @@ def test_workspaces_of_another_stream_are_not_handed_out(L):  # noqa: F811
     assert int(out["out_n"]) == m
     assert torch.equal(out["out_expert"][:m], want[here] - 8)
     assert torch.equal(out["out_token"][:m], (here // k).int())
+
+
+@pytest.mark.parametrize("name", list(FE.BAD_TOKENS))
+@pytest.mark.parametrize("tile", [None, "64", "256"])
+def test_tokens_out_of_range_are_absent(L, monkeypatch, name, tile):  # noqa: F811
+    if tile:
+        monkeypatch.setenv("LRM_FWD_TILE", tile)
+    c = dict(FE.bad_token_case(name), bad=True)
+    out, before = run_forward(L, c)
+    FC.judge_forward(c, out, before)
+
+
+@pytest.mark.parametrize("one_launch", ["0", "1"])
+@pytest.mark.parametrize("name", ["middle", "runs", "padded", "many_blocks"])
+def test_backward_of_tokens_out_of_range(L, monkeypatch, name, one_launch):  # noqa: F811
+    """dX of a call with absent pairs equals that of the call without them (both
+    keep every pair: every row's sums have the same terms in the same order)."""
+    monkeypatch.setenv("LRM_SELECT_ONE_LAUNCH", one_launch)
+    c = FE.bad_token_case(name)
+    T, E, N, bf = c["T"], c["E"], c["N"], torch.bfloat16
+    g = FC.gen("bad tokens back", name)
+    G = FC.normal(g, T, c["d"], dtype=bf)
+    X, W = c["X"].to(bf).contiguous(), c["W"].to(bf)
+    p = c["pairs"]
+    here = (p["token"] >= 0) & (p["token"] < T)
+
+    def back(pick):
+        pr = L.Pairs(*(dev(torch.from_numpy(p[k][pick])) for k in ("token", "expert", "weight")), T, E)
+        pb = L.linear_problem(pr, dev(X), "token", dev(G), "token", dev(W), [N] * E)
+        out = dict(dW=filled((E, c["d"], c["d_in"]), torch.float32),
+                   dX=filled((T, c["d_in"]), torch.float32))
+        ws = L.lrm_expert_backward(pb, out)
+        torch.cuda.synchronize()
+        return out, L.lrm_check_device_errors(ws)
+
+    got, status = back(np.ones(N, bool))
+    want, ok = back(here)
+    assert (status, ok) == (L.LRM_ERR_INDEX, L.LRM_OK)
+    assert torch.equal(got["dX"], want["dX"])
+    assert float((got["dW"] - want["dW"]).abs().max()) <= 1e-5 * float(want["dW"].abs().max())
