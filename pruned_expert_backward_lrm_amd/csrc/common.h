@@ -94,11 +94,12 @@ __device__ __forceinline__ int64_t pair_row(int rows_is_pair, const int32_t* tok
 __device__ __forceinline__ float sigmoidf_acc(float a) { return 1.0f / (1.0f + expf(-a)); }
 
 // 1 / (1 + e^-a) from the hardware's exp2 and reciprocal with one Newton step:
-// relative error about (|a| + 2) 2^-24; e^-a is held below 2^126.
+// relative error about (|a| + 2) 2^-24; 0 below -87 (e^-a of 2^126 and more), so
+// that a times it is, for the largest a too.
 __device__ __forceinline__ float sigmoid_of(float a) {
-  const float d = 1.f + __builtin_amdgcn_exp2f(fminf(a * -1.44269504f, 126.f));
+  const float d = 1.f + __builtin_amdgcn_exp2f(a * -1.44269504f);
   const float r = __builtin_amdgcn_rcpf(d);
-  return fmaf(r, fmaf(-d, r, 1.f), r);
+  return a < -87.f ? 0.f : fmaf(r, fmaf(-d, r, 1.f), r);
 }
 
 // Phi(z), the normal distribution function, and e = e^(-z^2/2), which both GELU
@@ -127,7 +128,7 @@ constexpr int kActNone = 0, kActRelu = 1, kActGelu = 2, kActSilu = 3;
 template <int ACT, bool FAST>
 __device__ __forceinline__ void act_both(float z, float& y, float& g) {
   if constexpr (ACT == kActRelu) {
-    y = z > 0.f ? z : 0.f;
+    y = z <= 0.f ? 0.f : z;  // (NaN stays NaN)
     g = z > 0.f ? 1.f : 0.f;
   } else if constexpr (ACT == kActGelu) {
     float e, phi;
@@ -152,6 +153,8 @@ template <int ACT, bool FAST>
 __device__ __forceinline__ float act_of(float z) {
   float y, g;
   act_both<ACT, FAST>(z, y, g);
+  // (Phi(z) is 1 there, and its polynomial no number for an infinite z)
+  if constexpr (ACT == kActGelu && FAST) y = z > 64.f ? z : y;
   return y;
 }
 

@@ -30,19 +30,26 @@ __device__ __forceinline__ float act_rt(int act, float z) {
 // y between the down product and the join takes 24 bits: its bf16 rounding
 // (which is Yp where the caller wants it) and the next 8 bits, a signed byte of
 // the difference of the bit patterns.  With bf16 alone Y would carry two
-// roundings of half the terms' size on top of its own.  The lowest bit is set
-// first, so that no value lies half-way between two bf16 values: the byte is
-// then bits 8 .. 15 themselves, read as signed.  The join adds half of the last
-// place: 2^-16 of the value at most.
-__device__ __forceinline__ float odd(float y) { return __uint_as_float(__float_as_uint(y) | 1u); }
+// roundings of half the terms' size on top of its own.  A value half-way between
+// two bf16 values goes away from zero, so that the byte is bits 8 .. 15
+// themselves, read as signed.  The join adds half of the last place: 2^-16 of
+// the value at most.  An infinity (a sum past fp32) stays one: no finite value
+// leaves its 16 bits above a byte of zero.  A NaN stays one, since its low 16 bits
+// are zero: they come from bf16 inputs or the hardware's own.
+__device__ __forceinline__ uint32_t away_bf16x2(float lo, float hi) {
+  return __builtin_amdgcn_perm(__float_as_uint(hi) + 0x8000u, __float_as_uint(lo) + 0x8000u, 0x07060302u);
+}
 // bits 8 .. 15 of four values
 __device__ __forceinline__ uint32_t next_bytes(f32x4 y) {
   const uint32_t lo = __builtin_amdgcn_perm(__float_as_uint(y[1]), __float_as_uint(y[0]), 0x00000501u);
   const uint32_t hi = __builtin_amdgcn_perm(__float_as_uint(y[3]), __float_as_uint(y[2]), 0x00000501u);
   return (lo & 0xffffu) | hi << 16;
 }
+// INF: an infinity stays one (otherwise it becomes a NaN)
+template <bool INF>
 __device__ __forceinline__ float join_bits(uint32_t hi16, int lo8) {
-  return __uint_as_float((hi16 << 16) + (uint32_t)(lo8 * 256 + 128));
+  const uint32_t u = (hi16 << 16) + (uint32_t)(lo8 * 256);
+  return __uint_as_float(INF && (u << 1) == 0xff000000u ? u : u + 128u);
 }
 
 // act of a wave's row of fragments; one loop over registers for each kind
@@ -369,11 +376,8 @@ __device__ __forceinline__ int fwd_store(const FwdGemmArgs& g, const FwdJob& job
         if (!EPI || g.Y) {
           if (EPI && g.act != kActNone) act_rows<FO, true>(g.act, u);
 #pragma unroll
-          for (int j = 0; j < FO; ++j) {
-#pragma unroll
-            for (int q = 0; q < 4; ++q) u[j][q] = odd(u[j][q]);
-            v[j] = pack4(u[j]);
-          }
+          for (int j = 0; j < FO; ++j)
+            v[j] = u32x2{away_bf16x2(u[j][0], u[j][1]), away_bf16x2(u[j][2], u[j][3])};
           put(g.Y, v);
           if (g.Ylo) {
             // 16 rows of FO * 16 bytes: lane l holds 16 columns of row l / FO
@@ -698,28 +702,39 @@ __global__ __launch_bounds__(256) void k_fwd_join(FwdJoinArgs a) {
   const int p1 = min(max(a.tok_off[t + 1], p0), a.N);
   if (c >= a.d) return;
   Vec<BF16> sum;
-#pragma unroll
-  for (int j = 0; j < V; ++j) sum.v[j] = 0.f;
-  if (a.R) sum = Vec<BF16>::load(a.R, (int64_t)t * a.ldr + c);
   float (&acc)[V] = sum.v;
-  for (int p = p0; p < p1; ++p) {
-    if (a.pos[p] < 0) continue;
-    const float w = a.weight[p];
-    const int64_t at = (int64_t)p * a.d + c;
-    if constexpr (BF16) {
-      const u32x4 x = *reinterpret_cast<const u32x4*>((const uint16_t*)a.Y + at);
-      const u32x2 lo = *reinterpret_cast<const u32x2*>(a.Ylo + at);
+  auto add_up = [&](auto inf) {
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const uint32_t hi = (x[j >> 1] >> (16 * (j & 1))) & 0xffffu;
-        const int l8 = (int)(int8_t)(lo[j >> 2] >> (8 * (j & 3)));
-        acc[j] = fmaf(w, join_bits(hi, l8), acc[j]);
+    for (int j = 0; j < V; ++j) acc[j] = 0.f;
+    if (a.R) sum = Vec<BF16>::load(a.R, (int64_t)t * a.ldr + c);
+    for (int p = p0; p < p1; ++p) {
+      if (a.pos[p] < 0) continue;
+      const float w = a.weight[p];
+      const int64_t at = (int64_t)p * a.d + c;
+      if constexpr (BF16) {
+        const u32x4 x = *reinterpret_cast<const u32x4*>((const uint16_t*)a.Y + at);
+        const u32x2 lo = *reinterpret_cast<const u32x2*>(a.Ylo + at);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          const uint32_t hi = (x[j >> 1] >> (16 * (j & 1))) & 0xffffu;
+          const int l8 = (int)(int8_t)(lo[j >> 2] >> (8 * (j & 3)));
+          acc[j] = fmaf(w, join_bits<inf>(hi, l8), acc[j]);
+        }
+      } else {
+        const f32x4 x = *reinterpret_cast<const f32x4*>((const float*)a.Y + at);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) acc[j] = fmaf(w, x[j], acc[j]);
       }
-    } else {
-      const f32x4 x = *reinterpret_cast<const f32x4*>((const float*)a.Y + at);
-#pragma unroll
-      for (int j = 0; j < 4; ++j) acc[j] = fmaf(w, x[j], acc[j]);
     }
+  };
+  add_up(std::false_type());
+  if constexpr (BF16) {
+    // a NaN may have been an infinity: once more (the test for one in every term
+    // took 5 us of the 1450 of a 16384-token call)
+    bool nan = false;
+#pragma unroll
+    for (int j = 0; j < V; ++j) nan |= acc[j] != acc[j];
+    if (nan) add_up(std::true_type());
   }
   sum.store(a.out, (int64_t)t * a.d + c);
 }

@@ -138,3 +138,43 @@ def bad_token_case(name):
         else:
             tok[int(at * N)] = t
     return c
+
+
+# ------------------------------------------- products past fp32, and no numbers
+# Column 0 of some tokens is huge, and so is some weight rows' column 0: their
+# product passes fp32 (upwards only where the activation of -inf is no number).
+# One token holds a NaN.
+OVERFLOW = {
+    "none": FC._f("linear", 90, 5, 2, 16, 24, residual=True),
+    "relu": FC._f("linear", 90, 5, 2, 16, 40, act="relu", bias=True),
+    "gelu": FC._f("linear", 90, 5, 2, 24, 24, act="gelu"),
+    "silu": FC._f("linear", 90, 5, 2, 16, 24, act="silu", residual=True),
+    "f32": FC._f("linear", 90, 5, 2, 16, 24, "f32", act="relu", residual=True),
+    "gelu_f32": FC._f("linear", 90, 5, 2, 16, 24, "f32", act="gelu"),
+    "few": FC._f("linear", 9, 5, 2, 16, 24, act="relu"),
+}
+
+
+def overflow_case(name):
+    c = FC.build_forward(OVERFLOW[name], "overflow " + name)
+    c["X_store"][1::4, 0] = 3e38
+    c["W"][:, ::5, 0] = 4.0
+    if c["act"] in ("none", "relu"):
+        c["W"][:, 1::5, 0] = -4.0
+    c["X_store"][2, 3] = float("nan")
+    return c
+
+
+def judge_overflow(c, got):
+    """Z, Yp and Y: infinities and NaN where the formula in fp32 has them; the
+    finite ones in coarse bounds (the other tests have the fine ones)."""
+    ref = OF.forward("linear", c["pairs"], c["T"], c["E"], c["X"], W=c["W"], bias=c["bias_t"],
+                     act_name=c["act"], residual=c["R"])
+    for k in ("Z", "Yp", "Y"):
+        want, v = ref[k].float(), got[k].cpu().float()
+        assert torch.isinf(want).any() and torch.isnan(want).any()
+        assert torch.equal(torch.isnan(v), torch.isnan(want)), k
+        inf = torch.isinf(want)
+        assert torch.equal(v[inf], want[inf]) and not torch.isinf(v[~inf]).any(), k
+        fin = torch.isfinite(want)
+        assert ((v - want).abs()[fin] <= 2.0 ** -6 * (want.abs()[fin] + 1)).all(), k

@@ -55,3 +55,25 @@ def test_emu_tokens_out_of_range_are_absent(driver, tmp_path, name, path):  # no
     got = emu(driver, tmp_path, c, expect=(0, 8),
               env_extra={"LRM_FWD_TILE": "64"} if path == "tiles" else None)
     FC.judge_forward(c, got, {k: held(*v) for k, v in FC.forward_shapes(c).items()})
+
+
+@pytest.mark.parametrize("name", list(FE.OVERFLOW))
+def test_emu_overflow_stays_infinite(driver, tmp_path, name):  # noqa: F811
+    c = FE.overflow_case(name)
+    FE.judge_overflow(c, emu(driver, tmp_path, c))
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_emu_relu_keeps_nan(driver, tmp_path, dtype):  # noqa: F811
+    c = FC._g(12, 3, 2, 24, dtype, act="relu")
+    c.update(pairs=FC.make_pairs(12, 3, 2, 1), N=24)
+    g, dt = FC.gen("relu nan"), FC.DT[dtype]
+    c["Z"], c["dY"] = FC.normal(g, 24, 24, dtype=dt), FC.normal(g, 12, 24, dtype=dt)
+    c["Z"][5, 7] = float("nan")
+    pr, f32 = c["pairs"], torch.float32
+    nums = [4, 12, 24, 3, 0, int(dtype == "bf16"), 1, 0, 24, 0, 24, 24, 0, 4 * 24,
+            nbytes((24, 24), dt), -1]
+    dw, G = call(driver, tmp_path, nums, [pr["token"], pr["expert"], pr["weight"], c["dY"], c["Z"]],
+                 [((24,), f32), ((24, 24), dt)])
+    assert torch.isnan(dw).nonzero()[:, 0].tolist() == [5]
+    assert G[5, 7] == 0 and not torch.isnan(G).any()

@@ -104,3 +104,13 @@ def test_backward_of_tokens_out_of_range(L, monkeypatch, name, one_launch):  # n
     assert (status, ok) == (L.LRM_ERR_INDEX, L.LRM_OK)
     assert torch.equal(got["dX"], want["dX"])
     assert float((got["dW"] - want["dW"]).abs().max()) <= 1e-5 * float(want["dW"].abs().max())
+
+
+@pytest.mark.parametrize("tile", [None, "128", "256"])
+@pytest.mark.parametrize("name", list(FE.OVERFLOW))
+def test_overflow_stays_infinite(L, monkeypatch, name, tile):  # noqa: F811
+    if tile:
+        monkeypatch.setenv("LRM_FWD_TILE", tile)
+    c = FE.overflow_case(name)
+    out, _ = run_forward(L, c)
+    FE.judge_overflow(c, out)
