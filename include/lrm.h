@@ -502,7 +502,9 @@ int64_t lrm_max_kept(int32_t N, int32_t E, const int32_t* quota);
  *     be NaN or infinite).  A row may leave no expert.
  *   scores: s_e = softmax of z over the eligible experts, or sigmoid(z_e)
  *   keys:   c_e = s_e + bias[e]; the bias (a load-balancing term) takes part in
- *     the choice only
+ *     the choice only.  An expert with a bias of -inf is neither chosen nor
+ *     counted for its group (it stays in the softmax; expert_mask takes it out of
+ *     that too, and costs nothing); other biases must be finite
  *   groups: with n_group > 1 the experts form n_group runs of E / n_group; a
  *     group's score is the largest key of its eligible experts
  *     (LRM_GROUP_MAX) or the sum of the two largest (LRM_GROUP_TOP2; of the

@@ -42,6 +42,8 @@ def route(logits, k, score="softmax", renorm=True, scale=1.0, n_group=1, topk_gr
         s = _scores(row, on, score)
         # without a bias the exact scores order like the logits
         key = row if b is None else [s[e] + b[e] for e in range(E)]
+        if b is not None:  # a bias of -inf closes its expert to the choice
+            on = [on[e] and b[e] > -math.inf for e in range(E)]
         if n_group > 1:
             per = E // n_group
             best = []

@@ -19,7 +19,8 @@
 // are exact.  With a bias, and for sums of two scores, the keys are first
 // formed in fp32; their error is below kKeyTol (1 + |key|/8), so a token whose
 // neighbouring keys are further apart than that is decided.  The others (a few
-// per mille) are chosen again from keys formed in fp64.
+// per mille; all, where a bias is -inf: Fixed has no scale then) are chosen again
+// from keys formed in fp64.
 #include "common.h"
 #include "launch.h"
 

@@ -178,3 +178,30 @@ def judge_overflow(c, got):
         assert torch.equal(v[inf], want[inf]) and not torch.isinf(v[~inf]).any(), k
         fin = torch.isfinite(want)
         assert ((v - want).abs()[fin] <= 2.0 ** -6 * (want.abs()[fin] + 1)).all(), k
+
+
+# ------------------------------------------------- biases of minus infinity
+# They close an expert to the choice alone.
+CLOSED = {
+    "few_left": dict(T=30, E=16, k=4, dtype="f32", score="sigmoid", open=3),
+    "some": dict(T=30, E=40, k=4, dtype="bf16", score="sigmoid", open=30),
+    "softmax": dict(T=30, E=40, k=4, dtype="f32", open=20, renorm=False),
+    "groups": dict(T=30, E=64, k=4, dtype="f32", score="sigmoid", open=20, n_group=8, topk_group=2),
+    "groups_max": dict(T=30, E=60, k=4, dtype="bf16", open=20, n_group=10, topk_group=2,
+                       group_rule="max"),
+    "wide": dict(T=8, E=600, k=6, dtype="f32", score="sigmoid", open=300),
+    "none_left": dict(T=8, E=16, k=2, dtype="f32", open=0),
+}
+
+
+def closed_case(name):
+    c = dict(score="softmax", renorm=True, scale=1.0, n_group=1, topk_group=1, group_rule="top2")
+    c.update(CLOSED[name])
+    T, E = c["T"], c["E"]
+    g = FC.gen("closed", name)
+    c["logits"] = FC.normal(g, T, E, std=2.0, dtype=FC.DT[c["dtype"]])
+    c["bias_t"] = FC.normal(g, E, std=0.3)
+    c["bias_t"][torch.randperm(E, generator=g)[c["open"]:]] = -float("inf")
+    c["tmask"] = c["emask"] = None
+    c["ld"] = E
+    return c

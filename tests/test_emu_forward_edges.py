@@ -77,3 +77,9 @@ def test_emu_relu_keeps_nan(driver, tmp_path, dtype):  # noqa: F811
                  [((24,), f32), ((24, 24), dt)])
     assert torch.isnan(dw).nonzero()[:, 0].tolist() == [5]
     assert G[5, 7] == 0 and not torch.isnan(G).any()
+
+
+@pytest.mark.parametrize("name", list(FE.CLOSED))
+def test_emu_bias_of_minus_infinity_closes_an_expert(driver, tmp_path, name):  # noqa: F811
+    c = FE.closed_case(name)
+    FC.judge_route(c, *emu_route(driver, tmp_path, c))

@@ -3,9 +3,11 @@ and the epilogue's backward pass (see test_forward_host)."""
 
 import contextlib
 
+import numpy as np
 import pytest
 import torch
 
+from oracle import forward as OF
 from pruned_expert_backward_lrm_amd import lrm as L
 
 
@@ -96,3 +98,18 @@ def test_experts_that_share_weights_are_refused():
     one = L.Pairs(i32(8), i32(8), torch.zeros(8), 4, 1)  # of one expert any stride will do
     assert L.linear_forward(one, X, "token", W.expand(1, -1, -1)).c.w_stride == 96
     assert L.linear_forward(one, X, "token", store.as_strided((1, 12, 8), (7, 8, 1))).c.w_stride == 96
+
+
+def test_bias_of_minus_infinity_by_hand():
+    """Expert 1 is closed: not chosen, nor counted for its group, but part of the
+    softmax."""
+    z, b = torch.tensor([[0.0, 2.0, 1.0, 0.0]]), torch.tensor([0.0, -float("inf"), 0.0, 0.0])
+    e, w = OF.route(z, 4, renorm=False, bias=b)
+    s = torch.softmax(z[0].double(), 0)
+    assert e.tolist() == [2, 0, 3, -1]
+    assert np.allclose(w, [float(s[2]), float(s[0]), float(s[3]), 0.0])
+    e, _ = OF.route(z, 2, n_group=2, topk_group=1, group_rule="max", bias=b)
+    assert e.tolist() == [2, 3]
+    e, _ = OF.route(torch.tensor([[0.6, 2.0, 0.0, -9.0]]), 2, score="sigmoid", n_group=2, topk_group=1,
+                    bias=b)
+    assert e.tolist() == [0, -1]

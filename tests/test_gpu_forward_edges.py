@@ -114,3 +114,9 @@ def test_overflow_stays_infinite(L, monkeypatch, name, tile):  # noqa: F811
     c = FE.overflow_case(name)
     out, _ = run_forward(L, c)
     FE.judge_overflow(c, out)
+
+
+@pytest.mark.parametrize("name", list(FE.CLOSED))
+def test_bias_of_minus_infinity_closes_an_expert(L, name):  # noqa: F811
+    c = FE.closed_case(name)
+    FC.judge_route(c, *gpu_route(L, c))
