@@ -175,9 +175,18 @@ def _ptr(t) -> int | None:
     return t.data_ptr()
 
 
-def _stream(stream=None) -> int:
+def _stream(stream=None, device=None) -> int:
+    """The stream's handle; device: where the call's tensors are, which has to be
+    the current GPU and the stream's."""
     if stream is None:
+        if device is not None and device.index is None:
+            raise ValueError(f"the tensors are on {device}, not on a GPU")
         stream = torch.cuda.current_stream()
+        if device is not None and stream.device_index != device.index:
+            raise ValueError(f"the tensors are on {device}, which is not the current device")
+    elif device is not None and not stream.device_index == device.index == torch.cuda.current_device():
+        raise ValueError(f"the tensors are on {device}: not a GPU, not the current device, or not "
+                         "the stream's device")
     return stream.cuda_stream
 
 
@@ -232,9 +241,7 @@ def _scratch(nbytes: int, device, stream):
 
 
 def _ws(nbytes: int, device, ws, stream=None):
-    if ws is not None:
-        return ws
-    return _scratch(max(int(nbytes), 256), device, stream)
+    return ws if ws is not None else _scratch(max(int(nbytes), 256), device, stream)
 
 
 def _quota_arr(q):
@@ -519,7 +526,7 @@ def lrm_route(r: Router, expert, weight, token=None, counts=None, ws=None, strea
     if counts is not None:
         ws = _ws(r.ws_bytes, counts.device, ws, stream)
     _check(_lib.lrm_route(C.byref(r.c), _ptr(expert), _ptr(weight), _ptr(token), _ptr(counts),
-                          _ptr(ws), ws.numel() if ws is not None else 0, _stream(stream)),
+                          _ptr(ws), ws.numel() if ws is not None else 0, _stream(stream, on)),
            "lrm_route")
 
 
@@ -535,7 +542,7 @@ def lrm_route_bwd(r: Router, expert, dweight, dlogits: torch.Tensor, stream=None
                          "on the logits' device")
     ldd = dlogits.stride(0) if r.T > 1 else max(dlogits.stride(0), r.E)
     _check(_lib.lrm_route_bwd(C.byref(r.c), _ptr(expert), _ptr(dweight), _ptr(dlogits), ldd,
-                              _stream(stream)), "lrm_route_bwd")
+                              _stream(stream, r.device)), "lrm_route_bwd")
 
 
 def lrm_route_share(T: int, k: int, expert, weight, e0: int, E: int, out_token, out_expert,
@@ -553,7 +560,7 @@ def lrm_route_share(T: int, k: int, expert, weight, e0: int, E: int, out_token, 
     _check(_lib.lrm_route_share(int(T), int(k), _ptr(expert), _ptr(weight), int(e0), int(E),
                                 _ptr(out_token), _ptr(out_expert), _ptr(out_weight),
                                 _ptr(out_slot), _ptr(out_n), _ptr(ws), ws.numel(),
-                                _stream(stream)), "lrm_route_share")
+                                _stream(stream, out_n.device)), "lrm_route_share")
 
 
 # ------------------------------------------------------ the experts forward
@@ -673,7 +680,8 @@ def lrm_expert_forward(f: Forward, outputs, ws=None, stream=None):
     if ws is None:
         ws = _grown(lrm_forward_workspace_size(f), f.pairs.token.device, stream)
     _check(_lib.lrm_expert_forward(C.byref(f.c), C.byref(o), _ptr(ws),
-                                   ws.numel() if ws is not None else 0, _stream(stream)),
+                                   ws.numel() if ws is not None else 0,
+                                   _stream(stream, f.pairs.token.device)),
            "lrm_expert_forward")
     return ws
 
@@ -715,6 +723,7 @@ def lrm_pair_grad(g: PairGrad, outputs, ws=None, stream=None):
     if ws is None:
         ws = _grown(lrm_pair_grad_workspace_size(g), g.pairs.token.device, stream)
     _check(_lib.lrm_pair_grad(C.byref(g.c), C.byref(o), _ptr(ws),
-                              ws.numel() if ws is not None else 0, _stream(stream)),
+                              ws.numel() if ws is not None else 0,
+                              _stream(stream, g.pairs.token.device)),
            "lrm_pair_grad")
     return ws

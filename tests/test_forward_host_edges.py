@@ -19,7 +19,7 @@ class FakeLibrary:
 
 
 class FakeStream:
-    cuda_stream = 0
+    cuda_stream, device_index = 0, 0
 
 
 def i32(*shape):
@@ -113,3 +113,32 @@ def test_bias_of_minus_infinity_by_hand():
     e, _ = OF.route(torch.tensor([[0.6, 2.0, 0.0, -9.0]]), 2, score="sigmoid", n_group=2, topk_group=1,
                     bias=b)
     assert e.tolist() == [0, -1]
+
+
+@pytest.mark.parametrize("name", ["lrm_route", "lrm_route_bwd", "lrm_route_share", "lrm_expert_forward",
+                                  "lrm_pair_grad"])
+def test_tensors_in_host_memory_are_refused(monkeypatch, name):
+    """The library would hand their addresses to the GPU."""
+    X, n = torch.zeros(4, 8), i32(8)
+    calls = dict(every_call(None), lrm_route_bwd=lambda: L.lrm_route_bwd(L.Router(X, 2), n,
+                                                                         torch.zeros(8), X))
+    monkeypatch.setattr(L, "_lib", FakeLibrary())
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda *a: FakeStream())
+    with pytest.raises(ValueError, match="GPU"):
+        calls[name]()
+    with pytest.raises(ValueError, match="GPU"):
+        L._stream(FakeStream(), X.device)
+
+
+def test_a_call_on_another_device_is_refused(monkeypatch):
+    class On(FakeStream):
+        def __init__(self, index):
+            self.device_index = index
+
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda *a: On(0))
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
+    here, there = torch.device("cuda", 0), torch.device("cuda", 1)
+    assert L._stream(None, here) == 0 and L._stream(On(0), here) == 0 and L._stream(On(1)) == 0
+    for stream, device in ((None, there), (On(1), here), (On(1), there), (On(0), there)):
+        with pytest.raises(ValueError, match="device"):
+            L._stream(stream, device)
