@@ -156,10 +156,18 @@ bool few_pairs(const lrm_pairs* p) {
   return p->N <= kFewPairs && p->T <= 65535 && p->N <= (int64_t)kFewRows * p->E;
 }
 // Few enough that a token's pairs are joined where they are multiplied, each
-// token reading its experts' weights on its own (the same layer: 1 token 20 us
-// against 29 with the products and the sum apart, 2 tokens 32 against 53, 4
-// tokens 63 against 64; a lone token shares no expert).
-bool few_join(const lrm_pairs* p) { return p->T == 1 || (int64_t)p->N * 4 <= p->E; }
+// token reading its experts' weights on its own, a block for 8 columns of every
+// token (a token should bring two of its eight waves a pair, and one without
+// pairs brings none: 2 T <= N; a lone token shares no expert).  Joined against the
+// products and the sum apart, us, weights from memory:
+//   128 experts, 2048/768: 1 token of 8 pairs 35 and 40, 2 tokens 51 and 57, 4
+//     tokens 84 and 87; 4 tokens of 2 pairs 39 and 38, of 1 pair 31 and 27
+//   32 experts, 4096/1408: 1 token of 8 pairs 70 and 75; 2 of 1 pair 42 and 37
+//   64 experts, 1024/512: 4 tokens of 4 pairs 25 and 30
+//   8 pairs among 4096 tokens (128 experts, 2048/768): 2392 and 30
+bool few_join(const lrm_pairs* p) {
+  return p->T == 1 || ((int64_t)p->N * 4 <= p->E && 2ll * p->T <= p->N);
+}
 
 struct FwdWs {
   BucketWs b;

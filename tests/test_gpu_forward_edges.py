@@ -120,3 +120,40 @@ def test_overflow_stays_infinite(L, monkeypatch, name, tile):  # noqa: F811
 def test_bias_of_minus_infinity_closes_an_expert(L, name):  # noqa: F811
     c = FE.closed_case(name)
     FC.judge_route(c, *gpu_route(L, c))
+
+
+@pytest.mark.parametrize("T", [65535, 65536])
+def test_few_pairs_among_many_tokens(L, T):  # noqa: F811
+    """A GPU's share of a batch may hold next to nothing: the tokens without pairs
+    cost what a copy of the residual costs, not a product each."""
+    case = FC._f("swiglu", 3, 32, 2, 2048, 64, residual=True, outs=("Y",))
+    c = FC.build_forward(case, "few among many")
+    where = np.array([5, 40000, T - 1])
+    pr = dict(c["pairs"], token=where[c["pairs"]["token"]].astype(np.int32))
+    bf = torch.bfloat16
+    X, R = torch.zeros(T, 2048, dtype=bf, device=DEV), torch.randn(T, 2048, device=DEV).to(bf)
+    at = dev(torch.from_numpy(where))
+    X[at], R[at] = dev(c["X"]), dev(c["R"])
+    pairs = L.Pairs(*(dev(torch.from_numpy(pr[k])) for k in ("token", "expert", "weight")), T, 32)
+    f = L.swiglu_forward(pairs, X, *(dev(c[w]) for w in ("W_gate", "W_up", "W_down")), residual=R)
+    Y = filled((T, 2048), bf)
+    ws = L.lrm_expert_forward(f, dict(Y=Y))
+    torch.cuda.synchronize()
+    FC.judge_forward(c, dict(Y=Y[at]))
+    rest = torch.ones(T, dtype=torch.bool, device=DEV)
+    rest[at] = False
+    assert torch.equal(Y[rest], R[rest])
+
+    def best_of(call):
+        times = []
+        for _ in range(5):
+            a, b = (torch.cuda.Event(enable_timing=True) for _ in range(2))
+            a.record()
+            call()
+            b.record()
+            torch.cuda.synchronize()
+            times.append(a.elapsed_time(b))
+        return min(times)
+
+    copy = best_of(lambda: Y.copy_(R))
+    assert best_of(lambda: L.lrm_expert_forward(f, dict(Y=Y), ws=ws)) < 20 * copy + 0.2
