@@ -592,8 +592,8 @@ typedef enum lrm_act { LRM_ACT_NONE = 0, LRM_ACT_RELU = 1, LRM_ACT_GELU = 2, LRM
  * with e the expert of p.  bf16 runs on MFMA with fp32 accumulation, fp32 in
  * fp32; silu(a) b is rounded to the inputs' dtype between the two products
  * (held in fp32 where Y is wanted of one token's pairs, at most 64 of them, or of
- * at most E / 4 pairs, two or more a token on average); bias, activation, weights, the sum
- * over pairs and the residual are fp32 and rounded once. */
+ * at most E / 4 pairs, two or more a token on average); bias, activation,
+ * weights, the sum over pairs and the residual are fp32 and rounded once. */
 typedef struct lrm_forward {
   int32_t kind;  /* lrm_kind */
   int32_t act;   /* lrm_act (LINEAR; NONE for SWIGLU) */

@@ -155,14 +155,16 @@ __device__ __forceinline__ void emit(const FwdGemmArgs& g, int e, int m, int p, 
 // 1.5 stages before they are needed (96 KB in flight per CU).  Waits name how
 // many younger memory instructions may stand (the counter retires in order), so
 // that neither the loads behind a part nor a finished tile's stores are waited
-// for.  The down product (768 x 2048, 131072 rows) takes 546 us, with four
-// stages of 64 bytes it took 647; 200 us of it go to 805 MB of stores that the
-// loads of the next tile cannot pass in that counter.
+// for.  The down product (768 x 2048, 131072 rows) takes 534 us, with four
+// stages of 64 bytes it took 647.  A copy without its 805 MB of stores took 406 us
+// when it took 546, one that stores to a few lines in the L2 505: 100 us are the
+// store code's, 40 the memory's.  The matrix pipes are busy 43 % of its cycles,
+// and 60 % of the gate/up product's.
 //
 // Persistent blocks: each XCD (block b runs on XCD b mod 8) owns a contiguous
 // eighth of the tiles, in which an expert's tiles lie 8 row tiles high, column
 // by column, so that the tiles running on it at a time share operand panels in
-// its L2 (1.24 GB fetched for 0.8 GB of weights and 0.54 GB of gathered rows).
+// its L2 (1.09 GB fetched for 0.8 GB of weights and rows gathered 8 times from 67 MB).
 //
 // fp32 runs v_mfma_f32_16x16x4: a lane's 16-byte granule holds four k, and
 // step s multiplies the s-th of every lane.  Which k those are is the same for

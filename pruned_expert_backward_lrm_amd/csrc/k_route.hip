@@ -11,8 +11,8 @@
 // complement below it (16 bits of each for bf16 logits, 32 otherwise), so that
 // one maximum over the lanes decides key and tie; every lane sorts its 8 once
 // and a round only compares the lanes' heads (65536 tokens, 128 experts, top-8:
-// 11.3 us, and 3.9 for the counts, instead of 26 with a search of all 8 every
-// round; 273 vector instructions for four tokens bound it).  Larger rows and
+// 11.8 us, and 3.8 for the counts, instead of 26 with a search of all 8 every
+// round; 271 vector instructions for four tokens, 7 us of issue).  Larger rows and
 // fp64 keys take the maximum key, then the minimum expert among its holders.
 //
 // Order of the choice: without a bias the scores order like the logits, which
@@ -637,7 +637,7 @@ __device__ __forceinline__ float chosen_weight(const RouteArgs& a, bool has, flo
 // bf16 logits that are the keys as they are (no bias, no groups), in aligned
 // rows of whole lanes: keys straight from the words, weights from the keys.
 // (A kernel of its own: as a branch of k_route the scalar registers spill, and
-// the 65536-token call took 14.2 us instead of 11.3.)
+// the 65536-token call took 14.2 us when this took 11.3.)
 template <int LPT>
 __global__ __launch_bounds__(kRouteThreads) void k_route_direct(RouteArgs a) {
   LRM_DYN_SHARED(int, hist);
@@ -827,6 +827,12 @@ __global__ __launch_bounds__(1024) void k_route_counts(int nblk, int E, const in
 }
 
 // ------------------------------------------------------------- backward
+// 65536 tokens, 128 experts, top-8, bf16, renormalised: 12.4 us; 377 vector
+// instructions for four tokens, about half of them in the comparisons that spread
+// the k slots over a lane's columns, are 10 us of issue.  Where every logit has a
+// gradient and the rows are not 16-byte aligned (15001 x 161 fp32: 18.6 us), a
+// lane's 8 neighbouring columns take a load and a store each, and the row's lines
+// are asked for 8 times: 1.24 M write requests for 9.7 MB.
 template <int LPT, int NV>
 __global__ __launch_bounds__(kRouteThreads) void k_route_bwd(RouteArgs a, const int32_t* expert,
                                                              const float* dweight, void* dlogits,
