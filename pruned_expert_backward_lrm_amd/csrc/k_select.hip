@@ -70,19 +70,42 @@ __device__ bool scan_kept_capped(int E, int* mcount, int32_t* out, int64_t cap, 
 // passed over, so that every entry has one writer while the others do not
 // decrease (absent pairs may lie inside a token's run; readers skip them by pos).
 // own: token[p] (not looked at for p = N); before: token[p - 1] (-1 for p = 0).
-// A run of absent pairs is walked back by the pair behind it alone.
+// A run of absent pairs is walked back by the pair behind it alone.  Long runs of
+// tokens without pairs (the padding behind a batch, a share that holds next to
+// nothing) are noted for the workgroup (fill_gaps), as far as there is room: one
+// thread writes 40 entries a microsecond.
+struct TokenGaps {
+  static constexpr int kLong = 64, kRoom = 128;
+  int n;  // noted, or more than there is room for
+  int lo[kRoom], hi[kRoom], at[kRoom];
+};
 __device__ __forceinline__ void token_offsets_at(int64_t p, int own, int before, int N, int T,
                                                  const int32_t* __restrict__ token,
-                                                 int32_t* __restrict__ tok_off) {
+                                                 int32_t* __restrict__ tok_off, TokenGaps& gaps) {
   const auto in = [T](int t) { return (unsigned)t < (unsigned)T; };
   const int hi = p == N ? T : own;
   if (p < N && !in(hi)) return;
-  if (!in(before) && p > 1 && T > 0) {
+  if (__builtin_expect(!in(before) && p > 1 && T > 0, 0)) {
 #pragma unroll 1
     for (const int32_t* q = token + p - 1; q != token && !in(before);) before = *--q;
   }
   const int lo = in(before) ? before + 1 : 0;
+  if (__builtin_expect(hi - lo >= TokenGaps::kLong, 0)) {
+    const int k = atomicAdd(&gaps.n, 1);
+    if (k < TokenGaps::kRoom) {
+      gaps.lo[k] = lo;
+      gaps.hi[k] = hi;
+      gaps.at[k] = (int)p;
+      return;
+    }
+  }
   for (int t = lo; t <= hi; ++t) tok_off[t] = (int32_t)p;
+}
+// All threads of the workgroup, after a barrier behind their token_offsets_at.
+template <int NT>
+__device__ __forceinline__ void fill_gaps(const TokenGaps& gaps, int32_t* __restrict__ tok_off) {
+  for (int k = 0; k < min(gaps.n, TokenGaps::kRoom); ++k)
+    for (int t = gaps.lo[k] + (int)threadIdx.x; t <= gaps.hi[k]; t += NT) tok_off[t] = gaps.at[k];
 }
 
 __global__ __launch_bounds__(256) void k_bucket_count(int N, int T, int E, int chunk,
@@ -92,7 +115,9 @@ __global__ __launch_bounds__(256) void k_bucket_count(int N, int T, int E, int c
                                                       uint32_t* __restrict__ blkerr,
                                                       int32_t* __restrict__ tok_off) {
   LRM_DYN_SHARED(int, hist);
+  __shared__ TokenGaps gaps;
   for (int e = threadIdx.x; e < E; e += 256) hist[e] = 0;
+  if (threadIdx.x == 0) gaps.n = 0;
   __syncthreads();
   const int64_t p0 = (int64_t)blockIdx.x * chunk;
   const int64_t p1 = min<int64_t>(p0 + chunk, N);
@@ -105,10 +130,10 @@ __global__ __launch_bounds__(256) void k_bucket_count(int N, int T, int E, int c
     const int before = p > 0 ? token[p - 1] : -1;
     if (p > 0 && before > t) bad |= kErrTokenOrder;
     if (e >= 0 && e < E && t >= 0 && t < T) atomicAdd(&hist[e], 1);
-    if (tok_off) token_offsets_at(p, t, before, N, T, token, tok_off);
+    if (tok_off) token_offsets_at(p, t, before, N, T, token, tok_off, gaps);
   }
   if (tok_off && p1 == N && threadIdx.x == 0)
-    token_offsets_at(N, T, N > 0 ? token[N - 1] : -1, N, T, token, tok_off);
+    token_offsets_at(N, T, N > 0 ? token[N - 1] : -1, N, T, token, tok_off, gaps);
   // this block's error bits: one word per block, written every call (no
   // zeroing pass); the scan kernel folds them into the call's error word
   __shared__ uint32_t berr;
@@ -117,6 +142,7 @@ __global__ __launch_bounds__(256) void k_bucket_count(int N, int T, int E, int c
   if (bad) atomicOr(&berr, bad);
   __syncthreads();
   if (threadIdx.x == 0) blkerr[blockIdx.x] = berr;
+  if (tok_off) fill_gaps<256>(gaps, tok_off);
   for (int e = threadIdx.x; e < E; e += 256) blkcnt[(int64_t)e * gridDim.x + blockIdx.x] = hist[e];
 }
 
@@ -360,6 +386,7 @@ __global__ __launch_bounds__(kSelThreads) void k_bucket_one(BucketArgs a) {
   LRM_DYN_SHARED(int, cnt);  // [NW][E], then the counts [E], then the offsets [E + 1]
   __shared__ int lds[NW + 1];
   __shared__ uint32_t eor;
+  __shared__ TokenGaps gaps;
   const int E = a.E, N = a.N, T = a.T;
   int* total = cnt + NW * E;
   int* off = total + E;
@@ -376,7 +403,10 @@ __global__ __launch_bounds__(kSelThreads) void k_bucket_one(BucketArgs a) {
     pv[u] = in && p > 0 ? a.token[p - 1] : -1;
   }
   for (int i = tid; i < NW * E; i += kSelThreads) cnt[i] = 0;
-  if (tid == 0) eor = 0u;
+  if (tid == 0) {
+    eor = 0u;
+    gaps.n = 0;
+  }
   __syncthreads();
   int* mine = cnt + w * E;
   uint32_t bad = 0;
@@ -389,9 +419,9 @@ __global__ __launch_bounds__(kSelThreads) void k_bucket_one(BucketArgs a) {
     if (!tin) bad |= kErrTokenRange;
     if (p > 0 && pv[u] > tv[u]) bad |= kErrTokenOrder;
     if (ein && tin) atomicAdd(&mine[ev[u]], 1);
-    if (a.tok_off) token_offsets_at(p, tv[u], pv[u], N, T, a.token, a.tok_off);
+    if (a.tok_off) token_offsets_at(p, tv[u], pv[u], N, T, a.token, a.tok_off, gaps);
   }
-  if (a.tok_off && tid == 0) token_offsets_at(N, T, a.token[N - 1], N, T, a.token, a.tok_off);
+  if (a.tok_off && tid == 0) token_offsets_at(N, T, a.token[N - 1], N, T, a.token, a.tok_off, gaps);
   if (bad) atomicOr(&eor, bad);
   __syncthreads();
   for (int e = tid; e < E; e += kSelThreads) {
@@ -440,6 +470,7 @@ __global__ __launch_bounds__(kSelThreads) void k_bucket_one(BucketArgs a) {
     }
     __builtin_amdgcn_wave_barrier();
   }
+  if (a.tok_off) fill_gaps<kSelThreads>(gaps, a.tok_off);
 }
 
 // One workgroup per expert.  keys[c] and ids cand[c] (or c itself when cand is
@@ -711,8 +742,12 @@ __global__ __launch_bounds__(kSelThreads) void k_select_small(SmallSelArgs a) {
   __shared__ uint32_t eor;
   const int e = blockIdx.x, tid = threadIdx.x, w = tid >> 6, l = lane_id();
   const int N = a.N, T = a.T, E = a.E;
+  __shared__ TokenGaps gaps;
   for (int i = tid; i < E; i += kSelThreads) cnt[i] = 0;
-  if (tid == 0) eor = 0u;
+  if (tid == 0) {
+    eor = 0u;
+    gaps.n = 0;
+  }
   __syncthreads();
   const int R = (N + kSelThreads - 1) / kSelThreads;
   const uint64_t lt = (l == 0) ? 0ull : (~0ull >> (64 - l));  // lanes below this one
@@ -749,7 +784,7 @@ __global__ __launch_bounds__(kSelThreads) void k_select_small(SmallSelArgs a) {
         if (valid) atomicAdd(&cnt[ex], 1);
         if (e == 0) {
           if (!valid) a.pos[p] = -1;
-          if (a.tok_off) token_offsets_at(p, tk, tpv[u], N, T, a.token, a.tok_off);
+          if (a.tok_off) token_offsets_at(p, tk, tpv[u], N, T, a.token, a.tok_off, gaps);
         }
       }
       const bool hit = valid && ex == e;
@@ -759,7 +794,7 @@ __global__ __launch_bounds__(kSelThreads) void k_select_small(SmallSelArgs a) {
     }
   }
   if (e == 0 && tid == 0 && a.tok_off)
-    token_offsets_at(N, T, N > 0 ? a.token[N - 1] : -1, N, T, a.token, a.tok_off);
+    token_offsets_at(N, T, N > 0 ? a.token[N - 1] : -1, N, T, a.token, a.tok_off, gaps);
   if (bad) atomicOr(&eor, bad);
   __syncthreads();
   // quotas: device array, or by value, or keep all
@@ -798,6 +833,7 @@ __global__ __launch_bounds__(kSelThreads) void k_select_small(SmallSelArgs a) {
     }
     if (tid == 0) a.err[0] = eor | (over ? kErrCapacity : 0u);
   }
+  if (e == 0 && a.tok_off) fill_gaps<kSelThreads>(gaps, a.tok_off);
   // the candidates written above are read back by other threads of the block
   __syncthreads();
   select_expert(c0, n, o, m, a.keys, a.cand, a.pos, a.kept);
@@ -807,9 +843,14 @@ __global__ __launch_bounds__(kSelThreads) void k_select_small(SmallSelArgs a) {
 __global__ __launch_bounds__(256) void k_token_offsets(int N, int T,
                                                        const int32_t* __restrict__ token,
                                                        int32_t* __restrict__ tok_off) {
+  __shared__ TokenGaps gaps;
+  if (threadIdx.x == 0) gaps.n = 0;
+  __syncthreads();
   const int64_t p = (int64_t)blockIdx.x * 256 + threadIdx.x;
-  if (p > N) return;
-  token_offsets_at(p, p < N ? token[p] : T, p > 0 ? token[p - 1] : -1, N, T, token, tok_off);
+  if (p <= N)
+    token_offsets_at(p, p < N ? token[p] : T, p > 0 ? token[p - 1] : -1, N, T, token, tok_off, gaps);
+  __syncthreads();
+  fill_gaps<256>(gaps, tok_off);
 }
 
 // mt_off[e] = sum over e' < e of ceil(M_e' / bm)  (row tiles of the dX GEMM)

@@ -205,3 +205,34 @@ def closed_case(name):
     c["tmask"] = c["emask"] = None
     c["ld"] = E
     return c
+
+
+# --------------------------------------------- long runs of tokens without pairs
+def sparse_case(name):
+    """`tail`, `head`: all pairs in 40 neighbouring tokens of 1000; `spread`: about 90
+    pairs over 6000 tokens, a third of the gaps long ones; `many`: more long gaps
+    than a workgroup notes; `none`."""
+    T, k, drop = {"tail": (40, 2, 0.0), "head": (40, 2, 0.0), "spread": (6000, 1, 0.985),
+                  "many": (60000, 1, 0.99), "none": (40, 2, 1.0)}[name]
+    c = FC.build_forward(FC._f("linear", T, 5, k, 8, 8, residual=name != "head", drop=drop,
+                               outs=("Y",)), "sparse " + name)
+    if name not in ("spread", "many"):  # the same pairs among more tokens
+        more, dt = 1000 - T, c["X"].dtype
+        g = FC.gen("sparse more", name)
+        first = name != "head"
+
+        def grow(m):
+            new = FC.normal(g, more, m.shape[1], dtype=dt)
+            return torch.cat([m, new] if first else [new, m])
+
+        c["X_store"] = grow(c["X_store"])
+        c["X"] = c["X_store"][:, :c["d_in"]]
+        if c["R"] is not None:
+            c["R"] = grow(c["R"])
+        if not first:
+            c["pairs"] = dict(c["pairs"], token=c["pairs"]["token"] + np.int32(more))
+        c["T"] = 1000
+    return c
+
+
+SPARSE = ("tail", "head", "spread", "none", "many")

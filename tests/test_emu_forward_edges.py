@@ -83,3 +83,9 @@ def test_emu_relu_keeps_nan(driver, tmp_path, dtype):  # noqa: F811
 def test_emu_bias_of_minus_infinity_closes_an_expert(driver, tmp_path, name):  # noqa: F811
     c = FE.closed_case(name)
     FC.judge_route(c, *emu_route(driver, tmp_path, c))
+
+
+@pytest.mark.parametrize("name", FE.SPARSE[:-1])
+def test_emu_long_runs_of_tokens_without_pairs(driver, tmp_path, name):  # noqa: F811
+    c = FE.sparse_case(name)
+    FC.judge_forward(c, emu(driver, tmp_path, c, env_extra={"LRM_FWD_TILE": "64"}))

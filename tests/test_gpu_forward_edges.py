@@ -144,16 +144,52 @@ def test_few_pairs_among_many_tokens(L, T):  # noqa: F811
     rest[at] = False
     assert torch.equal(Y[rest], R[rest])
 
-    def best_of(call):
-        times = []
-        for _ in range(5):
-            a, b = (torch.cuda.Event(enable_timing=True) for _ in range(2))
-            a.record()
-            call()
-            b.record()
-            torch.cuda.synchronize()
-            times.append(a.elapsed_time(b))
-        return min(times)
+    copy = time_of(lambda: Y.copy_(R))
+    assert time_of(lambda: L.lrm_expert_forward(f, dict(Y=Y), ws=ws)) < 20 * copy + 0.2
 
-    copy = best_of(lambda: Y.copy_(R))
-    assert best_of(lambda: L.lrm_expert_forward(f, dict(Y=Y), ws=ws)) < 20 * copy + 0.2
+
+@pytest.mark.parametrize("name", FE.SPARSE)
+def test_long_runs_of_tokens_without_pairs(L, monkeypatch, name):  # noqa: F811
+    monkeypatch.setenv("LRM_FWD_TILE", "128")
+    c = FE.sparse_case(name)
+    out, _ = run_forward(L, c)
+    FC.judge_forward(c, out)
+
+
+def time_of(call):
+    """The least of five, ms."""
+    times = []
+    for _ in range(5):
+        a, b = (torch.cuda.Event(enable_timing=True) for _ in range(2))
+        a.record()
+        call()
+        b.record()
+        torch.cuda.synchronize()
+        times.append(a.elapsed_time(b))
+    return min(times)
+
+
+@pytest.mark.parametrize("N", [0, 512, 16384])
+def test_tokens_behind_the_last_pair_cost_little(L, N):  # noqa: F811
+    """262144 tokens with pairs of the first ones only, forward and backward: Y is
+    the residual and dX is 0 there, without a thread that writes them one by one
+    (7 ms)."""
+    T, E, d, bf = 1 << 18, 8, 64, torch.bfloat16
+    g = FC.gen("behind", N)
+    tok = torch.arange(N, dtype=torch.int32) // 2
+    pairs = L.Pairs(dev(tok), dev(torch.randint(0, E, (N,), generator=g).int()),
+                    dev(torch.rand(N, generator=g)), T, E)
+    X, W = dev(FC.normal(g, T, d, dtype=bf)), dev(FC.normal(g, E, d, d, std=0.1, dtype=bf))
+    f = L.linear_forward(pairs, X, "token", W, residual=X)
+    Y = filled((T, d), bf)
+    ws = L.lrm_expert_forward(f, dict(Y=Y))
+    pb = L.linear_problem(pairs, X, "token", X, "token", W, [max(N // E, 1)] * E)
+    out = dict(dW=filled((E, d, d), torch.float32), dX=filled((T, d), torch.float32))
+    wb = L.lrm_expert_backward(pb, out)
+    torch.cuda.synchronize()
+    used = N // 2
+    assert torch.equal(Y[used:], X[used:]) and not out["dX"][used:].any()
+    if N:
+        assert not torch.equal(Y[:used], X[:used]) and out["dX"][:used].any()
+    assert time_of(lambda: L.lrm_expert_forward(f, dict(Y=Y), ws=ws)) < 1.5
+    assert time_of(lambda: L.lrm_expert_backward(pb, out, ws=wb)) < 1.5
