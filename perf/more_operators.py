@@ -1,0 +1,622 @@
+"""More measured operators: what makes a training step of a layer's gradients.
+
+Four operators, each in a plain form (elementary torch operations in 32 bits,
+64 where 32 lose what matters) and as the calls of the framework:
+
+* ``balance``      the router's balance loss and z loss, and the experts' counts
+* ``balance_bwd``  their gradient, joined with that of the routing weights
+* ``sumsq``        the sum of squares of many gradients (for their norm)
+* ``adamw``        an AdamW step over many tensors, moments in 32 or 8 bits
+
+``own`` selects the form; ``listed``, ``draw``, ``prepare``, ``run``, ``work``
+and ``exact`` are what a measuring program calls.
+"""
+
+import math
+
+import torch
+
+own = False
+
+DEVICE = "cuda"
+TYPES = {"bf16": torch.bfloat16, "f32": torch.float32}
+SIZE = {"bf16": 2, "f32": 4}
+BLOCK = 32  # elements that share an exponent of the 8-bit moments
+
+
+# ------------------------------------------------------------------- cases
+def _balance(name, op, T, E, k, S, dtype="bf16", score="softmax", z=True, counts=True, renorm=True,
+             weights=True, padded=0.0, down=0):
+    # S 0: the whole batch as one; counts: the router's are at hand; weights: the
+    # gradient of the routing weights is joined
+    c = dict(op=op, T=T, E=E, k=k, S=S, dtype=dtype, score=score, z=z,
+             counts=counts and S == 0, renorm=renorm,
+             weights=weights, padded=padded, down=down)
+    return dict(c, name=name) if name else c
+
+
+def _tensors(name, op, n, least, most, p="f32", g="f32", master=False, bits=32, clip=True):
+    # n tensors of least to most elements (their logarithms evenly spread)
+    c = dict(op=op, n=n, least=least, most=most, g=g)
+    if op == "adamw":
+        c.update(p=p, master=master, bits=bits, clip=clip)
+    return dict(c, name=name) if name else c
+
+
+EXPERTS = 32 * 768 * 2048  # one projection of 32 experts of the Qwen3-30B-A3B-shaped layer
+
+
+def listed():
+    return [
+        # a small micro-batch, counts from the choice: nothing but latency
+        _balance("balance_small", "balance", 256, 16, 2, 0, counts=False),
+        # a training step's tokens (the largest of the benchmark's workloads), the
+        # balance of the whole batch, counts from the router or summed over GPUs
+        _balance("balance_train", "balance", 65536, 128, 8, 0),
+        # the balance of every sequence of a padded batch, sigmoid scores
+        _balance("balance_seqs", "balance", 16384, 256, 8, 13, dtype="f32", score="sigmoid", z=False,
+                 counts=False, padded=0.1),
+        # training: both losses and the routing weights in one gradient
+        _balance("balance_bwd_train", "balance_bwd", 65536, 128, 8, 0),
+        # the same by sequence at odd sizes, weights not renormalised, experts out
+        _balance("balance_bwd_seqs", "balance_bwd", 15001, 161, 6, 9, dtype="f32", renorm=False,
+                 down=3, padded=0.1),
+        # the norm of a layer's gradients: three projections of 32 experts
+        _tensors("sumsq_layer", "sumsq", 3, EXPERTS, EXPERTS),
+        # the norm over many small tensors (norms, biases, routers) in bf16
+        _tensors("sumsq_many", "sumsq", 300, 64, 65536, g="bf16"),
+        # a router and a few norms: latency
+        _tensors("adamw_small", "adamw", 6, 128, 262144, clip=False),
+        # a model's many small tensors at once, clipped
+        _tensors("adamw_many", "adamw", 400, 64, 65536),
+        # a layer's experts: bf16 weights with fp32 masters, fp32 gradients
+        _tensors("adamw_layer", "adamw", 3, EXPERTS, EXPERTS, p="bf16", master=True),
+        # the same in the least memory: 8-bit moments, bf16 weights and gradients
+        _tensors("adamw8_layer", "adamw", 3, EXPERTS, EXPERTS, p="bf16", g="bf16", bits=8),
+        # one projection of 8 experts and smaller odd tensors, fp32 with 8-bit moments
+        _tensors("adamw8_odd", "adamw", 11, 1001, 8 * 1024 * 1408, bits=8),
+    ]
+
+
+def _log(rng, lo, hi):
+    return int(round(math.exp(rng.uniform(math.log(lo), math.log(hi)))))
+
+
+def draw(rng):
+    op = rng.choice(["balance", "balance_bwd", "sumsq", "adamw", "adamw"])
+    if op in ("balance", "balance_bwd"):
+        E = _log(rng, 4, 512)
+        T = min(_log(rng, 1, 65536), 65536 * 128 // E)
+        score = rng.choice(["softmax", "sigmoid"])
+        S = rng.choice([0, 0, _log(rng, 1, 64)])
+        # (a choice of every expert balances itself: no gradient)
+        return _balance(None, op, T, E, rng.randint(1, min(E // 2, 12)), S,
+                        dtype=rng.choice(["bf16", "f32"]), score=score,
+                        z=score == "softmax" and rng.random() < 0.6,
+                        counts=S == 0 and rng.random() < 0.5, renorm=rng.random() < 0.6,
+                        weights=rng.random() < 0.7,
+                        padded=rng.choice([0.0, 0.0, 0.2]) if T >= 64 else 0.0,
+                        down=rng.randint(0, 2) if E > 8 else 0)
+    n = _log(rng, 1, 400)
+    most = min(_log(rng, 64, EXPERTS), 3 * EXPERTS // n)
+    least = rng.randint(1, most)
+    g = rng.choice(["bf16", "f32"])
+    if op == "sumsq":
+        return _tensors(None, op, n, least, most, g=g)
+    p = rng.choice(["bf16", "f32"])
+    return _tensors(None, op, n, least, most, p=p, g=g, master=p == "bf16" and rng.random() < 0.5,
+                    bits=rng.choice([8, 32]), clip=rng.random() < 0.7)
+
+
+# ------------------------------------------------------------------ inputs
+def _sizes(c):
+    """Elements of every tensor, and its first block of 32 in the buffers that hold them all."""
+    n, lo, hi = c["n"], math.log(c["least"]), math.log(c["most"])
+    # (a step coprime to most n: sizes come in no order)
+    sizes = [int(round(math.exp(lo + (hi - lo) * (i * 61 % n) / max(n - 1, 1)))) for i in range(n)]
+    first = [0]
+    for s in sizes:
+        first.append(first[-1] + -(-s // BLOCK))
+    return sizes, first
+
+
+def prepare(case, seed):
+    c = case
+    gen = torch.Generator(device=DEVICE)
+    gen.manual_seed(seed)
+    s = dict(case=c)
+    if c["op"] in ("sumsq", "adamw"):
+        return _prepare_tensors(s, c, gen, seed)
+    T, E, k = c["T"], c["E"], c["k"]
+    z = torch.randn(T, E, generator=gen, device=DEVICE).mul_(1.5)
+    z -= 0.3 * torch.log1p(torch.randperm(E, generator=gen, device=DEVICE).float())
+    z = z.to(TYPES[c["dtype"]])
+    s["token_mask"] = s["expert_mask"] = s["seq"] = s["counts"] = None
+    if c["padded"]:  # the padding's logits hold whatever was there
+        keep = torch.rand(T, generator=gen, device=DEVICE) >= c["padded"]
+        s["token_mask"] = keep.to(torch.uint8)
+        z[~keep] = float("nan")
+    if c["down"]:
+        m = torch.ones(E, dtype=torch.uint8, device=DEVICE)
+        m[torch.randperm(E, generator=gen, device=DEVICE)[:c["down"]]] = 0
+        s["expert_mask"] = m
+        z[:, m == 0] = float("nan")
+    s["logits"] = z
+    if c["S"]:  # cuts anywhere: sequences of no token among them, tokens behind the last
+        cuts = torch.randint(0, T + 1, (c["S"] - 1,), generator=gen, device=DEVICE)
+        ends = torch.tensor([0, T - T // 50], device=DEVICE)
+        s["seq"] = torch.cat([ends, cuts.clamp_max(T - T // 50)]).sort().values.int()
+    x, ok = _eligible(s)
+    top = x.sort(dim=1, descending=True, stable=True)
+    e = top.indices[:, :k].masked_fill(top.values[:, :k] == -math.inf, -1)
+    s["expert"] = e.int().reshape(-1)
+    if c["counts"]:
+        s["counts"] = torch.bincount(s["expert"].long() + 1, minlength=E + 1)[1:].int()
+    s["coef"], s["z_coef"] = 0.01, 1e-3 if c["z"] else 0.0
+    if c["op"] == "balance_bwd":
+        s["saved"] = _balance_plain(s)["saved"]
+        # four micro-batches make one step
+        s["dloss"] = torch.full((2,), 0.25, device=DEVICE)
+        # of the losses' gradients' size
+        d = torch.randn(T * k, generator=gen, device=DEVICE) * (0.02 / T)
+        s["dweight"] = d if c["weights"] else None
+    return s
+
+
+def _prepare_tensors(s, c, gen, seed):
+    sizes, first = _sizes(c)
+    total = first[-1] * BLOCK
+    # what lies between two tensors is zero and stays so
+    inside = torch.zeros(total, dtype=torch.bool, device=DEVICE)
+    decay = torch.zeros(first[-1], 1, device=DEVICE)
+    for i, (n, b) in enumerate(zip(sizes, first)):
+        inside[b * BLOCK:b * BLOCK + n] = True
+        decay[b:first[i + 1]] = 0.0 if i % 3 == 1 else 0.1  # (norms and biases have none)
+
+    def normal(std):
+        return torch.randn(total, generator=gen, device=DEVICE).mul_(std).mul_(inside)
+
+    s.update(sizes=sizes, first=first)
+    s["g"] = normal(1e-3).to(TYPES[c["g"]])
+    if c["op"] == "sumsq":
+        return s
+    s["decay"], s["seed"], s["step"] = decay, seed, 1000
+    s["lr"], s["beta1"], s["beta2"], s["eps"], s["scale"] = 2e-5, 0.9, 0.999, 1e-8, 0.25
+    s["max_norm"] = 1.0 if c["clip"] else 0.0
+    w = normal(0.02)
+    s["p"] = w.to(TYPES[c["p"]])
+    s["master"] = w if c["master"] else None
+    m, v = normal(1e-4), normal(2.5e-4).square_()
+    if c["bits"] == 8:
+        half = torch.full((), 0x7fff, dtype=torch.int64, device=DEVICE)
+        s["m"], s["m_exp"] = _encode(m.view(-1, BLOCK), half, True)
+        s["v"], s["v_exp"] = _encode(v.view(-1, BLOCK), half, False)
+    else:
+        s["m"], s["v"] = m, v
+    return s
+
+
+# ------------------------------------------------- plain form: balance loss
+def _eligible(s):
+    z = s["logits"].float()
+    ok = z > -math.inf
+    if s["expert_mask"] is not None:
+        ok &= s["expert_mask"].bool()
+    if s["token_mask"] is not None:
+        ok &= s["token_mask"].bool()[:, None]
+    return z.masked_fill(~ok, -math.inf), ok
+
+
+def _places(s):
+    """Sequence of every token (S: none), and how many there are."""
+    T = s["case"]["T"]
+    t = torch.arange(T, device=DEVICE)
+    if s["seq"] is None:
+        return torch.zeros_like(t), 1
+    S = s["seq"].numel() - 1
+    at = torch.searchsorted(s["seq"].long(), t, right=True) - 1
+    return torch.where(at < 0, S, at), S
+
+
+def _shares(s):
+    """Shares p of the experts, 1 less the score (sigmoid), log of the exps' sum, live tokens."""
+    z, ok = _eligible(s)
+    top = z.max(1, keepdim=True).values
+    live = top[:, 0] > -math.inf
+    if s["case"]["score"] == "sigmoid":
+        f = (1.0 / (1.0 + torch.exp(-z))).masked_fill(~ok, 0.0)
+        rest = 1.0 / (1.0 + torch.exp(z))
+        return f / f.sum(1, keepdim=True).clamp_min(1e-38), rest, None, live
+    top = top.masked_fill(~live[:, None], 0.0)
+    f = torch.exp(z - top)
+    total = f.sum(1, keepdim=True)
+    lse = (top + torch.log(total)).masked_fill(~live[:, None], 0.0)
+    return f / total.clamp_min(1e-38), None, lse, live
+
+
+def _balance_plain(s):
+    c = s["case"]
+    E, k = c["E"], c["k"]
+    p, _, lse, live = _shares(s)
+    at, S = _places(s)
+    used = live & (at < S)
+    out = {}
+    counts = s["counts"]
+    if counts is None:
+        e = s["expert"].long()
+        on = (e >= 0) & (at < S).repeat_interleave(k)
+        if s["token_mask"] is not None:
+            on &= s["token_mask"].bool().repeat_interleave(k)
+        place = at.repeat_interleave(k) * E + e
+        counts = torch.bincount(torch.where(on, place, S * E), minlength=S * E + 1)[:S * E].int()
+        out["counts"] = counts.view(S, E)
+    # (long sums, in 64 bits: a product with the sequences' indicators, or just a sum)
+    member = (torch.arange(S, device=DEVICE)[:, None] == torch.where(used, at, S)).double()
+    sums = member @ p.double() if S > 1 else (member[0, :, None] * p.double()).sum(0, keepdim=True)
+    n = member.sum(1)
+    f = counts.view(S, E).double()
+    f = f / f.sum(1, keepdim=True).clamp_min(1.0)
+    M = E if s["expert_mask"] is None else (s["expert_mask"] != 0).sum()
+    a = (s["coef"] * M * f / n.clamp_min(1.0)[:, None] / (n > 0).sum().clamp_min(1)).float()
+    a = a.masked_fill((n == 0)[:, None], 0.0)
+    b = (2.0 * s["z_coef"] / n.sum().clamp_min(1.0)).float()
+    out["saved"] = torch.cat([a, b.expand(S, 1)], 1)
+    z = torch.zeros((), dtype=torch.float64, device=DEVICE)
+    if c["z"]:
+        z = 0.5 * b.double() * (lse[:, 0].double().square() * used).sum()
+    out["loss"] = torch.stack([(a.double() * sums).sum(), z]).float()
+    return out
+
+
+def _balance_bwd_plain(s):
+    c = s["case"]
+    T, k = c["T"], c["k"]
+    p, rest, lse, live = _shares(s)
+    at, S = _places(s)
+    saved = torch.cat([s["saved"], torch.zeros_like(s["saved"][:1])])[at]
+    a, b = saved[:, :-1], saved[:, -1:]
+    d = s["dloss"][0] * p * (a - (p * a).sum(1, keepdim=True))
+    if rest is not None:
+        d = d * rest
+    if c["z"]:
+        d = d + s["dloss"][1] * b * lse * p
+    d = d.masked_fill((p == 0) | ~live[:, None], 0.0)
+    if s["dweight"] is not None:
+        z, _ = _eligible(s)
+        e = s["expert"].view(T, k).long()
+        full = e >= 0
+        e = e.clamp_min(0)
+        u = s["dweight"].view(T, k).masked_fill(~full, 0.0)
+        x = z.gather(1, e).masked_fill(~full, -math.inf)
+        low = 1.0 / (1.0 + torch.exp(x))
+        if c["renorm"]:
+            if c["score"] == "sigmoid":  # sigmoid(x) / sum as a softmax of log sigmoid
+                x = torch.minimum(x, torch.zeros_like(x)) - torch.log1p(torch.exp(-x.abs()))
+            top = x.max(1, keepdim=True).values
+            w = torch.exp(x - top.masked_fill(top == -math.inf, 0.0))
+            w = w / w.sum(1, keepdim=True).clamp_min(1e-38)
+            r = w * (u - (w * u).sum(1, keepdim=True))
+            r = r * low if c["score"] == "sigmoid" else r
+        elif c["score"] == "sigmoid":
+            r = u * low * (1.0 - low)
+        else:
+            r = p.gather(1, e).masked_fill(~full, 0.0) * u
+            d = d - p * r.sum(1, keepdim=True)
+        d = d.scatter_add(1, e, r.masked_fill(~full, 0.0))
+    return dict(dlogits=d.to(TYPES[c["dtype"]]))
+
+
+# ------------------------------------------------------- plain form: AdamW
+# Random numbers of the roundings: multiply-xorshift mixing with the fractional
+# bits of the golden ratio and of the square roots of 2 and 3.
+GOLD, ROOT2, ROOT3, WORD = 0x9E3779B9, 0x6A09E667, 0xBB67AE85, 0xFFFFFFFF
+
+
+def _mix(x):
+    x = x ^ x >> 16
+    x = x * ROOT2 & WORD
+    x = x ^ x >> 15
+    x = x * ROOT3 & WORD
+    return x ^ x >> 16
+
+
+def _key(seed, step):
+    key = _mix((seed & WORD) + GOLD & WORD)
+    key = _mix((key ^ seed >> 32 & WORD) + GOLD & WORD)
+    key = _mix((key ^ step & WORD) + GOLD & WORD)
+    return _mix((key ^ step >> 32) + GOLD & WORD)
+
+
+def _random(s):
+    """16 random bits an element for m, v and p: [blocks][32] each."""
+    blocks = torch.arange(s["first"][-1], device=DEVICE)
+    key = _mix(_key(s["seed"], s["step"]) + blocks * GOLD + (blocks >> 32) * ROOT3 & WORD)
+    h = key[:, None] + torch.arange(BLOCK, device=DEVICE) * GOLD & WORD
+    h = h ^ h >> 16
+    h = h * ROOT2 & WORD
+    h = h ^ h >> 15
+    q = h * ROOT3 & WORD
+    return h & 0xFFFF, h >> 16, (q ^ q >> 16) & 0xFFFF
+
+
+def _encode(x, r, signed):
+    """Blocks of 32 values as 8-bit floats above a shared exponent (their largest's):
+    3 bits of mantissa, 4 of exponent and a sign, or 5 of exponent; r: 16 random bits."""
+    top = 15 if signed else 31
+    u = x.abs().contiguous().view(torch.int32).long()
+    e = ((u.max(1, keepdim=True).values + 0xFFFFF) >> 23).clamp_min(top + 1)
+    code = (u + (r * 16 + 8) - ((e - top) << 23)) >> 20
+    code = code.clamp(0, 8 * top + 7)
+    if signed:
+        code = torch.where((x < 0) & (code > 0), code + 128, code)
+    else:  # (what is not zero stays so: it is divided by)
+        code = torch.where(u > 0, code.clamp_min(1), code)
+    return code.to(torch.uint8).view(-1), e.to(torch.uint8).view(-1)
+
+
+def _decode(code, e, signed):
+    top = 15 if signed else 31
+    code, e = code.view(-1, BLOCK).int(), e.view(-1, 1).int()
+    c = code & 127 if signed else code
+    x = ((c << 20) + ((e - top) << 23)).view(torch.float32)
+    x = torch.where(c > 0, x, torch.zeros_like(x))
+    return torch.where(code > 127, -x, x) if signed else x
+
+
+def _sumsq_plain(s):
+    return dict(sumsq=s["g"].double().square().sum().view(1))
+
+
+def _adamw_plain(s):
+    c = s["case"]
+    eight = c["bits"] == 8
+    f = torch.full((), s["scale"], device=DEVICE)
+    if c["clip"]:
+        norm = s["scale"] * torch.sqrt(_sumsq_plain(s)["sumsq"][0])
+        f = (s["scale"] * torch.clamp_max(s["max_norm"] / norm, 1.0)).float()
+    g = f * s["g"].float().view(-1, BLOCK)
+    if eight:
+        m, v = _decode(s["m"], s["m_exp"], True), _decode(s["v"], s["v_exp"], False)
+    else:
+        m, v = s["m"].view(-1, BLOCK), s["v"].view(-1, BLOCK)
+    m = s["beta1"] * m + (1.0 - s["beta1"]) * g
+    v = s["beta2"] * v + (1.0 - s["beta2"]) * (g * g)
+    w = (s["p"] if s["master"] is None else s["master"]).float().view(-1, BLOCK)
+    size = s["lr"] / (1.0 - s["beta1"] ** s["step"])
+    root = math.sqrt(1.0 - s["beta2"] ** s["step"])
+    w = w * (1.0 - s["lr"] * s["decay"]) - size * m / (torch.sqrt(v) / root + s["eps"])
+    stochastic = c["p"] == "bf16" and s["master"] is None
+    rm, rv, rp = _random(s) if eight or stochastic else (None, None, None)
+    if stochastic:
+        u = w.view(torch.int32).long() + rp & ~0xFFFF
+        s["p"].copy_(u.to(torch.int32).view(torch.float32).view(-1))
+    else:
+        s["p"].copy_(w.view(-1))
+    if s["master"] is not None:
+        s["master"].copy_(w.view(-1))
+    if not eight:
+        s["m"].copy_(m.view(-1))
+        s["v"].copy_(v.view(-1))
+        return dict(p=s["p"], master=s["master"], m=s["m"], v=s["v"])
+    s["m"], s["m_exp"] = _encode(m, rm, True)
+    s["v"], s["v_exp"] = _encode(v, rv, False)
+    # (4 significant bits: bf16 holds them)
+    return dict(p=s["p"], master=s["master"],
+                m=_decode(s["m"], s["m_exp"], True).to(torch.bfloat16).view(-1),
+                v=_decode(s["v"], s["v_exp"], False).to(torch.bfloat16).view(-1))
+
+
+# ----------------------------------------------------- the framework's calls
+def _handle(s):
+    """The descriptors, outputs and workspace that a program keeps over its calls."""
+    from pruned_expert_backward_lrm_amd import lrm as L
+
+    c = s["case"]
+
+    def new(*shape, dtype):
+        return torch.empty(*shape, dtype=dtype, device=DEVICE)
+
+    if c["op"] in ("balance", "balance_bwd"):
+        S = max(c["S"], 1)
+        r = L.Router(s["logits"], c["k"], score=c["score"], renorm=c["renorm"],
+                     expert_mask=s["expert_mask"], token_mask=s["token_mask"])
+        b = L.Balance(r, expert=s["expert"], counts=s["counts"], seq=s["seq"], coef=s["coef"],
+                      z_coef=s["z_coef"])
+        if c["op"] == "balance_bwd":
+            o = dict(dlogits=new(c["T"], c["E"], dtype=TYPES[c["dtype"]]))
+            return lambda: L.lrm_balance_bwd(b, s["saved"], o["dlogits"], dloss=s["dloss"],
+                                             dweight=s["dweight"]), o
+        o = dict(loss=new(2, dtype=torch.float32), saved=new(S, c["E"] + 1, dtype=torch.float32))
+        if s["counts"] is None:
+            o.update(counts=new(S, c["E"], dtype=torch.int32))
+        ws = new(L.lrm_balance_workspace_size(b), dtype=torch.uint8)
+        return lambda: L.lrm_balance_loss(b, o["loss"], o["saved"], counts=o.get("counts"), ws=ws), o
+
+    def parts(flat, per=1):  # the tensors, or their exponents (per BLOCK), in what holds all
+        return None if flat is None else [
+            flat[f * BLOCK // per:f * BLOCK // per + -(-n // per)]
+            for f, n in zip(s["first"], s["sizes"])]
+
+    g = parts(s["g"])
+    sumsq = new(1, dtype=torch.float64)
+    if c["op"] == "sumsq":
+        ps = L.Params(g=g)
+        ws = new(L.lrm_sumsq_workspace_size(ps), dtype=torch.uint8)
+        return lambda: L.lrm_grad_sumsq(ps, sumsq, ws=ws), dict(sumsq=sumsq)
+    eight = c["bits"] == 8
+    decay = [0.0 if i % 3 == 1 else 0.1 for i in range(c["n"])]
+    exps = dict(m_exp=parts(s["m_exp"], BLOCK), v_exp=parts(s["v_exp"], BLOCK)) if eight else {}
+    ps = L.Params(g=g, p=parts(s["p"]), m=parts(s["m"]), v=parts(s["v"]), master=parts(s["master"]),
+                  weight_decay=decay, **exps)
+    opt = L.AdamW(lr=s["lr"], beta1=s["beta1"], beta2=s["beta2"], eps=s["eps"], seed=s["seed"],
+                  grad_scale=s["scale"], max_norm=s["max_norm"], sumsq=sumsq if c["clip"] else None)
+    ws = new(L.lrm_sumsq_workspace_size(ps), dtype=torch.uint8)
+    o = dict(p=s["p"], master=s["master"], m=s["m"], v=s["v"])
+    if eight:
+        o.update(m=new(s["m"].numel(), dtype=torch.bfloat16), v=new(s["v"].numel(), dtype=torch.bfloat16))
+
+    def call():
+        if c["clip"]:
+            L.lrm_grad_sumsq(ps, sumsq, ws=ws)
+        L.lrm_adamw(ps, opt, s["step"])
+        if eight:  # what the moments are now
+            L.lrm_moment_read(s["m"], s["m_exp"], o["m"], "m")
+            L.lrm_moment_read(s["v"], s["v_exp"], o["v"], "v")
+
+    return call, o
+
+
+PLAIN = {"balance": _balance_plain, "balance_bwd": _balance_bwd_plain, "sumsq": _sumsq_plain,
+         "adamw": _adamw_plain}
+
+
+def run(state):
+    if not own:
+        return PLAIN[state["case"]["op"]](state)
+    if "handle" not in state:
+        state["handle"] = _handle(state)
+    call, out = state["handle"]
+    call()
+    return out
+
+
+# -------------------------------------------------------------------- work
+def work(case):
+    c = case
+    if c["op"] in ("balance", "balance_bwd"):
+        T, E, k, S = c["T"], c["E"], c["k"], max(c["S"], 1)
+        rows = T * E * SIZE[c["dtype"]]
+        if c["op"] == "balance":
+            n = rows + S * (2 * E + 1) * 4 + (0 if c["counts"] else T * k * 4)
+            return dict(bytes=n, flops=6.0 * T * E)
+        n = 2 * rows + S * (E + 1) * 4 + (T * k * 8 if c["weights"] else 0)
+        return dict(bytes=n, flops=9.0 * T * E)
+    n = sum(_sizes(c)[0])
+    if c["op"] == "sumsq":
+        return dict(bytes=n * SIZE[c["g"]], flops=2.0 * n)
+    # (clipping: the norm has to be known before the first weight changes)
+    b = SIZE[c["g"]] * (2 if c["clip"] else 1) + SIZE[c["p"]] * (1 if c["master"] else 2)
+    b += 8 if c["master"] else 0
+    # 8 bits: read and written in the step, then read as what they stand for
+    b += 16 if c["bits"] == 32 else 2 * (3 * (1 + 1 / BLOCK) + 2)
+    return dict(bytes=n * b, flops=16.0 * n)
+
+
+# -------------------------------------------------- the definitions, 64 bits
+def _exact_balance(s):
+    """The two losses as functions of the logits, with what they keep."""
+    c = s["case"]
+    T, E, k = c["T"], c["E"], c["k"]
+    z = s["logits"].double()
+    dead = torch.zeros(T, E, dtype=torch.bool, device=DEVICE)
+    if s["expert_mask"] is not None:
+        dead |= s["expert_mask"][None, :] == 0
+    if s["token_mask"] is not None:
+        dead |= s["token_mask"][:, None] == 0
+    alive = ~dead.all(1)
+    z = torch.where(dead, torch.full_like(z, -1e4), z).requires_grad_(True)
+    if c["score"] == "sigmoid":
+        score = torch.sigmoid(z) * ~dead
+        p = score / (score.sum(1, keepdim=True) + (~alive)[:, None].double())
+    else:
+        score = p = torch.softmax(z, 1) * alive[:, None]
+    cuts = [0, T] if s["seq"] is None else s["seq"].tolist()
+    lens = [int(alive[i:j].sum()) for i, j in zip(cuts, cuts[1:])]
+    full = max(sum(n > 0 for n in lens), 1)
+    M = E - (0 if s["expert_mask"] is None else int((s["expert_mask"] == 0).sum()))
+    bal, rows = z.sum() * 0.0, []
+    b = 2 * s["z_coef"] / max(sum(lens), 1)
+    for i, j, n in zip(cuts, cuts[1:], lens):
+        if s["counts"] is not None:
+            cnt = s["counts"].double()
+        else:
+            e = s["expert"][i * k:j * k]
+            cnt = torch.stack([(e == x).sum() for x in range(E)]).double()
+        a = cnt / max(float(cnt.sum()), 1.0) * (s["coef"] * M / (n * full) if n else 0.0)
+        bal = bal + (p[i:j].sum(0) * a).sum()
+        rows.append(torch.cat([a, torch.full((1,), b, dtype=torch.float64, device=DEVICE)]))
+    lse = torch.logsumexp(z, 1)[cuts[0]:cuts[-1]]
+    zl = 0.5 * b * (lse.square() * alive[cuts[0]:cuts[-1]]).sum()
+    return z, score, alive, bal, zl, torch.stack(rows)
+
+
+def _exact_random(s, blocks):
+    M = 2 ** 32
+
+    def mix(x):
+        for shift, by in ((16, ROOT2), (15, ROOT3)):
+            x = (x ^ (x >> shift)) * by % M
+        return x ^ (x >> 16)
+
+    key = 0
+    for i, part in enumerate((s["seed"] % M, s["seed"] // M, s["step"] % M, s["step"] // M)):
+        key = mix(((key ^ part) + GOLD) % M)
+    at = torch.arange(blocks, device=DEVICE)
+    h = (mix((at * GOLD + key) % M)[:, None] + torch.arange(BLOCK, device=DEVICE) * GOLD) % M
+    h = (h ^ (h >> 16)) * ROOT2 % M
+    h = h ^ (h >> 15)
+    q = h * ROOT3 % M
+    return (h % 65536).double(), (h // 65536).double(), ((q ^ (q >> 16)) % 65536).double()
+
+
+def _exact_round(x, bits, r):
+    """x to so many bits behind the leading one, up with the probability of what is cut off."""
+    step = torch.exp2(torch.frexp(x)[1].double() - 1 - bits)
+    return torch.where(x == 0, x, torch.sign(x) * torch.floor(x.abs() / step + r) * step)
+
+
+def _exact_8bit(x, r, octaves, signed):
+    most = x.abs().amax(1, keepdim=True)
+    mant, e = torch.frexp(most)
+    e = e - 1 + (mant > 0.9375).int()  # (the largest must not round past 1.875 of its octave)
+    q = _exact_round(x, 3, (r * 16 + 8) / 2 ** 20)
+    least = 1.125 * torch.exp2(e.double() - (octaves - 1))
+    if signed:
+        return torch.where(q.abs() < least, torch.zeros_like(q), q)
+    return torch.where((x > 0) & (q < least), least.expand_as(q), q)
+
+
+def exact(case, seed):
+    s = prepare(case, seed)
+    c = case
+    if c["op"] == "sumsq":
+        g = s["g"].double()
+        return dict(sumsq=torch.dot(g, g).view(1))
+    if c["op"] in ("balance", "balance_bwd"):
+        z, score, alive, bal, zl, saved = _exact_balance(s)
+        if c["op"] == "balance":
+            out = dict(loss=torch.stack([bal, zl]).detach(), saved=saved)
+            return out if s["counts"] is not None else dict(out, counts=None)
+        total = s["dloss"][0].double() * bal + s["dloss"][1].double() * zl
+        if s["dweight"] is not None:
+            e = s["expert"].view(c["T"], c["k"]).long()
+            there = (e >= 0).double()
+            w = score.gather(1, e.clamp_min(0)) * there
+            if c["renorm"]:
+                w = w / (w.sum(1, keepdim=True) + (there.sum(1, keepdim=True) == 0).double())
+            total = total + (w.reshape(-1) * s["dweight"].double()).sum()
+        return dict(dlogits=torch.autograd.grad(total, z)[0])
+    g, scale = s["g"].double(), s["scale"]
+    if c["clip"]:
+        scale *= min(1.0, s["max_norm"] / (scale * float(torch.linalg.vector_norm(g))))
+    g = scale * g
+    if c["bits"] == 8:
+        m, v = _decode(s["m"], s["m_exp"], True).double(), _decode(s["v"], s["v_exp"], False).double()
+    else:
+        m, v = s["m"].double(), s["v"].double()
+    m = m.view(-1).lerp(g, 1 - s["beta1"])
+    v = v.view(-1).lerp(g.square(), 1 - s["beta2"])
+    w = (s["p"] if s["master"] is None else s["master"]).double()
+    hat = m / (1 - s["beta1"] ** s["step"])
+    den = (v / (1 - s["beta2"] ** s["step"])).sqrt() + s["eps"]
+    decay = s["decay"].double().expand(-1, BLOCK).reshape(-1)
+    w = w - s["lr"] * (hat / den + decay * w)
+    out = dict(p=w, master=None if s["master"] is None else w, m=m, v=v)
+    if c["bits"] == 8 or (c["p"] == "bf16" and s["master"] is None):
+        rm, rv, rp = _exact_random(s, s["first"][-1])
+        if c["bits"] == 8:
+            out.update(m=_exact_8bit(m.view(-1, BLOCK), rm, 16, True).view(-1),
+                       v=_exact_8bit(v.view(-1, BLOCK), rv, 32, False).view(-1))
+        if c["p"] == "bf16" and s["master"] is None:
+            out.update(p=_exact_round(w, 7, rp.view(-1) / 65536))
+    return out
