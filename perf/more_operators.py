@@ -257,14 +257,14 @@ def _balance_plain(s):
     f = counts.view(S, E).double()
     f = f / f.sum(1, keepdim=True).clamp_min(1.0)
     M = E if s["expert_mask"] is None else (s["expert_mask"] != 0).sum()
-    a = (s["coef"] * M * f / n.clamp_min(1.0)[:, None] / (n > 0).sum().clamp_min(1)).float()
-    a = a.masked_fill((n == 0)[:, None], 0.0)
-    b = (2.0 * s["z_coef"] / n.sum().clamp_min(1.0)).float()
-    out["saved"] = torch.cat([a, b.expand(S, 1)], 1)
+    a = (M * f / n.clamp_min(1.0)[:, None]).masked_fill((n == 0)[:, None], 0.0)
+    factor = torch.stack([s["coef"] / (n > 0).sum().clamp_min(1).double(),
+                          2.0 * s["z_coef"] / n.sum().clamp_min(1.0)])
+    out["saved"] = torch.cat([a.view(-1), factor]).float()
     z = torch.zeros((), dtype=torch.float64, device=DEVICE)
     if c["z"]:
-        z = 0.5 * b.double() * (lse[:, 0].double().square() * used).sum()
-    out["loss"] = torch.stack([(a.double() * sums).sum(), z]).float()
+        z = 0.5 * (lse[:, 0].double().square() * used).sum()
+    out["loss"] = (factor * torch.stack([(a * sums).sum(), z])).float()
     return out
 
 
@@ -273,13 +273,13 @@ def _balance_bwd_plain(s):
     T, k = c["T"], c["k"]
     p, rest, lse, live = _shares(s)
     at, S = _places(s)
-    saved = torch.cat([s["saved"], torch.zeros_like(s["saved"][:1])])[at]
-    a, b = saved[:, :-1], saved[:, -1:]
-    d = s["dloss"][0] * p * (a - (p * a).sum(1, keepdim=True))
+    f = s["dloss"] * s["saved"][-2:]
+    a = torch.cat([s["saved"][:-2], torch.zeros(c["E"], device=DEVICE)]).view(S + 1, -1)[at]
+    d = f[0] * p * (a - (p * a).sum(1, keepdim=True))
     if rest is not None:
         d = d * rest
     if c["z"]:
-        d = d + s["dloss"][1] * b * lse * p
+        d = d + f[1] * (at < S)[:, None] * lse * p
     d = d.masked_fill((p == 0) | ~live[:, None], 0.0)
     if s["dweight"] is not None:
         z, _ = _eligible(s)
@@ -426,7 +426,7 @@ def _handle(s):
             o = dict(dlogits=new(c["T"], c["E"], dtype=TYPES[c["dtype"]]))
             return lambda: L.lrm_balance_bwd(b, s["saved"], o["dlogits"], dloss=s["dloss"],
                                              dweight=s["dweight"]), o
-        o = dict(loss=new(2, dtype=torch.float32), saved=new(S, c["E"] + 1, dtype=torch.float32))
+        o = dict(loss=new(2, dtype=torch.float32), saved=new(S * c["E"] + 2, dtype=torch.float32))
         if s["counts"] is None:
             o.update(counts=new(S, c["E"], dtype=torch.int32))
         ws = new(L.lrm_balance_workspace_size(b), dtype=torch.uint8)
@@ -487,9 +487,9 @@ def work(case):
         T, E, k, S = c["T"], c["E"], c["k"], max(c["S"], 1)
         rows = T * E * SIZE[c["dtype"]]
         if c["op"] == "balance":
-            n = rows + S * (2 * E + 1) * 4 + (0 if c["counts"] else T * k * 4)
+            n = rows + S * E * 8 + (0 if c["counts"] else T * k * 4)
             return dict(bytes=n, flops=6.0 * T * E)
-        n = 2 * rows + S * (E + 1) * 4 + (T * k * 8 if c["weights"] else 0)
+        n = 2 * rows + S * E * 4 + (T * k * 8 if c["weights"] else 0)
         return dict(bytes=n, flops=9.0 * T * E)
     n = sum(_sizes(c)[0])
     if c["op"] == "sumsq":
@@ -525,19 +525,20 @@ def _exact_balance(s):
     full = max(sum(n > 0 for n in lens), 1)
     M = E - (0 if s["expert_mask"] is None else int((s["expert_mask"] == 0).sum()))
     bal, rows = z.sum() * 0.0, []
-    b = 2 * s["z_coef"] / max(sum(lens), 1)
+    factor = [s["coef"] / full, 2 * s["z_coef"] / max(sum(lens), 1)]
     for i, j, n in zip(cuts, cuts[1:], lens):
         if s["counts"] is not None:
             cnt = s["counts"].double()
         else:
             e = s["expert"][i * k:j * k]
             cnt = torch.stack([(e == x).sum() for x in range(E)]).double()
-        a = cnt / max(float(cnt.sum()), 1.0) * (s["coef"] * M / (n * full) if n else 0.0)
-        bal = bal + (p[i:j].sum(0) * a).sum()
-        rows.append(torch.cat([a, torch.full((1,), b, dtype=torch.float64, device=DEVICE)]))
+        a = cnt / max(float(cnt.sum()), 1.0) * (M / n if n else 0.0)
+        bal = bal + factor[0] * (p[i:j].sum(0) * a).sum()
+        rows.append(a)
+    rows.append(torch.tensor(factor, dtype=torch.float64, device=DEVICE))
     lse = torch.logsumexp(z, 1)[cuts[0]:cuts[-1]]
-    zl = 0.5 * b * (lse.square() * alive[cuts[0]:cuts[-1]]).sum()
-    return z, score, alive, bal, zl, torch.stack(rows)
+    zl = 0.5 * factor[1] * (lse.square() * alive[cuts[0]:cuts[-1]]).sum()
+    return z, score, alive, bal, zl, torch.cat(rows)
 
 
 def _exact_random(s, blocks):
