@@ -579,6 +579,59 @@ lrm_status lrm_route_share(int32_t T, int32_t k, const int32_t* expert, const fl
                            size_t ws_bytes, void* stream);
 size_t lrm_route_share_workspace_size(int32_t T, int32_t k);
 
+/* --------------------------------------------- balance of the experts' load */
+
+/* Balance loss and z loss of a router, per sequence or over the whole batch.
+ * Tokens t in [seq[s], seq[s+1]) form sequence s (tokens before the first and
+ * behind the last offset belong to none).  With the eligible experts of the
+ * router (see lrm_router; its bias, groups, scale and renormalisation take no part):
+ *   p_te = softmax of z over the eligible experts, or sigmoid(z_te) over its sum;
+ *          a token without eligible experts is left out (n_s: the others of s)
+ *   c_se = slots of the choice that name e, in s (see counts), M = experts whose
+ *          expert_mask is not 0, S' = sequences with n_s > 0, n = sum of n_s
+ *   f_se = c_se / sum over e of c_se (0 where there is none),
+ *   a_se = M f_se / n_s (0 where n_s = 0)
+ *   balance = coef / S' sum over s, e of a_se (sum over the tokens of s of p_te)
+ *   z       = z_coef / n sum over the tokens of sequences of (log sum_e exp z_te)^2
+ * The counts have no gradient.  coef = 1 and a balanced choice give balance = 1 or
+ * so.  Sums over tokens: fp32 over at most 512 tokens of a run, then fp64. */
+typedef struct lrm_balance {
+  lrm_router router;
+  const int32_t* expert; /* device [T*k], the choice (of lrm_route, or any: entries outside
+                            [0, E) or of masked experts and tokens are empty slots); may be
+                            NULL where counts is given and no routing gradient is wanted */
+  const int32_t* counts; /* device [S][E], c_se >= 0 (lrm_route's, or their sums over GPUs:
+                            only the ratios inside a sequence count), or NULL: from expert */
+  const int32_t* seq;    /* device [S+1], non-decreasing in [0, T] (results are undefined
+                            otherwise, every access stays in bounds), or NULL: S = 1, all tokens */
+  int32_t S;             /* sequences, 1..2^20; S * E < 2^31 */
+  float coef, z_coef;    /* finite; z_coef 0 with sigmoid scores */
+  int32_t _pad;
+} lrm_balance;
+
+/* The losses and what their gradient needs:
+ *   loss:   device [2] fp32 output: balance, z
+ *   saved:  device [S*E + 2] fp32 output: a_se, then coef / S' and 2 z_coef / n
+ *   counts: device [S][E] output, c_se, or NULL (must be NULL where b->counts is given)
+ * ws: device scratch of lrm_balance_workspace_size(b) bytes, 256-byte aligned. */
+lrm_status lrm_balance_loss(const lrm_balance* b, float* loss, float* saved, int32_t* counts,
+                            void* ws, size_t ws_bytes, void* stream);
+size_t lrm_balance_workspace_size(const lrm_balance* b);
+
+/* Gradient of the logits, of both losses and (dweight not NULL) of the routing
+ * weights as lrm_route_bwd forms it, added in fp32 and rounded once:
+ *   saved:   of lrm_balance_loss on the same b (its coef, z_coef and counts are
+ *            not read here)
+ *   dloss:   device [2] fp32, the gradients with respect to the two losses, or
+ *            NULL: 1 and 1
+ *   dweight: device [T*k] fp32, as lrm_route_bwd takes it for b->expert (all of the
+ *            router's settings apply), or NULL
+ *   dlogits: device [T][E] output of the logits' dtype, rows ldd >= E elements
+ *            apart, every element written (0 for masked ones); tokens of no
+ *            sequence have the gradient of the weights only */
+lrm_status lrm_balance_bwd(const lrm_balance* b, const float* saved, const float* dloss,
+                           const float* dweight, void* dlogits, int64_t ldd, void* stream);
+
 /* ------------------------------------------------------- the experts forward */
 
 /* Activation of a LINEAR projection (GELU: z * Phi(z), the exact form). */
@@ -663,6 +716,99 @@ typedef struct lrm_pair_grad_outputs {
 lrm_status lrm_pair_grad(const lrm_pair_grad_problem* g, const lrm_pair_grad_outputs* out,
                          void* ws, size_t ws_bytes, void* stream);
 size_t lrm_pair_grad_workspace_size(const lrm_pair_grad_problem* g);
+
+/* ---------------------------------------------- update of the parameters */
+
+/* Tensors that are updated together (a layer's weights, or a whole model's). */
+typedef struct lrm_param {
+  void* p;           /* device [n] of p_dtype: the weights */
+  const void* g;     /* device [n] of g_dtype: their gradient (dW of lrm_expert_backward) */
+  float* master;     /* device [n] fp32 weights behind bf16 p, or NULL */
+  void* m;           /* device [n]: first and second moment, fp32 or 8-bit codes; */
+  void* v;           /*   zero bytes everywhere are the state before the first step */
+  uint8_t* m_exp;    /* 8-bit moments: device [(n + 31) / 32], exponents of the */
+  uint8_t* v_exp;    /*   blocks (any address); NULL for fp32 moments */
+  int64_t n;         /* elements, 0..2^40 */
+  float lr;          /* factor on the step's learning rate, finite, >= 0 */
+  float weight_decay;/* finite */
+} lrm_param;
+
+/* How the moments are held.  LRM_MOMENTS_8BIT: blocks of 32 elements (the last
+ * one of a tensor may be shorter) share an exponent byte x; a code c stands for
+ *   v: 0 for c = 0, else (1 + (c & 7) / 8) 2^((c >> 3) - 31 + x - 127)
+ *   m: the same of c & 127 with 15 for 31, negative where bit 7 is set
+ * (32 and 16 octaves of 3-bit mantissas below the block's largest element). */
+typedef enum lrm_moments { LRM_MOMENTS_F32 = 0, LRM_MOMENTS_8BIT = 1 } lrm_moments;
+
+typedef struct lrm_params {
+  int32_t n;          /* tensors, 0..65536 */
+  int32_t p_dtype;    /* lrm_dtype of every p */
+  int32_t g_dtype;    /* lrm_dtype of every g */
+  int32_t moments;    /* lrm_moments */
+  int32_t masters;    /* 1: every tensor has a master (bf16 p), 0: none has */
+  int32_t _pad;
+  const lrm_param* param; /* HOST [n], read during the call */
+  void* table;        /* device, lrm_params_table_size(n) bytes, 256-byte aligned */
+  int64_t chunks;     /* sum of (param[i].n + 2047) / 2048, as lrm_params_table sets it */
+} lrm_params;
+
+/* Describes the tensors to the GPU: checks them, writes the table (kernels on the
+ * stream, 32 tensors each) and ps->chunks.  The table, the descriptor and the
+ * tensors stay where they are for every later call with ps.  p, m and v may be NULL
+ * in every tensor: such a list serves lrm_grad_sumsq only.  Tensors are dense and
+ * element-aligned (16-byte aligned ones are faster); what is written (p, master, m,
+ * v, exponents) must not share memory with any other array of the list. */
+lrm_status lrm_params_table(lrm_params* ps, size_t table_bytes, void* stream);
+size_t lrm_params_table_size(int32_t n);
+
+/* Sum of squares of all gradients (param[i].g), in fp64:
+ *   sumsq: device [1] fp64 output, 8-byte aligned (0 for no elements)
+ * ws: device scratch of lrm_sumsq_workspace_size(ps) bytes, 8-byte aligned. */
+lrm_status lrm_grad_sumsq(const lrm_params* ps, double* sumsq, void* ws, size_t ws_bytes,
+                          void* stream);
+size_t lrm_sumsq_workspace_size(const lrm_params* ps);
+
+/* One AdamW step over all tensors.  With t the step and c the gradients' factor:
+ *   m = beta1 m + (1 - beta1) c g         v = beta2 v + (1 - beta2) (c g)^2
+ *   p = p (1 - r wd) - r / (1 - beta1^t) m / (sqrt(v / (1 - beta2^t)) + eps)
+ * with r = lr * param.lr and wd = param.weight_decay, in fp32 (p the master, where
+ * there is one).
+ * Clipping: norm = |grad_scale| sqrt(sum of sumsq[0 .. n_sumsq)) (several
+ * entries: of several lists, or GPUs), c = grad_scale * min(1, max_norm /
+ * norm).  If the sum is not finite the call leaves everything as it was, the
+ * step counter too.  Without sumsq c = grad_scale.
+ * Rounding: p of bf16 with a master is the nearest of it.  What is rounded and
+ * read again by the next step, 8-bit moments and bf16 p without a master, is
+ * rounded up with the probability of what is cut off, so that steps smaller than
+ * a rounding count on average; the random numbers are a function of seed, t and
+ * the element's place in the list.  A second moment that is not 0 does not
+ * become 0.  Gradients must be finite (or sumsq given: they are, then); 8-bit
+ * moments must stay below 2^126 in magnitude. */
+typedef struct lrm_adamw_step {
+  double lr;            /* finite, >= 0 */
+  double beta1, beta2;  /* [0, 1) */
+  double eps;           /* finite, > 0 */
+  double grad_scale;    /* finite */
+  double max_norm;      /* finite, > 0; 0: no clipping */
+  int64_t step;         /* t, 1..2^53 (not read where steps is given) */
+  uint64_t seed;
+  const double* sumsq;  /* device [n_sumsq], or NULL (max_norm 0) */
+  int32_t n_sumsq;      /* 1..1024 (0: sumsq NULL) */
+  int32_t _pad;
+  const float* lr_dev;  /* device [1], read in place of lr (schedules under a captured
+                           graph), or NULL */
+  int64_t* steps;       /* device [1], steps made so far: t is one more, and the call
+                           counts it; or NULL */
+} lrm_adamw_step;
+
+lrm_status lrm_adamw(const lrm_params* ps, const lrm_adamw_step* a, void* stream);
+
+/* The values that 8-bit moments stand for:
+ *   codes: device [n], exps: device [(n + 31) / 32], of lrm_param
+ *   second: 0 for m, 1 for v
+ *   out: device [n] of dtype (bf16 holds every value exactly) */
+lrm_status lrm_moment_read(int64_t n, int32_t second, const void* codes, const uint8_t* exps,
+                           int32_t dtype, void* out, void* stream);
 
 /* ------------------------------------------------------------------ errors */
 

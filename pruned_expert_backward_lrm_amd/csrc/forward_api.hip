@@ -55,6 +55,35 @@ RouteArgs route_args(const lrm_router* r) {
 
 bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
 
+// ---------------------------------------------------------------- balance
+
+lrm_status check_balance(const lrm_balance* b) {
+  if (!b) return LRM_ERR_NULL;
+  LRM_TRY(check_router(&b->router));
+  if (b->S < 1 || b->S > (1 << 20) || (int64_t)b->S * b->router.E > 0x7fffffffll)
+    return LRM_ERR_SHAPE;
+  if (!b->seq && b->S != 1) return LRM_ERR_SHAPE;
+  if (!std::isfinite(b->coef) || !std::isfinite(b->z_coef)) return LRM_ERR_UNSUPPORTED;
+  if (b->z_coef != 0.f && b->router.score != LRM_SOFTMAX) return LRM_ERR_UNSUPPORTED;
+  if (!aligned4(b->expert) || !aligned4(b->counts) || !aligned4(b->seq)) return LRM_ERR_ALIGN;
+  return LRM_OK;
+}
+
+BalanceArgs carve_balance(Carve& c, const lrm_balance* b) {
+  BalanceArgs g{};
+  const int E = b->router.E, T = b->router.T;
+  g.S = b->S;
+  g.chunk = balance_chunk(T);
+  g.chunks = (int)(((int64_t)T + g.chunk - 1) / g.chunk);
+  const int64_t rows = (int64_t)g.chunks + b->S;
+  g.sums = c.take<float>(rows * E);
+  if (!b->counts) g.cnt = c.take<int32_t>(rows * E);
+  g.rows = c.take<BalanceRow>(rows);
+  g.seq_bal = c.take<double>((int64_t)b->S * ((E + kJoinCols - 1) / kJoinCols));
+  g.seq_rows = c.take<BalanceSeq>(b->S);
+  return g;
+}
+
 // --------------------------------------------------------------- bucketing
 // The pairs in expert order (every pair kept), as the backward's bucketing
 // with LRM_KEEP_ALL makes it.
@@ -357,6 +386,48 @@ lrm_status lrm_route_bwd(const lrm_router* r, const int32_t* expert, const float
     return LRM_ERR_ALIGN;
   LRM_TRY_HIP(launch_route_bwd(route_args(r), expert, dweight, dlogits, ldd,
                                rows16(dlogits, ldd, r->dtype), as_stream(stream)));
+  return LRM_OK;
+}
+
+size_t lrm_balance_workspace_size(const lrm_balance* b) {
+  if (check_balance(b) != LRM_OK) return 0;
+  Carve c(nullptr);
+  carve_balance(c, b);
+  return c.size();
+}
+
+lrm_status lrm_balance_loss(const lrm_balance* b, float* loss, float* saved, int32_t* counts,
+                            void* ws, size_t ws_bytes, void* stream) {
+  LRM_TRY(check_balance(b));
+  if (!loss || !saved) return LRM_ERR_NULL;
+  if (!b->counts && !b->expert && b->router.T > 0) return LRM_ERR_NULL;
+  if (b->counts && counts) return LRM_ERR_UNSUPPORTED;
+  if (!aligned4(loss) || !aligned4(saved) || !aligned4(counts)) return LRM_ERR_ALIGN;
+  if (!ws || ws_bytes < lrm_balance_workspace_size(b)) return LRM_ERR_WORKSPACE;
+  if ((reinterpret_cast<uintptr_t>(ws) & (kAlign - 1)) != 0) return LRM_ERR_ALIGN;
+  Carve c(ws);
+  BalanceArgs g = carve_balance(c, b);
+  g.coef = b->coef; g.z_coef = b->z_coef;
+  g.expert = b->expert; g.counts = b->counts; g.seq = b->seq;
+  g.loss = loss; g.saved = saved; g.counts_out = counts;
+  LRM_TRY_HIP(launch_balance(route_args(&b->router), g, as_stream(stream)));
+  return LRM_OK;
+}
+
+lrm_status lrm_balance_bwd(const lrm_balance* b, const float* saved, const float* dloss,
+                           const float* dweight, void* dlogits, int64_t ldd, void* stream) {
+  LRM_TRY(check_balance(b));
+  const lrm_router* r = &b->router;
+  if (!saved || (r->T > 0 && (!dlogits || (dweight && !b->expert)))) return LRM_ERR_NULL;
+  if (ldd < r->E) return LRM_ERR_SHAPE;
+  if (!aligned4(saved) || !aligned4(dloss) || !aligned4(dweight) ||
+      reinterpret_cast<uintptr_t>(dlogits) % esize(r->dtype) != 0)
+    return LRM_ERR_ALIGN;
+  BalanceBwdArgs g{};
+  g.S = b->S; g.vec_out = rows16(dlogits, ldd, r->dtype); g.ldd = ldd;
+  g.expert = b->expert; g.seq = b->seq; g.saved = saved; g.dloss = dloss;
+  g.dweight = dweight; g.dlogits = dlogits;
+  LRM_TRY_HIP(launch_balance_bwd(route_args(r), g, as_stream(stream)));
   return LRM_OK;
 }
 

@@ -1,0 +1,412 @@
+// Update of the parameters: the gradients' sum of squares, the AdamW step, and
+// the values of 8-bit moments.  (What becomes of the weight gradients that the
+// LRMoE backward pass makes; the pages leave the optimizer as it is.)
+//
+// All are bound by memory: one pass over every array, each element read and
+// written once.  The tensors of a list are cut into chunks of 2048 elements, 8
+// neighbours a thread; persistent blocks take the chunks in turn and find a
+// chunk's tensor in the table by bisection (wave-uniform, so scalar loads).
+//
+// 8-bit moments (see lrm.h): 4 lanes hold a block of 32, whose largest magnitude
+// they find with two quad permutations.  The shared exponent x is the largest's,
+// one more where its mantissa is above 7/8, so that rounding up never leaves
+// the top octave.  A code is the fp32 bits above bit 20, less the exponent of
+// the block's lowest octave; 16 random bits below bit 20 (and a half of what is
+// below them) are added first, so an element is rounded up with the probability
+// of what is cut off.  With nearest rounding v would stand still: a step of beta2
+// = 0.999 changes it by 0.1 %, half a step of three mantissa bits is 3 to 6 %.
+#include "common.h"
+#include "update.h"
+
+namespace lrm {
+
+namespace {
+
+// The table does not change while a kernel runs: read as constant memory, so that
+// the loads stay scalar although the kernel stores to memory as well.
+#ifdef LRM_CPU_EMU
+#define LRM_CONST
+#else
+#define LRM_CONST __attribute__((address_space(4)))
+#endif
+
+// The tensor that holds chunk c: the last one that starts at or before it.
+__device__ __forceinline__ ParamEntry tensor_of(const ParamTable& t, int64_t c) {
+  const LRM_CONST int64_t* chunk0 = (const LRM_CONST int64_t*)t.chunk0;
+  int lo = 0, hi = t.n;
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (chunk0[mid] <= c) lo = mid;
+    else hi = mid;
+  }
+  const LRM_CONST ParamEntry* e = (const LRM_CONST ParamEntry*)t.entry + lo;
+  return ParamEntry{e->p, e->g, e->master, e->m, e->v, e->m_exp, e->v_exp, e->n,
+                    e->chunk0, e->block0, e->lr, e->decay, e->vec, 0};
+}
+
+// Eight neighbours from element i (those at or past n: 0).
+template <bool BF16>
+__device__ __forceinline__ void load8(const void* base, int64_t i, int64_t n, bool vec, float (&x)[8]) {
+  if (vec && i + 8 <= n) {
+    if constexpr (BF16) {
+      const u32x4 q = *reinterpret_cast<const u32x4*>((const uint16_t*)base + i);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        x[2 * j] = bf16_lo(q[j]);
+        x[2 * j + 1] = bf16_hi(q[j]);
+      }
+    } else {
+      const f32x4 q = *reinterpret_cast<const f32x4*>((const float*)base + i);
+      const f32x4 r = *reinterpret_cast<const f32x4*>((const float*)base + i + 4);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        x[j] = q[j];
+        x[4 + j] = r[j];
+      }
+    }
+    return;
+  }
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    x[j] = 0.f;
+    if (i + j < n)
+      x[j] = BF16 ? bf16_to_f32(((const uint16_t*)base)[i + j]) : ((const float*)base)[i + j];
+  }
+}
+__device__ __forceinline__ void store8(float* base, int64_t i, int64_t n, bool vec, const float (&x)[8]) {
+  if (vec && i + 8 <= n) {
+    *reinterpret_cast<f32x4*>(base + i) = f32x4{x[0], x[1], x[2], x[3]};
+    *reinterpret_cast<f32x4*>(base + i + 4) = f32x4{x[4], x[5], x[6], x[7]};
+    return;
+  }
+#pragma unroll
+  for (int j = 0; j < 8; ++j)
+    if (i + j < n) base[i + j] = x[j];
+}
+// bf16 bits in the upper halves of x
+__device__ __forceinline__ void store8_hi(uint16_t* base, int64_t i, int64_t n, bool vec,
+                                          const uint32_t (&x)[8]) {
+  if (vec && i + 8 <= n) {
+    u32x4 q;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) q[j] = (x[2 * j] >> 16) | (x[2 * j + 1] & 0xffff0000u);
+    *reinterpret_cast<u32x4*>(base + i) = q;
+    return;
+  }
+#pragma unroll
+  for (int j = 0; j < 8; ++j)
+    if (i + j < n) base[i + j] = (uint16_t)(x[j] >> 16);
+}
+
+// Eight codes, four a word.
+__device__ __forceinline__ u32x2 load_codes(const uint8_t* base, int64_t i, int64_t n, bool vec) {
+  if (vec && i + 8 <= n) return *reinterpret_cast<const u32x2*>(base + i);
+  u32x2 q = {0u, 0u};
+#pragma unroll
+  for (int j = 0; j < 8; ++j)
+    if (i + j < n) q[j >> 2] |= (uint32_t)base[i + j] << (8 * (j & 3));
+  return q;
+}
+__device__ __forceinline__ void store_codes(uint8_t* base, int64_t i, int64_t n, bool vec, u32x2 q) {
+  if (vec && i + 8 <= n) {
+    *reinterpret_cast<u32x2*>(base + i) = q;
+    return;
+  }
+#pragma unroll
+  for (int j = 0; j < 8; ++j)
+    if (i + j < n) base[i + j] = (uint8_t)(q[j >> 2] >> (8 * (j & 3)));
+}
+
+// Octaves below the shared exponent's: 15 (m) or 31 (v).
+constexpr int kTopM = 15, kTopV = 31;
+
+template <bool SECOND>
+__device__ __forceinline__ void decode8(u32x2 q, uint32_t e, float (&x)[8]) {
+  const uint32_t low = (e - (SECOND ? kTopV : kTopM)) << 23;
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    const uint32_t b = q[j >> 2] >> (8 * (j & 3));
+    const uint32_t c = b & (SECOND ? 255u : 127u);
+    uint32_t u = (c << 20) + low;
+    u = c ? u : 0u;
+    if (!SECOND) u |= (b << 24) & 0x80000000u;
+    x[j] = __uint_as_float(u);
+  }
+}
+
+// The exponent that a block's four lanes share, from the bits of their largest
+// magnitudes.
+__device__ __forceinline__ uint32_t quad_max(uint32_t u) {
+  uint32_t o = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)u, 0xB1, 0xf, 0xf, false);
+  u = o > u ? o : u;
+  o = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)u, 0x4E, 0xf, 0xf, false);
+  return o > u ? o : u;
+}
+template <bool SECOND>
+__device__ __forceinline__ uint32_t block_exponent(const float (&x)[8]) {
+  constexpr uint32_t least = (SECOND ? kTopV : kTopM) + 1;
+  float top = 0.f;
+#pragma unroll
+  for (int j = 0; j < 8; ++j) top = fmaxf(top, fabsf(x[j]));
+  const uint32_t e = (quad_max(__float_as_uint(top)) + 0xfffffu) >> 23;
+  return e > least ? e : least;
+}
+// r: 16 random bits an element at bit SECOND ? 16 : 0 of each.
+template <bool SECOND>
+__device__ __forceinline__ u32x2 encode8(const float (&x)[8], uint32_t e, const uint32_t (&r)[8]) {
+  constexpr int top = SECOND ? kTopV : kTopM, most = 8 * top + 7;
+  const int low = (int)((e - top) << 23);
+  u32x2 q = {0u, 0u};
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    const uint32_t u = __float_as_uint(x[j]), mag = u & 0x7fffffffu;
+    const uint32_t add = ((SECOND ? r[j] >> 16 : r[j] & 0xffffu) << 4) | 8u;
+    int c = ((int)(mag + add) - low) >> 20;
+    const int least = SECOND && mag ? 1 : 0;
+    c = c < least ? least : (c > most ? most : c);
+    if (!SECOND) c |= c ? (int)(u >> 24 & 128u) : 0;
+    q[j >> 2] |= (uint32_t)c << (8 * (j & 3));
+  }
+  return q;
+}
+
+// ------------------------------------------------------------------ table
+__global__ __launch_bounds__(64) void k_params_table(TableBatch b, int first, int count, int n,
+                                                     int64_t chunks, ParamEntry* entry,
+                                                     int64_t* chunk0) {
+  const int i = threadIdx.x;
+  if (i < count) {
+    entry[first + i] = b.entry[i];
+    chunk0[first + i] = b.entry[i].chunk0;
+  }
+  if (i == 0 && first + count == n) chunk0[n] = chunks;
+}
+
+// --------------------------------------------------------- sum of squares
+// Squares and sums in fp64: nothing overflows, and what is not finite shows.
+template <bool BF16>
+__global__ __launch_bounds__(256) void k_grad_sumsq(ParamTable t, double* part) {
+  __shared__ double lds[4];
+  const int64_t chunks = t.chunk0[t.n];
+  double sum = 0.0;
+  for (int64_t c = blockIdx.x; c < chunks; c += gridDim.x) {
+    const ParamEntry e = tensor_of(t, c);
+    float x[8];
+    load8<BF16>(e.g, (c - e.chunk0) * kChunk + threadIdx.x * 8, e.n, e.vec != 0, x);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) sum = fma((double)x[j], (double)x[j], sum);
+  }
+  sum = wave_sum(sum);
+  if (lane_id() == 0) lds[threadIdx.x >> 6] = sum;
+  __syncthreads();
+  if (threadIdx.x == 0) part[blockIdx.x] = (lds[0] + lds[1]) + (lds[2] + lds[3]);
+}
+
+__global__ __launch_bounds__(256) void k_sumsq_join(int n, const double* part, double* sumsq) {
+  __shared__ double lds[4];
+  double v[kUpdateBlocks / 256];
+#pragma unroll
+  for (int q = 0; q < kUpdateBlocks / 256; ++q) {
+    const int i = q * 256 + threadIdx.x;
+    v[q] = i < n ? part[i] : 0.0;
+  }
+  double sum = 0.0;
+#pragma unroll
+  for (int q = 0; q < kUpdateBlocks / 256; ++q) sum += v[q];
+  sum = wave_sum(sum);
+  if (lane_id() == 0) lds[threadIdx.x >> 6] = sum;
+  __syncthreads();
+  if (threadIdx.x == 0) sumsq[0] = (lds[0] + lds[1]) + (lds[2] + lds[3]);
+}
+
+// ------------------------------------------------------------------ AdamW
+__device__ __forceinline__ double total_of(const double* sumsq, int n) {
+  double s = 0.0;
+  for (int i = 0; i < n; ++i) s += sumsq[i];
+  return s;
+}
+__device__ __forceinline__ bool finite64(double x) { return x - x == 0.0; }
+
+template <int P, bool GB, bool EIGHT>
+__global__ __launch_bounds__(256) void k_adamw(ParamTable t, AdamArgs a) {
+  double f = a.grad_scale;
+  if (a.sumsq) {
+    const double sum = total_of(a.sumsq, a.n_sumsq);
+    if (!finite64(sum)) return;
+    const double norm = fabs(a.grad_scale) * sqrt(sum);
+    if (a.max_norm > 0.0 && norm > a.max_norm) f *= a.max_norm / norm;
+  }
+  const int64_t step = a.steps ? a.steps[0] + 1 : a.step;
+  const double lr = a.lr_dev ? (double)a.lr_dev[0] : a.lr;
+  const double size = lr / -expm1((double)step * a.ln1);
+  const float root = (float)(1.0 / sqrt(-expm1((double)step * a.ln2)));
+  const uint32_t key = step_key(a.seed, (uint64_t)step);
+  const float c = (float)f, b1 = (float)a.beta1, d1 = (float)(1.0 - a.beta1), b2 = (float)a.beta2,
+              d2 = (float)(1.0 - a.beta2), eps = (float)a.eps;
+  constexpr bool RANDOM_P = P == 1;
+  const int64_t chunks = t.chunk0[t.n];
+  for (int64_t ch = blockIdx.x; ch < chunks; ch += gridDim.x) {
+    const ParamEntry e = tensor_of(t, ch);
+    const int64_t i = (ch - e.chunk0) * kChunk + threadIdx.x * 8, n = e.n;
+    const bool vec = e.vec != 0;
+    const float up = (float)(size * (double)e.lr), down = (float)(lr * (double)e.lr * (double)e.decay);
+    float g[8], w[8], m[8], v[8];
+    const int64_t blk = i >> 5, blkc = i < n ? blk : 0;
+    load8<GB>(e.g, i, n, vec, g);
+    load8<P == 1>(P == 2 ? (const void*)e.master : e.p, i, n, vec, w);
+    if constexpr (EIGHT) {
+      const u32x2 qm = load_codes((const uint8_t*)e.m, i, n, vec);
+      const u32x2 qv = load_codes((const uint8_t*)e.v, i, n, vec);
+      decode8<false>(qm, e.m_exp[blkc], m);
+      decode8<true>(qv, e.v_exp[blkc], v);
+    } else {
+      load8<false>(e.m, i, n, vec, m);
+      load8<false>(e.v, i, n, vec, v);
+    }
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const float x = c * g[j];
+      m[j] = fmaf(b1, m[j], d1 * x);
+      v[j] = fmaf(b2, v[j], d2 * (x * x));
+      const float den = fmaf(__builtin_amdgcn_sqrtf(v[j]), root, eps);
+      w[j] = fmaf(-up, m[j] * __builtin_amdgcn_rcpf(den), fmaf(-down, w[j], w[j]));
+    }
+    uint32_t r[8];
+    if constexpr (EIGHT || RANDOM_P) {
+      const uint64_t b = (uint64_t)(e.block0 + blk);
+      const uint32_t kb = mix32(key + (uint32_t)b * kGold + (uint32_t)(b >> 32) * kRoot3) +
+                          (uint32_t)(i & 31) * kGold;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        r[j] = kb + (uint32_t)j * kGold;
+        r[j] ^= r[j] >> 16;
+        r[j] *= kRoot2;
+        r[j] ^= r[j] >> 15;
+      }
+    }
+    if constexpr (EIGHT) {
+      const uint32_t em = block_exponent<false>(m), ev = block_exponent<true>(v);
+      if (i < n) {
+        store_codes((uint8_t*)e.m, i, n, vec, encode8<false>(m, em, r));
+        store_codes((uint8_t*)e.v, i, n, vec, encode8<true>(v, ev, r));
+        if ((i & 31) == 0) {
+          e.m_exp[blk] = (uint8_t)em;
+          e.v_exp[blk] = (uint8_t)ev;
+        }
+      }
+    } else {
+      store8((float*)e.m, i, n, vec, m);
+      store8((float*)e.v, i, n, vec, v);
+    }
+    if constexpr (P != 1) store8(P == 2 ? e.master : (float*)e.p, i, n, vec, w);
+    if constexpr (P != 0) {
+      uint32_t u[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        u[j] = __float_as_uint(w[j]);
+        if constexpr (RANDOM_P) {
+          const uint32_t q = r[j] * kRoot3;
+          u[j] += (q ^ (q >> 16)) & 0xffffu;
+        } else if (j & 1) {
+          const uint32_t two = cvt_pk_bf16(w[j - 1], w[j]);
+          u[j - 1] = two << 16;
+          u[j] = two;
+        }
+      }
+      store8_hi((uint16_t*)e.p, i, n, vec, u);
+    }
+  }
+}
+
+// After the step: one more is made, if it was.
+__global__ __launch_bounds__(64) void k_count_step(AdamArgs a, int64_t* steps) {
+  if (threadIdx.x != 0) return;
+  if (a.sumsq && !finite64(total_of(a.sumsq, a.n_sumsq))) return;
+  steps[0] += 1;
+}
+
+// ---------------------------------------------------------------- reading
+template <bool SECOND, bool BF16>
+__global__ __launch_bounds__(256) void k_moment_read(int64_t n, const uint8_t* codes, const uint8_t* exps,
+                                                     bool vec, void* out) {
+  const int64_t step = (int64_t)gridDim.x * 2048;
+  for (int64_t i = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 8; i < n; i += step) {
+    float x[8];
+    decode8<SECOND>(load_codes(codes, i, n, vec), exps[i >> 5], x);
+    if constexpr (BF16) {
+      uint32_t u[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) u[j] = __float_as_uint(x[j]);
+      store8_hi((uint16_t*)out, i, n, vec, u);
+    } else {
+      store8((float*)out, i, n, vec, x);
+    }
+  }
+}
+
+template <int P, bool GB>
+void adamw_launch(const ParamTable& t, int grid, int eight, const AdamArgs& a, hipStream_t s) {
+  if (eight)
+    LRM_LAUNCH(grid, 256, 0, s, k_adamw<P, GB, true>)(t, a);
+  else
+    LRM_LAUNCH(grid, 256, 0, s, k_adamw<P, GB, false>)(t, a);
+}
+
+int update_grid(int64_t chunks) { return (int)(chunks < kUpdateBlocks ? chunks : kUpdateBlocks); }
+
+}  // namespace
+
+hipError_t launch_params_table(const TableBatch& b, int first, int count, int n, int64_t chunks,
+                               void* table, hipStream_t s) {
+  ParamEntry* entry = static_cast<ParamEntry*>(table);
+  LRM_LAUNCH(1, 64, 0, s, k_params_table)(b, first, count, n, chunks, entry,
+                                          reinterpret_cast<int64_t*>(entry + n));
+  return hipGetLastError();
+}
+
+hipError_t launch_grad_sumsq(const ParamTable& t, int64_t chunks, int g_bf16, double* part,
+                             double* sumsq, hipStream_t s) {
+  const int grid = update_grid(chunks);
+  if (grid > 0) {
+    if (g_bf16)
+      LRM_LAUNCH(grid, 256, 0, s, k_grad_sumsq<true>)(t, part);
+    else
+      LRM_LAUNCH(grid, 256, 0, s, k_grad_sumsq<false>)(t, part);
+  }
+  LRM_LAUNCH(1, 256, 0, s, k_sumsq_join)(grid, part, sumsq);
+  return hipGetLastError();
+}
+
+hipError_t launch_adamw(const ParamTable& t, int64_t chunks, int p, int g_bf16, int eight,
+                        const AdamArgs& a, int64_t* steps, hipStream_t s) {
+  const int grid = update_grid(chunks);
+  if (grid > 0) {
+    if (p == 0 && !g_bf16) adamw_launch<0, false>(t, grid, eight, a, s);
+    else if (p == 0) adamw_launch<0, true>(t, grid, eight, a, s);
+    else if (p == 1 && !g_bf16) adamw_launch<1, false>(t, grid, eight, a, s);
+    else if (p == 1) adamw_launch<1, true>(t, grid, eight, a, s);
+    else if (!g_bf16) adamw_launch<2, false>(t, grid, eight, a, s);
+    else adamw_launch<2, true>(t, grid, eight, a, s);
+  }
+  if (steps) LRM_LAUNCH(1, 64, 0, s, k_count_step)(a, steps);
+  return hipGetLastError();
+}
+
+hipError_t launch_moment_read(int64_t n, int second, const uint8_t* codes, const uint8_t* exps,
+                              int bf16, void* out, hipStream_t s) {
+  if (n <= 0) return hipSuccess;
+  const bool vec = (reinterpret_cast<uintptr_t>(codes) & 7u) == 0 && (reinterpret_cast<uintptr_t>(out) & 15u) == 0;
+  const int64_t blocks = (n + 2047) / 2048;
+  const int grid = (int)(blocks < 8 * kUpdateBlocks ? blocks : 8 * kUpdateBlocks);
+  if (second && bf16)
+    LRM_LAUNCH(grid, 256, 0, s, k_moment_read<true, true>)(n, codes, exps, vec, out);
+  else if (second)
+    LRM_LAUNCH(grid, 256, 0, s, k_moment_read<true, false>)(n, codes, exps, vec, out);
+  else if (bf16)
+    LRM_LAUNCH(grid, 256, 0, s, k_moment_read<false, true>)(n, codes, exps, vec, out);
+  else
+    LRM_LAUNCH(grid, 256, 0, s, k_moment_read<false, false>)(n, codes, exps, vec, out);
+  return hipGetLastError();
+}
+
+}  // namespace lrm

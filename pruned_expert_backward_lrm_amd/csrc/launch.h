@@ -258,6 +258,50 @@ hipError_t launch_route_share(int64_t n, int k, const int32_t* expert, const flo
                               int E, int32_t* out_token, int32_t* out_expert, float* out_weight,
                               int32_t* out_slot, int32_t* out_n, int32_t* cnt, hipStream_t s);
 
+// --------------------------------------------------- balance of the load
+// What a chunk of tokens and a sequence have in common: live tokens, filled slots,
+// sum of log^2; and the same of a whole sequence.
+struct BalanceRow {
+  double lse2;
+  int live, filled;
+};
+struct BalanceSeq {
+  double lse2, live;
+};
+// lrm_balance_loss: chunks runs of chunk tokens (balance_chunk), sums and cnt
+// [chunks + S][E], rows [chunks + S], seq_bal [S][tiles of kJoinCols experts],
+// seq_rows [S].  cnt is null where counts is given.
+struct BalanceArgs {
+  int S, chunk, chunks;
+  float coef, z_coef;
+  const int32_t* expert;
+  const int32_t* counts;
+  const int32_t* seq;
+  float* loss;
+  float* saved;
+  int32_t* counts_out;
+  float* sums;
+  int32_t* cnt;
+  BalanceRow* rows;
+  double* seq_bal;
+  BalanceSeq* seq_rows;
+};
+constexpr int kBalanceChunks = 512;
+constexpr int kJoinCols = 64;
+int balance_chunk(int T);
+hipError_t launch_balance(const RouteArgs& a, const BalanceArgs& b, hipStream_t s);
+struct BalanceBwdArgs {
+  int S, vec_out;
+  int64_t chunk, ldd;
+  const int32_t* expert;
+  const int32_t* seq;
+  const float* saved;
+  const float* dloss;
+  const float* dweight;
+  void* dlogits;
+};
+hipError_t launch_balance_bwd(const RouteArgs& a, const BalanceBwdArgs& b, hipStream_t s);
+
 // ------------------------------------------------- epilogue backward
 // lrm_pair_grad.  With dbias: the pairs bucketed by expert (offsets [E+1], kept
 // [N], pos [N], by launch_bucket with keep_all) and part, scratch of

@@ -40,6 +40,8 @@ ROWS = {"token": LRM_ROWS_TOKEN, "pair": LRM_ROWS_PAIR}
 SCORES = {"softmax": 0, "sigmoid": 1}
 GROUP_RULES = {"max": 0, "top2": 1}
 ACTS = {"none": 0, "relu": 1, "gelu": 2, "silu": 3}
+LRM_MOMENTS_F32, LRM_MOMENTS_8BIT = 0, 1
+MOMENTS = {"m": 0, "v": 1}
 
 
 class LrmError(RuntimeError):
@@ -107,6 +109,28 @@ class lrm_pair_grad_outputs(C.Structure):
     _fields_ = [(n, C.c_void_p) for n in ("dweight", "G", "dbias")]
 
 
+class lrm_balance(C.Structure):
+    _fields_ = [("router", lrm_router), ("expert", C.c_void_p), ("counts", C.c_void_p),
+                ("seq", C.c_void_p), ("S", C.c_int32), ("coef", C.c_float), ("z_coef", C.c_float),
+                ("_pad", C.c_int32)]
+
+
+class lrm_param(C.Structure):
+    _fields_ = [(n, C.c_void_p) for n in ("p", "g", "master", "m", "v", "m_exp", "v_exp")] + \
+        [("n", C.c_int64), ("lr", C.c_float), ("weight_decay", C.c_float)]
+
+
+class lrm_params(C.Structure):
+    _fields_ = [(n, C.c_int32) for n in ("n", "p_dtype", "g_dtype", "moments", "masters", "_pad")] + \
+        [("param", C.POINTER(lrm_param)), ("table", C.c_void_p), ("chunks", C.c_int64)]
+
+
+class lrm_adamw_step(C.Structure):
+    _fields_ = [(n, C.c_double) for n in ("lr", "beta1", "beta2", "eps", "grad_scale", "max_norm")] + \
+        [("step", C.c_int64), ("seed", C.c_uint64), ("sumsq", C.c_void_p), ("n_sumsq", C.c_int32),
+         ("_pad", C.c_int32), ("lr_dev", C.c_void_p), ("steps", C.c_void_p)]
+
+
 _P = C.c_void_p
 _SZ = C.c_size_t
 _I32 = C.c_int32
@@ -157,6 +181,15 @@ _sigs = {
     "lrm_pair_grad": (C.c_int, [C.POINTER(lrm_pair_grad_problem),
                                 C.POINTER(lrm_pair_grad_outputs), _P, _SZ, _P]),
     "lrm_pair_grad_workspace_size": (_SZ, [C.POINTER(lrm_pair_grad_problem)]),
+    "lrm_balance_loss": (C.c_int, [C.POINTER(lrm_balance), _P, _P, _P, _P, _SZ, _P]),
+    "lrm_balance_workspace_size": (_SZ, [C.POINTER(lrm_balance)]),
+    "lrm_balance_bwd": (C.c_int, [C.POINTER(lrm_balance), _P, _P, _P, _P, C.c_int64, _P]),
+    "lrm_params_table": (C.c_int, [C.POINTER(lrm_params), _SZ, _P]),
+    "lrm_params_table_size": (_SZ, [_I32]),
+    "lrm_grad_sumsq": (C.c_int, [C.POINTER(lrm_params), _P, _P, _SZ, _P]),
+    "lrm_sumsq_workspace_size": (_SZ, [C.POINTER(lrm_params)]),
+    "lrm_adamw": (C.c_int, [C.POINTER(lrm_params), C.POINTER(lrm_adamw_step), _P]),
+    "lrm_moment_read": (C.c_int, [C.c_int64, _I32, _P, _P, _I32, _P, _P]),
 }
 for _name, (_res, _args) in _sigs.items():
     _f = getattr(_lib, _name)
@@ -563,6 +596,65 @@ def lrm_route_share(T: int, k: int, expert, weight, e0: int, E: int, out_token, 
                                 _stream(stream, out_n.device)), "lrm_route_share")
 
 
+# ----------------------------------------------- balance of the experts' load
+class Balance:
+    """An lrm_balance over a Router plus the tensors that keep its memory alive.
+    expert: int32 [T*k], the choice; counts: int32 [S][E] slots per expert (of
+    lrm_route, or summed over GPUs), None: from the choice; seq: int32 [S+1],
+    the sequences' offsets, None: one sequence of all tokens."""
+
+    def __init__(self, router: Router, expert=None, counts=None, seq=None, coef: float = 0.01,
+                 z_coef: float = 0.0):
+        on = router.device
+        _slots("expert", expert, router.T * router.k, torch.int32, on)
+        if seq is not None:
+            if seq.dim() != 1 or seq.numel() < 2:
+                raise ValueError("seq must hold the offsets of one sequence at least")
+            _slots("seq", seq, 2, torch.int32, on)
+        self.S = 1 if seq is None else int(seq.numel()) - 1
+        _slots("counts", counts, self.S * router.E, torch.int32, on)
+        self.router = router
+        self.keep = [router, expert, counts, seq]
+        self.has_expert, self.has_counts = expert is not None, counts is not None
+        self.c = lrm_balance(router.c, _ptr(expert), _ptr(counts), _ptr(seq), self.S, float(coef),
+                             float(z_coef), 0)
+
+
+def lrm_balance_workspace_size(b: Balance) -> int:
+    return int(_lib.lrm_balance_workspace_size(C.byref(b.c)))
+
+
+def lrm_balance_loss(b: Balance, loss, saved, counts=None, ws=None, stream=None):
+    """The balance loss and the z loss (fp32 loss[2]), what their gradient needs
+    (fp32 saved[S*E + 2]) and, where b has none, the counts (int32 [S][E])."""
+    on = b.router.device
+    _slots("loss", loss, 2, torch.float32, on)
+    _slots("saved", saved, b.S * b.router.E + 2, torch.float32, on)
+    _slots("counts", counts, b.S * b.router.E, torch.int32, on)
+    if ws is None:
+        ws = _grown(lrm_balance_workspace_size(b), on, stream)
+    _check(_lib.lrm_balance_loss(C.byref(b.c), _ptr(loss), _ptr(saved), _ptr(counts), _ptr(ws),
+                                 ws.numel() if ws is not None else 0, _stream(stream, on)),
+           "lrm_balance_loss")
+
+
+def lrm_balance_bwd(b: Balance, saved, dlogits: torch.Tensor, dloss=None, dweight=None, stream=None):
+    """Gradient of the logits (their dtype, [T][E]): of both losses, from their
+    gradients (fp32 dloss[2], None: ones), and with dweight (fp32 [T*k]) of the
+    routing weights too, in place of lrm_route_bwd."""
+    r = b.router
+    _slots("saved", saved, b.S * r.E + 2, torch.float32, r.device)
+    _slots("dloss", dloss, 2, torch.float32, r.device)
+    _slots("dweight", dweight, r.T * r.k, torch.float32, r.device)
+    if dlogits.shape != (r.T, r.E) or (r.E > 1 and dlogits.stride(1) != 1) or \
+            dtype_code(dlogits) != r.c.dtype or dlogits.device != r.device:
+        raise ValueError("dlogits must be [T][E] of the logits' dtype with unit column stride "
+                         "on the logits' device")
+    ldd = dlogits.stride(0) if r.T > 1 else max(dlogits.stride(0), r.E)
+    _check(_lib.lrm_balance_bwd(C.byref(b.c), _ptr(saved), _ptr(dloss), _ptr(dweight), _ptr(dlogits),
+                                ldd, _stream(stream, r.device)), "lrm_balance_bwd")
+
+
 # ------------------------------------------------------ the experts forward
 class Forward:
     """An lrm_forward plus the objects that keep its memory alive."""
@@ -727,3 +819,137 @@ def lrm_pair_grad(g: PairGrad, outputs, ws=None, stream=None):
                               _stream(stream, g.pairs.token.device)),
            "lrm_pair_grad")
     return ws
+
+
+# ---------------------------------------------- update of the parameters
+def _bytes(t):
+    return t.data_ptr(), t.data_ptr() + t.numel() * t.element_size()
+
+
+class Params:
+    """Tensors that are updated together: an lrm_params, its table on the GPU
+    (written on the given or the current stream) and the tensors themselves.
+
+    g: their gradients (fp32 or bf16, all alike); p: the weights (fp32 or bf16);
+    m, v: the moments, fp32, or uint8 codes with the blocks' exponents m_exp and
+    v_exp (uint8 [(n + 31) // 32] each); master: fp32 weights behind bf16 p; lr,
+    weight_decay: a number for all, or one each.  All lists have one entry a
+    tensor; entries are contiguous.  With g alone: for lrm_grad_sumsq."""
+
+    def __init__(self, g, p=None, m=None, v=None, master=None, m_exp=None, v_exp=None, lr=1.0,
+                 weight_decay=0.0, stream=None):
+        g = list(g)
+        n = len(g)
+        lists = {"p": p, "master": master, "m": m, "v": v, "m_exp": m_exp, "v_exp": v_exp}
+        lists = {k: list(x) for k, x in lists.items() if x is not None}
+        if not g:
+            raise ValueError("at least one tensor is wanted")
+        self.device = g[0].device
+        eight = "m_exp" in lists
+        want = {"g": g[0].dtype, "p": lists["p"][0].dtype if lists.get("p") else None,
+                "master": torch.float32, "m": torch.uint8 if eight else torch.float32,
+                "v": torch.uint8 if eight else torch.float32, "m_exp": torch.uint8,
+                "v_exp": torch.uint8}
+        written = []
+        for name, ts in [("g", g), *lists.items()]:
+            if len(ts) != n:
+                raise ValueError(f"{name} must have {n} tensors, as g has")
+            for i, t in enumerate(ts):
+                size = g[i].numel()
+                size = (size + 31) // 32 if name.endswith("_exp") else size
+                if t.dtype != want[name] or t.numel() != size or not t.is_contiguous() or \
+                        t.device != self.device:
+                    raise ValueError(f"{name}[{i}] must be a contiguous {want[name]} tensor of "
+                                     f"{size} elements on {self.device}")
+                if size:
+                    written.append((*_bytes(t), name != "g", f"{name}[{i}]"))
+        # (what is written lies apart from everything; gradients may share memory)
+        written.sort()
+        end, last, end_w, last_w = -1, "", -1, ""
+        for lo, hi, w, name in written:
+            if lo < (end if w else end_w):
+                raise ValueError(f"{name} shares memory with {last if w else last_w}")
+            if hi > end:
+                end, last = hi, name
+            if w and hi > end_w:
+                end_w, last_w = hi, name
+
+        def each(x, name):
+            x = [float(y) for y in x] if isinstance(x, (list, tuple)) else [float(x)] * n
+            if len(x) != n:
+                raise ValueError(f"{name} must be a number or {n} of them")
+            return x
+
+        lr, weight_decay = each(lr, "lr"), each(weight_decay, "weight_decay")
+        self.param = (lrm_param * n)()
+        for i, q in enumerate(self.param):
+            q.g, q.n, q.lr, q.weight_decay = _ptr(g[i]), g[i].numel(), lr[i], weight_decay[i]
+            for name, ts in lists.items():
+                setattr(q, name, _ptr(ts[i]))
+        self.n = n
+        self.keep = [g, lists]
+        self.table = _scratch(int(_lib.lrm_params_table_size(n)), self.device, stream)
+        self.c = lrm_params(n, dtype_code(lists["p"][0]) if lists.get("p") else LRM_F32,
+                            dtype_code(g[0]), LRM_MOMENTS_8BIT if eight else LRM_MOMENTS_F32,
+                            int("master" in lists), 0, self.param, _ptr(self.table), 0)
+        _check(_lib.lrm_params_table(C.byref(self.c), self.table.numel(),
+                                     _stream(stream, self.device)), "lrm_params_table")
+
+
+def lrm_sumsq_workspace_size(ps: Params) -> int:
+    return int(_lib.lrm_sumsq_workspace_size(C.byref(ps.c)))
+
+
+def lrm_grad_sumsq(ps: Params, sumsq, ws=None, stream=None):
+    """The sum of squares of all gradients (fp64 sumsq[0])."""
+    _slots("sumsq", sumsq, 1, torch.float64, ps.device)
+    if ws is None:
+        ws = _grown(lrm_sumsq_workspace_size(ps), ps.device, stream)
+    _check(_lib.lrm_grad_sumsq(C.byref(ps.c), _ptr(sumsq), _ptr(ws),
+                               ws.numel() if ws is not None else 0, _stream(stream, ps.device)),
+           "lrm_grad_sumsq")
+
+
+class AdamW:
+    """An lrm_adamw_step: the settings of lrm_adamw, and the device tensors that
+    it reads.  lr: a number, or an fp32 tensor of one entry on the GPU (read when
+    the step runs); sumsq: fp64, sums of squares of the gradients (all entries are
+    added): for clipping to max_norm (0: none), and a step whose sum is not
+    finite is left out; steps: int64 tensor of one entry, counted by the calls."""
+
+    def __init__(self, lr=1e-3, beta1: float = 0.9, beta2: float = 0.999, eps: float = 1e-8,
+                 seed: int = 0, grad_scale: float = 1.0, max_norm: float = 0.0, sumsq=None,
+                 steps=None):
+        lr_dev = lr if isinstance(lr, torch.Tensor) else None
+        for name, t, dt in (("lr", lr_dev, torch.float32), ("steps", steps, torch.int64)):
+            if t is not None and (t.dtype != dt or t.numel() != 1):
+                raise ValueError(f"{name} must be one {dt} value")
+        if sumsq is not None and (sumsq.dtype != torch.float64 or not sumsq.is_contiguous()):
+            raise ValueError("sumsq must be a contiguous torch.float64 tensor")
+        self.keep = [t for t in (lr_dev, sumsq, steps) if t is not None]
+        self.c = lrm_adamw_step(0.0 if lr_dev is not None else float(lr), float(beta1), float(beta2),
+                                float(eps), float(grad_scale), float(max_norm), 0,
+                                int(seed) & 0xFFFFFFFFFFFFFFFF, _ptr(sumsq),
+                                0 if sumsq is None else sumsq.numel(), 0, _ptr(lr_dev), _ptr(steps))
+
+
+def lrm_adamw(ps: Params, opt: AdamW, step: int = 0, stream=None):
+    """One AdamW step over all tensors; step: its number, from 1 (not read where
+    opt counts the steps on the GPU)."""
+    for t in opt.keep:
+        if t.device != ps.device:
+            raise ValueError(f"the step's tensors must be on {ps.device}")
+    opt.c.step = int(step)
+    _check(_lib.lrm_adamw(C.byref(ps.c), C.byref(opt.c), _stream(stream, ps.device)), "lrm_adamw")
+
+
+def lrm_moment_read(codes, exps, out, which: str, stream=None):
+    """The values that 8-bit moments (uint8 codes [n], exponents [(n + 31) // 32])
+    stand for; which: "m" or "v"; out: fp32 or bf16 [n]."""
+    n = out.numel()
+    _slots("codes", codes, n, torch.uint8, out.device)
+    _slots("exps", exps, (n + 31) // 32, torch.uint8, out.device)
+    if not out.is_contiguous():
+        raise ValueError("out must be contiguous")
+    _check(_lib.lrm_moment_read(n, MOMENTS[which], _ptr(codes), _ptr(exps), dtype_code(out), _ptr(out),
+                                _stream(stream, out.device)), "lrm_moment_read")

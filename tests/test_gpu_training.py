@@ -1,0 +1,498 @@
+"""GPU parity of the balance losses, their gradient and the update of the
+parameters against the fp64 oracle, through the Python binding of the C ABI; and
+the calls together, as a training step makes them."""
+
+import math
+
+import numpy as np
+import pytest
+import torch
+
+import training_cases as TC
+from oracle import training as OT
+from test_gpu_forward import L, dev, filled  # noqa: F401
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda"
+
+
+# ---------------------------------------------------------------- balance
+def make_balance(L, c):  # noqa: F811
+    T, E, ld = c["T"], c["E"], c["ld"] or c["E"]
+    store = torch.zeros(T, ld, dtype=c["logits"].dtype, device=DEV)
+    store[:, :E] = dev(c["logits"])
+    r = L.Router(store[:, :E], c["k"], score=c["score"], renorm=c["renorm"],
+                 expert_mask=dev(c["expert_mask"]), token_mask=dev(c["token_mask"]))
+    seq = None if c["seq"] is None else torch.tensor(c["seq"], dtype=torch.int32, device=DEV)
+    return L.Balance(r, expert=dev(c["expert"]), counts=dev(c["counts_in"]), seq=seq, coef=c["coef"],
+                     z_coef=c["z_coef"])
+
+
+def run_balance(L, c, b, stream=None):  # noqa: F811
+    loss, saved = filled((2,), torch.float32), filled((b.S * c["E"] + 2,), torch.float32)
+    counts = filled((b.S, c["E"]), torch.int32) if c["counts_in"] is None else None
+    if stream is not None:
+        stream.wait_stream(torch.cuda.current_stream())
+    L.lrm_balance_loss(b, loss, saved, counts=counts, stream=stream)
+    return loss, saved, counts
+
+
+@pytest.mark.parametrize("name", sorted(TC.BALANCE))
+def test_balance(L, name):  # noqa: F811
+    c = TC.balance_case(name)
+    b = make_balance(L, c)
+    loss, saved, counts = run_balance(L, c, b)
+    torch.cuda.synchronize()
+    TC.check_balance(c, loss.cpu(), saved.cpu(), None if counts is None else counts.cpu())
+    side = torch.cuda.Stream()
+    again = run_balance(L, c, b, side)
+    side.synchronize()
+    assert torch.equal(again[0], loss) and torch.equal(again[1], saved)
+    T, E = c["T"], c["E"]
+    for gap, dweight, dloss in ((3, True, True), (0, False, False), (0, True, False)):
+        store = filled((T, E + gap), c["logits"].dtype)
+        L.lrm_balance_bwd(b, saved, store[:, :E], dloss=dev(c["dloss"]) if dloss else None,
+                          dweight=dev(c["dweight"]) if dweight else None)
+        torch.cuda.synchronize()
+        TC.check_balance_bwd(c, store[:, :E].cpu(), dweight, dloss)
+        assert (store[:, E:].contiguous().view(torch.uint8) == 0xCD).all()
+
+
+TC.BALANCE_LARGE = {
+    "many": dict(T=4001, E=32, k=4),
+    "many_bf16": dict(T=3000, E=48, k=3, dtype="bf16", renorm=False, padded=0.1),
+    "many_seqs": dict(T=2500, E=40, k=2, score="sigmoid", seq=[0, 0, 1, 700, 701, 1500, 1500, 2400]),
+    "short_seqs": dict(T=900, E=16, k=2, seq=list(range(0, 901, 3))),
+}
+
+
+@pytest.mark.parametrize("name", sorted(TC.BALANCE_LARGE))
+def test_balance_many_tokens(L, name):  # noqa: F811
+    c = TC.balance_case(name, **TC.BALANCE_LARGE[name])
+    b = make_balance(L, c)
+    loss, saved, counts = run_balance(L, c, b)
+    out = filled((c["T"], c["E"]), c["logits"].dtype)
+    L.lrm_balance_bwd(b, saved, out, dloss=dev(c["dloss"]), dweight=dev(c["dweight"]))
+    torch.cuda.synchronize()
+    TC.check_balance(c, loss.cpu(), saved.cpu(), counts.cpu())
+    TC.check_balance_bwd(c, out.cpu())
+
+
+def test_balance_without_tokens(L):  # noqa: F811
+    r = L.Router(torch.empty(0, 8, device=DEV), 2)
+    b = L.Balance(r, expert=torch.empty(0, dtype=torch.int32, device=DEV), coef=0.5, z_coef=0.25)
+    loss, saved, counts = filled((2,), torch.float32), filled((10,), torch.float32), filled((8,), torch.int32)
+    L.lrm_balance_loss(b, loss, saved, counts=counts)
+    L.lrm_balance_bwd(b, saved, torch.empty(0, 8, device=DEV))
+    assert loss.tolist() == [0.0, 0.0] and counts.tolist() == [0] * 8
+    assert saved.tolist() == [0.0] * 8 + [0.5, 0.5]
+
+
+def test_balance_counts_of_the_router(L):  # noqa: F811
+    """The router's counts and the choice give the same bits."""
+    T, E, k = 3000, 64, 4
+    z = dev(TC.normal(TC.gen("router counts"), T, E))
+    r = L.Router(z, k)
+    e, w, counts = (filled((T * k,), torch.int32), filled((T * k,), torch.float32),
+                    filled((E,), torch.int32))
+    L.lrm_route(r, e, w, counts=counts)
+    got = []
+    for b in (L.Balance(r, expert=e), L.Balance(r, counts=counts)):
+        loss, saved = filled((2,), torch.float32), filled((E + 2,), torch.float32)
+        L.lrm_balance_loss(b, loss, saved)
+        got.append(torch.cat([loss, saved]))
+    assert torch.equal(*got)
+
+
+def test_balance_offsets_that_make_no_sense_stay_in_bounds(L):  # noqa: F811
+    """Decreasing and outlying offsets: results are undefined, memory is not."""
+    T, E = 200, 16
+    z = dev(TC.normal(TC.gen("bad seq"), T, E))
+    r = L.Router(z, 2)
+    e = torch.zeros(T * 2, dtype=torch.int32, device=DEV)
+    for seq in ([50, 20, 300, -7, 100], [-5, 2 ** 31 - 1, -2 ** 31, 90], [1000, 2000]):
+        b = L.Balance(r, expert=e, seq=torch.tensor(seq, dtype=torch.int32, device=DEV))
+        n = b.S * E + 2
+        saved, counts, loss = filled((n + 64,), torch.float32), filled((b.S * E + 64,), torch.int32), \
+            filled((66,), torch.float32)
+        ws = filled((L.lrm_balance_workspace_size(b) + 256,), torch.uint8)
+        out = filled((T + 4, E), torch.float32)
+        L.lrm_balance_loss(b, loss[:2], saved[:n], counts=counts[:b.S * E], ws=ws[:-256])
+        L.lrm_balance_bwd(b, torch.zeros(n, device=DEV), out[:T])
+        torch.cuda.synchronize()
+        for t in (saved[n:], counts[b.S * E:], loss[2:], ws[-256:], out[T:]):
+            assert (t.contiguous().view(torch.uint8) == 0xCD).all()
+
+
+# ------------------------------------------------------------- parameters
+GAP = 64  # bytes of 0xCD on both sides of every array
+
+
+def placed(t, skip):
+    """t on the GPU, `skip` elements behind a 64-byte boundary, 0xCD around it."""
+    if t is None:
+        return None, None
+    es = t.element_size()
+    raw = torch.full((GAP + skip * es + t.numel() * es + GAP,), 0xCD, dtype=torch.uint8, device=DEV)
+    at = GAP + skip * es
+    x = raw[at:at + t.numel() * es].view(t.dtype)
+    x.copy_(t)
+    return x, raw
+
+
+def on_gpu(L, c, **kw):  # noqa: F811
+    keys = ("g", "p", "master", "m", "v", "m_exp", "v_exp")
+    both = [{k: placed(q[k], c["offset"]) for k in keys} for q in c["t"]]
+    lists = {k: [b[k][0] for b in both] for k in keys if c["t"][0][k] is not None}
+    ps = L.Params(**lists, lr=c["lrs"], weight_decay=c["decays"], **kw)
+    return ps, lists, [b[k][1] for b in both for k in keys if b[k][1] is not None]
+
+
+def back(c, lists):
+    return [{k: lists[k][i].cpu() if k in lists else None
+             for k in ("p", "master", "m", "v", "m_exp", "v_exp")} for i in range(len(c["t"]))]
+
+
+def options(L, c, **kw):  # noqa: F811
+    o = dict(lr=c["lr"], beta1=c["beta1"], beta2=c["beta2"], eps=c["eps"], seed=c["seed"],
+             grad_scale=c["scale"], max_norm=c["max_norm"])
+    return L.AdamW(**dict(o, **kw))
+
+
+@pytest.mark.parametrize("name", sorted(TC.PARAMS))
+def test_adamw(L, name):  # noqa: F811
+    c = TC.param_case(name)
+    ps, lists, raws = on_gpu(L, c)
+    sumsq = filled((1,), torch.float64)
+    L.lrm_grad_sumsq(ps, sumsq)
+    L.lrm_adamw(ps, options(L, c, sumsq=sumsq if c["clip"] else None), c["step"])
+    torch.cuda.synchronize()
+    assert abs(float(sumsq) - c["sumsq"]) <= 1e-13 * c["sumsq"]
+    TC.check_adamw(c, back(c, lists))
+    for raw in raws:  # nothing around an array has changed
+        assert (raw[:GAP] == 0xCD).all() and (raw[-GAP:] == 0xCD).all()
+
+
+@pytest.mark.parametrize("name", ["eight_bf16", "odd_f32"])
+def test_adamw_rate_and_step_on_the_gpu(L, name):  # noqa: F811
+    c = TC.param_case(name)
+    c["lr"] = float(np.float32(c["lr"]))
+    ps, lists, _ = on_gpu(L, c)
+    parts = torch.tensor([c["sumsq"] / 2, c["sumsq"] / 4, c["sumsq"] / 4], dtype=torch.float64, device=DEV)
+    steps = torch.tensor([c["step"] - 1], device=DEV)
+    opt = options(L, c, lr=torch.tensor([c["lr"]], device=DEV), sumsq=parts, steps=steps)
+    L.lrm_adamw(ps, opt)
+    torch.cuda.synchronize()
+    assert int(steps) == c["step"]
+    TC.check_adamw(c, back(c, lists))
+
+
+@pytest.mark.parametrize("bad", [float("inf"), float("nan")])
+def test_a_gradient_that_is_not_finite_changes_nothing(L, bad):  # noqa: F811
+    for name in ("eight_bf16", "master"):
+        c = TC.param_case(name)
+        ps, lists, _ = on_gpu(L, c)
+        lists["g"][0][5] = bad
+        before = {k: [t.clone() for t in ts] for k, ts in lists.items()}
+        sumsq, steps = filled((1,), torch.float64), torch.tensor([4], device=DEV)
+        L.lrm_grad_sumsq(ps, sumsq)
+        L.lrm_adamw(ps, options(L, c, sumsq=sumsq, steps=steps))
+        torch.cuda.synchronize()
+        assert not math.isfinite(float(sumsq)) and int(steps) == 4
+        for k, ts in lists.items():
+            for x, y in zip(ts, before[k]):
+                assert torch.equal(x.view(torch.uint8), y.view(torch.uint8)), k
+
+
+def test_huge_gradients_do_not_overflow_the_norm(L):  # noqa: F811
+    g = [torch.full((5000,), 1e30, device=DEV), torch.full((3,), -3e38, device=DEV)]
+    ps = L.Params(g=g)
+    sumsq = filled((1,), torch.float64)
+    L.lrm_grad_sumsq(ps, sumsq)
+    want = float((g[0].double() ** 2).sum() + (g[1].double() ** 2).sum())
+    assert abs(float(sumsq) - want) <= 1e-13 * want
+
+
+@pytest.mark.parametrize("bits", [32, 8])
+def test_many_tensors(L, bits):  # noqa: F811
+    """More tensors than one launch of the table takes, and more chunks than blocks."""
+    rng = np.random.default_rng(3)
+    sizes = [int(v) for v in rng.integers(0, 3000, 200)] + [2048 * 2200 + 13]
+    g = TC.gen("many tensors")
+    total = sum(sizes)
+    flat = {k: dev(TC.normal(g, total, std=0.02)) for k in ("p", "g")}
+    step, lr = 3, 1e-2
+    lists = {k: [x.clone() for x in flat[k].split(sizes)] for k in flat}
+    if bits == 8:
+        for k in "mv":
+            lists[k] = [torch.zeros(n, dtype=torch.uint8, device=DEV) for n in sizes]
+            lists[k + "_exp"] = [torch.zeros((n + 31) // 32, dtype=torch.uint8, device=DEV) for n in sizes]
+    else:
+        for k in "mv":
+            lists[k] = [torch.zeros(n, device=DEV) for n in sizes]
+    ps = L.Params(**lists)
+    sumsq = filled((1,), torch.float64)
+    L.lrm_grad_sumsq(ps, sumsq)
+    L.lrm_adamw(ps, L.AdamW(lr=lr), step)
+    G = flat["g"].double()
+    assert abs(float(sumsq) - float((G * G).sum())) <= 1e-12 * float(sumsq)
+    m, v = 0.1 * G, 0.001 * G * G
+    want = flat["p"].double() - lr * (m / (1 - 0.9 ** step)) / ((v / (1 - 0.999 ** step)).sqrt() + 1e-8)
+    got = torch.cat(lists["p"]).double()
+    # |update| is below 2 lr here: 12 u of it, half a step of the weight twice
+    assert ((got - want).abs() <= 24 * TC.U * lr + 3 * TC.U * want.abs() + 1e-12).all()
+    if bits == 8:  # each within a step of a mantissa of 3 bits, where its block holds it
+        for k, x, octaves, second in (("m", m, 15, 0), ("v", v, 31, 1)):
+            for i in (0, 57, len(sizes) - 1):
+                n = sizes[i]
+                if n == 0:
+                    continue
+                out = filled((n,), torch.float32)
+                L.lrm_moment_read(lists[k][i], lists[k + "_exp"][i], out, k)
+                ref = x.split(sizes)[i]
+                top = torch.nn.functional.pad(ref.abs(), (0, -n % 32)).view(-1, 32).amax(1)
+                top = top.repeat_interleave(32)[:n]
+                assert ((out - ref).abs() <= ref.abs() / 8 + top * 2.0 ** (1 - octaves)).all()
+
+
+def test_tensors_past_2_gib(L):  # noqa: F811
+    """Offsets past 2^31 elements: the last ones move as in a short tensor at the
+    same place of the list."""
+    n, tail = 2 ** 31 + 4096 + 37, 4096 + 37  # (the tail starts on a block of 32)
+    if torch.cuda.mem_get_info()[0] < 40 << 30:
+        pytest.skip("needs 40 GB of GPU memory")
+    gen = TC.gen("past")
+    w, g = (dev(TC.normal(gen, tail, std=0.02, dtype=torch.bfloat16)) for _ in range(2))
+
+    def state(size):
+        t = dict(p=torch.zeros(size, dtype=torch.bfloat16, device=DEV),
+                 g=torch.zeros(size, dtype=torch.bfloat16, device=DEV))
+        for k in "mv":
+            t[k] = torch.zeros(size, dtype=torch.uint8, device=DEV)
+            t[k + "_exp"] = torch.zeros((size + 31) // 32, dtype=torch.uint8, device=DEV)
+        t["p"][-tail:], t["g"][-tail:] = w, g
+        return t
+
+    t = state(n)
+    ps = L.Params(**{k: [x] for k, x in t.items()})
+    sumsq = filled((1,), torch.float64)
+    L.lrm_grad_sumsq(ps, sumsq)
+    assert abs(float(sumsq) - float((g.double() ** 2).sum())) <= 1e-13 * float(sumsq)
+    L.lrm_adamw(ps, L.AdamW(lr=1e-2, seed=5), 2)
+    bits = [OT.random_bits(5, 2, n - tail + j) for j in range(0, tail, 97)]
+    G = g.double().cpu().numpy()
+    for i, j in enumerate(range(0, tail, 97)):
+        x, _, _ = OT.adamw(float(w[j]), G[j], 0.0, 0.0, 2, 1e-2)
+        ref, far = OT.round_bf16(float(x), bits[i][2])
+        assert float(t["p"][n - tail + j]) == ref or far < 1e-3
+    assert int(t["m"][:n - tail].count_nonzero()) == 0 and int(t["v"][:n - tail].count_nonzero()) == 0
+    out = torch.empty(n, dtype=torch.bfloat16, device=DEV)
+    L.lrm_moment_read(t["m"], t["m_exp"], out, "m")
+    ref = 0.1 * g.double()
+    assert ((out[-tail:].double() - ref).abs() <= ref.abs() / 8 + 1e-5).all()
+    assert int(out[:n - tail].count_nonzero()) == 0
+
+
+def test_small_steps_count_on_average(L):  # noqa: F811
+    """Steps far below half a rounding: bf16 weights without a master and 8-bit
+    second moments move on average as they would in fp32."""
+    n, steps, lr = 1 << 16, 64, 2.0 ** -14
+    p = torch.full((n,), 1.0, dtype=torch.bfloat16, device=DEV)  # a step of p: 2^-7 above 1, 2^-8 below
+    g = torch.full((n,), 0.5, device=DEV)
+    zeros = lambda k: torch.zeros(k, dtype=torch.uint8, device=DEV)  # noqa: E731
+    m, v, me, ve = zeros(n), zeros(n), zeros(n // 32), zeros(n // 32)
+    # v starts at 1 and goes to 0.25 by 0.1 % a step
+    v.fill_(31 * 8)
+    ve.fill_(127)
+    ps = L.Params(g=[g], p=[p], m=[m], v=[v], m_exp=[me], v_exp=[ve])
+    count = torch.zeros(1, dtype=torch.int64, device=DEV)
+    opt = L.AdamW(lr=lr, seed=11, steps=count)
+    W, M, V = 1.0, 0.0, 1.0
+    for s in range(1, steps + 1):
+        L.lrm_adamw(ps, opt)
+        W, M, V = (float(x) for x in OT.adamw(np.float64(W), 0.5, M, V, s, lr))
+    out = torch.empty(n, device=DEV)
+    L.lrm_moment_read(v, ve, out, "v")
+    # v: one rounding a step, of a step of V/8 at most, with a probability of at
+    # most 2 (0.1 %) 8; the mean of n elements is off by less than 6 deviations
+    dev_v = math.sqrt(steps * 0.016) * V / 8
+    assert abs(float(out.double().mean()) - V) <= 6 * dev_v / math.sqrt(n) + 1e-3 * V
+    # the weights' mean: steps of 2^-8; the update follows sqrt(v), whose scatter
+    # (below 13 % of v) bends it by less than 2 %
+    moved = 1.0 - float(p.double().mean())
+    dev_p = math.sqrt(steps * (1 - W) / steps * 256) * 2.0 ** -8
+    assert abs(moved - (1.0 - W)) <= 6 * dev_p / math.sqrt(n) + 0.02 * (1.0 - W)
+
+
+@pytest.mark.parametrize("second", ["m", "v"])
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("skip", [0, 3])
+def test_moment_read(L, second, dtype, skip):  # noqa: F811
+    n = 70_001
+    codes = (torch.arange(n + skip) * 7 % 256).to(torch.uint8)[skip:]
+    exps = (torch.arange((n + 31) // 32) * 37 % 200 + 40).to(torch.uint8)
+    codes_d, _ = placed(codes, skip)
+    out = filled((n + 32,), TC.DT[dtype])
+    L.lrm_moment_read(codes_d, dev(exps), out[:n], second)
+    ref = torch.as_tensor(TC.values(codes.numpy(), exps.numpy(), second == "v"))
+    assert torch.equal(out[:n].cpu().double(), ref)
+    assert (out[n:].view(torch.uint8) == 0xCD).all()
+
+
+# --------------------------------------------------------------- together
+def layer(seed, T=96, h=32, d=40, E=6, k=2):
+    g = TC.gen("layer", seed)
+    return dict(T=T, h=h, d=d, E=E, k=k, X=TC.normal(g, T, h), Wr=TC.normal(g, E, h, std=0.3),
+                W=TC.normal(g, E, d, h, std=h ** -0.5), target=TC.normal(g, T, d),
+                token_mask=(torch.rand(T, generator=g) < 0.9).to(torch.uint8))
+
+
+def torch_loss(c, Wr, W, e):
+    """The loss of a choice, by definition (automatic differentiation gives the gradients)."""
+    T, E, k = c["T"], c["E"], c["k"]
+    on = c["token_mask"].bool()
+    z = c["X"].to(Wr.dtype) @ Wr.T
+    p = torch.softmax(z, 1)
+    e = e.view(T, k).long().clamp_min(0)
+    w = torch.softmax(z.gather(1, e), 1) * on[:, None]
+    y = torch.stack([(W[e[:, j]] @ c["X"].to(Wr.dtype)[:, :, None])[:, :, 0] for j in range(k)], 1)
+    Y = (w[:, :, None] * y).sum(1)
+    main = 0.5 * ((Y - c["target"].to(Wr.dtype)) ** 2 * on[:, None]).sum() / T
+    f = torch.bincount(e[on].reshape(-1), minlength=E).to(Wr.dtype)
+    bal = 0.02 * E * ((f / f.sum()) * p[on].mean(0)).sum()
+    zl = 0.002 * torch.logsumexp(z, 1)[on].square().mean()
+    return main, bal, zl
+
+
+def test_training_step_together(L):  # noqa: F811
+    """Logits to updated weights: route, balance, forward, the backward calls, the
+    norm and AdamW, against automatic differentiation in fp64."""
+    c = layer(1)
+    T, h, d, E, k = (c[x] for x in ("T", "h", "d", "E", "k"))
+    X, Wr, W, target, on = (dev(c[x]) for x in ("X", "Wr", "W", "target", "token_mask"))
+    Wr0, W0 = c["Wr"].double(), c["W"].double()
+    z = X @ Wr.T
+    r = L.Router(z, k, token_mask=on)
+    n = T * k
+    e, w, tok = (filled((n,), torch.int32), filled((n,), torch.float32), filled((n,), torch.int32))
+    L.lrm_route(r, e, w, token=tok)
+    ec = e.cpu()
+    b = L.Balance(r, expert=e, coef=0.02, z_coef=0.002)
+    loss, saved = filled((2,), torch.float32), filled((E + 2,), torch.float32)
+    L.lrm_balance_loss(b, loss, saved)
+    pairs = L.Pairs(tok, e, w, T, E)
+    f = L.linear_forward(pairs, X, "token", W)
+    Y, Yp = filled((T, d), torch.float32), torch.zeros(n, d, device=DEV)
+    L.lrm_expert_forward(f, dict(Y=Y, Yp=Yp))
+    dY = (Y - target) * on[:, None] / T
+    dw = filled((n,), torch.float32)
+    L.lrm_pair_grad(L.pair_grad_problem(pairs, dY, "token", Yp), dict(dweight=dw))
+    dz, dW = filled((T, E), torch.float32), filled((E, d, h), torch.float32)
+    L.lrm_balance_bwd(b, saved, dz, dweight=dw)
+    L.lrm_expert_backward(L.linear_problem(pairs, X, "token", dY, "token", W, None, flags=L.LRM_KEEP_ALL),
+                          dict(dW=dW, dX=filled((T, h), torch.float32)))
+    dWr = dz.T.contiguous() @ X
+    m = [torch.zeros_like(Wr), torch.zeros_like(W)]
+    v = [torch.zeros_like(Wr), torch.zeros_like(W)]
+    ps = L.Params(g=[dWr, dW], p=[Wr, W], m=m, v=v, weight_decay=[0.0, 0.1])
+    sumsq = filled((1,), torch.float64)
+    opt = L.AdamW(lr=1e-2, sumsq=sumsq, max_norm=0.1)
+    L.lrm_grad_sumsq(ps, sumsq)
+    L.lrm_adamw(ps, opt, 1)
+    torch.cuda.synchronize()
+    a, q = Wr0.clone().requires_grad_(True), W0.clone().requires_grad_(True)
+    main, bal, zl = torch_loss(c, a, q, ec)
+    ga, gq = torch.autograd.grad(main + bal + zl, (a, q))
+    for name, got, ref in (("balance", loss[0], bal), ("z", loss[1], zl)):
+        assert abs(got.item() - ref.item()) <= 2e-5 * abs(ref.item()), name
+    # products and sums in fp32 over h, d, T terms: n u of the sums of their sizes
+    for name, got, ref in (("dWr", dWr, ga), ("dW", dW, gq)):
+        err = (got.double().cpu() - ref).abs().max()
+        assert float(err) <= 1e-5 * float(ref.abs().max()), name
+    norm2 = float((ga ** 2).sum() + (gq ** 2).sum())
+    assert abs(float(sumsq) - norm2) <= 1e-5 * norm2
+    factor = min(1.0, 0.1 / math.sqrt(norm2))
+    for got, w0, gr, decay in ((Wr, Wr0, ga, 0.0), (W, W0, gq, 0.1)):
+        want, _, _ = OT.adamw(w0.numpy(), gr.numpy(), 0.0, 0.0, 1, 1e-2, decay=decay, factor=factor)
+        # the first step is lr sign(g), wherever g is not tiny
+        big = (factor * gr).abs() > 1e-5
+        assert (got.cpu().double() - torch.as_tensor(want))[big].abs().max() <= 1e-5
+        assert int(big.sum()) > 0.9 * big.numel() - 1 or decay
+
+
+def test_training_calls_in_one_graph(L):  # noqa: F811
+    """Captured once, replayed: losses, gradient, norm and the step, with rate and
+    step count on the GPU, as eager calls make them."""
+    T, E, k, n = 700, 24, 3, 5000
+    gen = TC.gen("graph")
+    z0 = dev(TC.normal(gen, T, E, dtype=torch.bfloat16))
+    p0 = dev(TC.normal(gen, n, std=0.02, dtype=torch.bfloat16))
+    extra = dev(TC.normal(gen, n, std=0.01))
+
+    def make():
+        s = dict(z=z0.clone(), p=p0.clone(), g=extra.clone(), lr=torch.full((1,), 1e-3, device=DEV),
+                 steps=torch.zeros(1, dtype=torch.int64, device=DEV),
+                 e=torch.empty(T * k, dtype=torch.int32, device=DEV), w=torch.empty(T * k, device=DEV),
+                 counts=torch.empty(E, dtype=torch.int32, device=DEV), loss=torch.empty(2, device=DEV),
+                 saved=torch.empty(E + 2, device=DEV), dz=torch.empty_like(z0),
+                 sumsq=torch.empty(1, dtype=torch.float64, device=DEV))
+        for x in "mv":
+            s[x] = torch.zeros(n, dtype=torch.uint8, device=DEV)
+            s[x + "e"] = torch.zeros((n + 31) // 32, dtype=torch.uint8, device=DEV)
+        r = L.Router(s["z"], k)
+        b = L.Balance(r, counts=s["counts"], z_coef=1e-3)
+        ps = L.Params(g=[s["g"]], p=[s["p"]], m=[s["m"]], v=[s["v"]], m_exp=[s["me"]], v_exp=[s["ve"]])
+        opt = L.AdamW(lr=s["lr"], seed=9, max_norm=0.5, sumsq=s["sumsq"], steps=s["steps"])
+        ws = [torch.empty(x, dtype=torch.uint8, device=DEV) for x in
+              (r.ws_bytes, L.lrm_balance_workspace_size(b), L.lrm_sumsq_workspace_size(ps))]
+
+        def call():
+            L.lrm_route(r, s["e"], s["w"], counts=s["counts"], ws=ws[0])
+            L.lrm_balance_loss(b, s["loss"], s["saved"], ws=ws[1])
+            L.lrm_balance_bwd(b, s["saved"], s["dz"])
+            L.lrm_grad_sumsq(ps, s["sumsq"], ws=ws[2])
+            L.lrm_adamw(ps, opt)
+        return s, call
+
+    a, eager = make()
+    b, captured = make()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        captured()
+    for i in range(4):
+        for s in (a, b):  # other inputs and another rate before every replay
+            s["z"].copy_(z0 * (1 + i))
+            s["g"].copy_(extra * (1 + i))
+            s["lr"].fill_(1e-3 / (1 + i))
+        eager()
+        torch.cuda.synchronize()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert int(b["steps"]) == i + 1
+        for key in a:
+            assert torch.equal(a[key].view(torch.uint8), b[key].view(torch.uint8)), (i, key)
+
+
+def test_two_streams_at_once(L):  # noqa: F811
+    """The same calls on two streams, each with its own tensors and workspaces."""
+    runs = []
+    for i in range(2):
+        c = TC.balance_case("many_bf16", **TC.BALANCE_LARGE["many_bf16"])
+        b = make_balance(L, c)
+        q = TC.param_case("eight_bf16")
+        ps, lists, _ = on_gpu(L, q)
+        runs.append((c, b, q, ps, lists, torch.cuda.Stream()))
+    torch.cuda.synchronize()
+    outs = []
+    for c, b, q, ps, lists, s in runs:
+        sumsq = filled((1,), torch.float64)
+        s.wait_stream(torch.cuda.current_stream())
+        got = run_balance(L, c, b, s)
+        L.lrm_grad_sumsq(ps, sumsq, stream=s)
+        L.lrm_adamw(ps, options(L, q, sumsq=sumsq), q["step"], stream=s)
+        outs.append((got, sumsq))
+    torch.cuda.synchronize()
+    for (c, b, q, ps, lists, s), (got, _) in zip(runs, outs):
+        TC.check_balance(c, got[0].cpu(), got[1].cpu(), got[2].cpu())
+        TC.check_adamw(q, back(q, lists))
