@@ -594,7 +594,7 @@ size_t lrm_route_share_workspace_size(int32_t T, int32_t k);
  *   balance = coef / S' sum over s, e of a_se (sum over the tokens of s of p_te)
  *   z       = z_coef / n sum over the tokens of sequences of (log sum_e exp z_te)^2
  * The counts have no gradient.  coef = 1 and a balanced choice give balance = 1 or
- * so.  Sums over tokens: fp32 over at most 512 tokens of a run, then fp64. */
+ * so.  Sums over tokens: fp32 over at most 256 tokens of a run, then fp64. */
 typedef struct lrm_balance {
   lrm_router router;
   const int32_t* expert; /* device [T*k], the choice (of lrm_route, or any: entries outside

@@ -73,14 +73,11 @@ BalanceArgs carve_balance(Carve& c, const lrm_balance* b) {
   BalanceArgs g{};
   const int E = b->router.E, T = b->router.T;
   g.S = b->S;
-  g.chunk = balance_chunk(T);
+  g.chunk = balance_chunk(T, E, b->router.k);
   g.chunks = (int)(((int64_t)T + g.chunk - 1) / g.chunk);
-  const int64_t rows = (int64_t)g.chunks + b->S;
-  g.sums = c.take<float>(rows * E);
-  if (!b->counts) g.cnt = c.take<int32_t>(rows * E);
-  g.rows = c.take<BalanceRow>(rows);
-  g.seq_bal = c.take<double>((int64_t)b->S * ((E + kJoinCols - 1) / kJoinCols));
-  g.seq_rows = c.take<BalanceSeq>(b->S);
+  g.rows = c.take<BalanceRow>((int64_t)g.chunks + b->S);
+  g.blocks = c.take<double>((int64_t)balance_join_blocks(b->S) * 4);
+  if (!b->counts) g.cnt = c.take<int32_t>((int64_t)b->S * E);
   return g;
 }
 

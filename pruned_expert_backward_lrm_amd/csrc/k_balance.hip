@@ -7,13 +7,14 @@
 // joined with that of the routing weights.  (The pages take a balanced router as
 // given; its counts are those of the controller: page 1, bullet "Квоты до вычислений".)
 //
-// The loss reads the logits once: a block takes a run of tokens (a chunk) and, for
-// every sequence that reaches into it, leaves one row of column sums, counts and
-// three numbers.  Chunk c and sequence s meet in row c + s: along the tokens one of
-// the two grows at a time, so no two pairs share a row and chunks + S rows are
-// enough, whatever the offsets (which only the GPU knows).  A second launch adds a
-// sequence's rows in fp64, a third one the sequences (not for a single one of up to
-// 256 experts).
+// f_se being the counts' ratios, the loss needs no sums per expert: a token adds
+// sum over e of c_se p_te, one number.  So where the counts are at hand the logits are
+// read once and every block leaves three numbers; where they are not, a histogram of
+// the choice comes first.  A block takes a run of tokens (a chunk); chunk c and
+// sequence s meet in row c + s of the scratch: along the tokens one of the two
+// grows at a time, so no two pairs share a row and chunks + S rows are enough,
+// whatever the offsets (which only the GPU knows).  The last launch adds a
+// sequence's rows with a wave, in fp64 and in order.
 #include "common.h"
 #include "launch.h"
 #include "route_util.h"
@@ -22,25 +23,113 @@ namespace lrm {
 
 namespace {
 
-template <int NV>
-constexpr int balance_threads() { return NV > 8 ? 256 : 512; }
+constexpr int kThreads = 256;
+constexpr float kLog2e = 1.44269504f, kLn2 = 0.693147181f;
 
-// e^x for x <= 0.  bf16 logits, good to 2^-9 of themselves, take the hardware's
-// exp2 of the rounded product (error 2^-24 |x|); fp32 ones put its error back.
-template <bool BF16>
-__device__ __forceinline__ float exp_row(float x) {
-  return BF16 ? __builtin_amdgcn_exp2f(x * 1.44269504f) : exp_of(x);
+__device__ __forceinline__ int64_t at_most(int64_t a, int64_t b) { return a < b ? a : b; }
+__device__ __forceinline__ int64_t at_least(int64_t a, int64_t b) { return a > b ? a : b; }
+
+template <typename V>
+__device__ __forceinline__ V wave_add(V v) { return group_all<kWave>(v, OpAdd()); }
+
+struct OpMaxF {
+  __device__ __forceinline__ float operator()(float a, float b) const { return fmaxf(a, b); }
+};
+
+// Column of a lane's j-th value.  VEC: aligned rows of a multiple of NV elements,
+// NV neighbours a lane, 16 bytes at a time; otherwise the lanes' columns alternate,
+// so that single elements load and store whole lines together.
+template <int LPT, int NV, bool VEC>
+__device__ __forceinline__ int column(int i, int j) { return VEC ? i * NV + j : j * LPT + i; }
+
+// (Loads of single elements are clamped, not guarded: behind a branch each would
+// wait for the one before.)
+template <int LPT, int NV, bool VEC, bool BF16>
+struct Row {
+  u32x4 q[VEC ? NV / (BF16 ? 8 : 4) : 1];
+  uint32_t x[VEC ? 1 : NV];
+  __device__ __forceinline__ void fetch(const void* row, int i, int E) {
+    if constexpr (VEC) {
+      const int c = i * NV < E ? i * NV : 0;
+      if constexpr (BF16) {
+        const u32x4* src = reinterpret_cast<const u32x4*>((const uint16_t*)row + c);
+#pragma unroll
+        for (int p = 0; p < NV / 8; ++p) q[p] = src[p];
+      } else {
+        const u32x4* src = reinterpret_cast<const u32x4*>((const float*)row + c);
+#pragma unroll
+        for (int p = 0; p < NV / 4; ++p) q[p] = src[p];
+      }
+    } else {
+#pragma unroll
+      for (int j = 0; j < NV; ++j) {
+        const int c = column<LPT, NV, VEC>(i, j), cc = c < E ? c : E - 1;
+        x[j] = BF16 ? ((const uint16_t*)row)[cc] : ((const uint32_t*)row)[cc];
+      }
+    }
+  }
+  // (columns at or past E: -inf)
+  __device__ __forceinline__ void values(int i, int E, float (&z)[NV]) const {
+    const float none = -__builtin_inff();
+    if constexpr (VEC) {
+      if constexpr (BF16) {
+#pragma unroll
+        for (int j = 0; j < NV; ++j) {
+          const uint32_t w = q[j / 8][(j & 7) >> 1];
+          z[j] = j & 1 ? bf16_hi(w) : bf16_lo(w);
+        }
+      } else {
+#pragma unroll
+        for (int j = 0; j < NV; ++j) z[j] = __uint_as_float(q[j / 4][j & 3]);
+      }
+      if (E == LPT * NV) return;
+#pragma unroll
+      for (int j = 0; j < NV; ++j) z[j] = i * NV < E ? z[j] : none;
+    } else {
+#pragma unroll
+      for (int j = 0; j < NV; ++j)
+        z[j] = column<LPT, NV, VEC>(i, j) < E ? __uint_as_float(BF16 ? x[j] << 16 : x[j]) : none;
+    }
+  }
+};
+
+// A bit for every column of the lane that takes part.
+template <int LPT, int NV, bool VEC>
+__device__ __forceinline__ uint64_t open_bits(const uint8_t* mask, int i, int E) {
+  if (!mask) return ~0ull;
+  uint64_t bits = 0;
+#pragma unroll
+  for (int j = 0; j < NV; ++j) {
+    const int c = column<LPT, NV, VEC>(i, j);
+    bits |= (uint64_t)(mask[c < E ? c : 0] != 0 ? 1u : 0u) << j;
+  }
+  return bits;
 }
 
-// Shares p of a lane's experts from their eligible logits z (masked: -inf), in
-// place; inv_sum their factor; rest (sigmoid): 1 - sigma.  Returns whether the
-// token has an eligible expert; lse: log of the exps' sum (softmax).
-template <int LPT, int NV, bool BF16, bool SIG, bool GRAD>
-__device__ __forceinline__ bool shares(float (&z)[NV], float (&rest)[GRAD && SIG ? NV : 1], float* lse) {
+// The lane's entries of a row of E numbers (0 past it).
+template <int LPT, int NV, bool VEC, typename V>
+__device__ __forceinline__ void numbers_row(const V* row, int i, int E, float (&w)[NV]) {
+  V x[NV];
+#pragma unroll
+  for (int j = 0; j < NV; ++j) {
+    const int c = column<LPT, NV, VEC>(i, j);
+    x[j] = row[c < E ? c : 0];
+  }
+#pragma unroll
+  for (int j = 0; j < NV; ++j) w[j] = column<LPT, NV, VEC>(i, j) < E ? (float)x[j] : 0.f;
+}
+
+// A lane's share of a token: the exps f of its eligible logits z (masked: -inf) in
+// place of them, with the row's largest taken out, inv one over their sum (0: no
+// eligible expert), lse its log.  One rounding in the exponent: f is good to 2^-24
+// of the logit's distance from the largest.  SIG: f = sigma, rest = 1 - sigma.
+template <int LPT, int NV, bool SIG, bool GRAD>
+__device__ __forceinline__ bool shares(float (&z)[NV], float (&rest)[GRAD && SIG ? NV : 1], bool want_lse,
+                                       float* inv, float* lse) {
   float top = -__builtin_inff(), sum = 0.f;
 #pragma unroll
-  for (int j = 0; j < NV; ++j) top = z[j] > top ? z[j] : top;
-  top = group_all<LPT>(top, OpMax());
+  for (int j = 0; j < NV; ++j) top = fmaxf(top, z[j]);
+  top = group_all<LPT>(top, OpMaxF());
   const bool live = top > -__builtin_inff();
   if constexpr (SIG) {
     // sigma times e^-m, m = top where every score would be tiny, so that the
@@ -48,382 +137,493 @@ __device__ __forceinline__ bool shares(float (&z)[NV], float (&rest)[GRAD && SIG
     const float m = live && top < -60.f ? top : 0.f;
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
-      const float q = exp_row<BF16>(-fabsf(z[j])), r = inv_of(1.f + q);
-      const float up = m < 0.f ? exp_row<BF16>(z[j] - m) : q;
+      const float q = __builtin_amdgcn_exp2f(fabsf(z[j]) * -kLog2e), r = inv_of(1.f + q);
+      const float up = m < 0.f ? __builtin_amdgcn_exp2f((z[j] - m) * kLog2e) : q;
       if constexpr (GRAD) rest[j] = z[j] > 0.f ? q * r : r;
       z[j] = z[j] > 0.f ? r : up * r;  // (0 for -inf)
       sum += z[j];
     }
+    sum = group_all<LPT>(sum, OpAdd());
+    *inv = live ? 1.f / sum : 0.f;
+    *lse = 0.f;
   } else {
-    const float m = live ? top : 0.f;
+    const float m = live ? top * kLog2e : 0.f;
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
-      z[j] = exp_row<BF16>(z[j] - m);
+      z[j] = __builtin_amdgcn_exp2f(fmaf(z[j], kLog2e, -m));
       sum += z[j];
     }
+    sum = group_all<LPT>(sum, OpAdd());
+    *inv = live ? inv_of(sum) : 0.f;  // (1 .. 4096)
+    *lse = want_lse && live ? fmaf(__builtin_amdgcn_logf(sum), kLn2, top) : 0.f;
   }
-  sum = group_all<LPT>(sum, OpAdd());
-  const float inv = live ? 1.f / sum : 0.f;
-#pragma unroll
-  for (int j = 0; j < NV; ++j) z[j] *= inv;
-  *lse = SIG || !live ? 0.f : top + logf(sum);
   return live;
 }
 
-// Largest s in [0, S) with seq[s] <= t, or 0.
+// Largest s in [0, S) with seq[s] <= t, or 0 (t the same in a whole wave): 64 places
+// are looked at at a time.
 __device__ __forceinline__ int sequence_at(const int32_t* seq, int S, int64_t t) {
-  int lo = 0, hi = S;
-  while (hi - lo > 1) {
-    const int mid = (lo + hi) >> 1;
-    if (seq[mid] <= t) lo = mid;
-    else hi = mid;
+  int lo = 0, n = S;
+  while (n > 1) {
+    const int step = (n + kWave - 1) / kWave, at = lane_id() * step;
+    const bool before = at < n && seq[lo + (at < n ? at : 0)] <= t;
+    const int c = __popcll(__ballot(before));
+    const int k = c > 0 ? (c - 1) * step : 0;
+    lo += k;
+    n = n - k < step ? n - k : step;
   }
   return lo;
 }
 
-// NV values from column c0 of row t of the output (columns at or past E: none).
-template <int NV>
-__device__ __forceinline__ void store_row(void* out, bool bf16, bool vec, int64_t at, int c0, int E,
+// The lane's values into the row that starts at element `at`.
+template <int LPT, int NV, bool VEC, bool BF16>
+__device__ __forceinline__ void store_row(void* out, bool vec, int64_t at, int i, int E,
                                           const float (&o)[NV]) {
-  if (vec && c0 + NV <= E) {
-    if (bf16) {
-      u32x4* dst = reinterpret_cast<u32x4*>((uint16_t*)out + at + c0);
+  if (VEC && vec) {
+    const int c = i * NV;
+    if (c >= E) return;
+    if constexpr (BF16) {
+      u32x4* dst = reinterpret_cast<u32x4*>((uint16_t*)out + at + c);
 #pragma unroll
       for (int q = 0; q < NV / 8; ++q)
         dst[q] = u32x4{cvt_pk_bf16(o[8 * q], o[8 * q + 1]), cvt_pk_bf16(o[8 * q + 2], o[8 * q + 3]),
                        cvt_pk_bf16(o[8 * q + 4], o[8 * q + 5]), cvt_pk_bf16(o[8 * q + 6], o[8 * q + 7])};
     } else {
-      f32x4* dst = reinterpret_cast<f32x4*>((float*)out + at + c0);
+      f32x4* dst = reinterpret_cast<f32x4*>((float*)out + at + c);
 #pragma unroll
       for (int q = 0; q < NV / 4; ++q) dst[q] = f32x4{o[4 * q], o[4 * q + 1], o[4 * q + 2], o[4 * q + 3]};
     }
     return;
   }
 #pragma unroll
-  for (int j = 0; j < NV; ++j)
-    if (c0 + j < E) {
-      if (bf16) ((uint16_t*)out)[at + c0 + j] = (uint16_t)f32_to_bf16_bits(o[j]);
-      else ((float*)out)[at + c0 + j] = o[j];
+  for (int j = 0; j < NV; ++j) {
+    const int c = column<LPT, NV, VEC>(i, j);
+    if (c < E) {
+      if constexpr (BF16) ((uint16_t*)out)[at + c] = (uint16_t)(cvt_pk_bf16(o[j], o[j]));
+      else ((float*)out)[at + c] = o[j];
     }
+  }
 }
 
-// ------------------------------------------------------------------- loss
-template <int LPT, int NV, bool BF16, bool SIG>
-__global__ __launch_bounds__(balance_threads<NV>()) void k_balance(RouteArgs a, BalanceArgs b) {
-  LRM_DYN_SHARED(float, dyn);  // [rows][E] column sums, int hist[E]
-  constexpr int NT = balance_threads<NV>(), tpb = NT / LPT, NW = NT / kWave;
-  constexpr int NR = NV == 8 ? NW : 1;  // rows of column sums: a wave's each, or one in turn
-  __shared__ BalanceRow part[NW];
-  int* hist = reinterpret_cast<int*>(dyn + NR * a.E);
-  const int i = threadIdx.x & (LPT - 1), slot = threadIdx.x / LPT;
-  const int w = threadIdx.x >> 6;
-  const uint64_t bits = expert_bits<NV>(a, i * NV);
-  const int64_t c0 = (int64_t)blockIdx.x * b.chunk;
-  const int64_t c1 = min<int64_t>(c0 + b.chunk, a.T);
-  if (b.cnt)
-    for (int e = threadIdx.x; e < a.E; e += NT) hist[e] = 0;
+// -------------------------------------------------------------- histogram
+// Slots of tokens [t0, t1) into hist (LDS, clear): kk places a token, the power of 2
+// from k on, four tokens a place in flight.
+__device__ __forceinline__ void count_slots(const RouteArgs& a, const int32_t* expert, int64_t t0,
+                                            int64_t t1, int nt, int log_kk, int* hist) {
+  const int i = threadIdx.x & ((1 << log_kk) - 1), step = nt >> log_kk;
+  if (i >= a.k) return;
+  for (int64_t t = t0 + (threadIdx.x >> log_kk); t < t1; t += 4 * step) {
+    int e[4], on[4];
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      const int64_t tq = t + q * step < t1 ? t + q * step : t;
+      e[q] = expert[tq * a.k + i];
+      on[q] = a.token_mask ? a.token_mask[tq] : 1;
+    }
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      const bool named = e[q] >= 0 && e[q] < a.E;
+      const int open = a.expert_mask ? a.expert_mask[named ? e[q] : 0] : 1;
+      if (t + q * step < t1 && named && on[q] && open) atomicAdd(&hist[e[q]], 1);
+    }
+  }
+}
+
+// Chunks of tokens; integer sums, so their order does not show.  out is clear.
+__global__ __launch_bounds__(kThreads) void k_balance_count(RouteArgs a, BalanceArgs b, int64_t chunk,
+                                                            int log_kk, int32_t* out) {
+  LRM_DYN_SHARED(int, hist);  // [E]
+  const int64_t c0 = (int64_t)blockIdx.x * chunk, c1 = at_most(c0 + chunk, a.T);
+  for (int e = threadIdx.x; e < a.E; e += kThreads) hist[e] = 0;
   for (int s = b.seq ? sequence_at(b.seq, b.S, c0) : 0; s < b.S; ++s) {
     int64_t t0 = c0, t1 = c1;
     if (b.seq) {
-      t0 = max<int64_t>(c0, b.seq[s]);
-      t1 = min<int64_t>(c1, b.seq[s + 1]);
+      t0 = at_least(c0, b.seq[s]);
+      t1 = at_most(c1, b.seq[s + 1]);
       if (b.seq[s] >= c1) break;
       if (t0 >= t1) continue;
     }
-    float acc[NV];
-#pragma unroll
-    for (int j = 0; j < NV; ++j) acc[j] = 0.f;
-    int live = 0, filled = 0;
-    double lse2 = 0.0;
-    __syncthreads();  // hist is clear, the row before has been read
-    for (int64_t r = t0; r < t1; r += tpb) {
-      const int64_t t = r + slot;
-      const bool in = t < t1;
-      const bool on = in && (a.token_mask ? a.token_mask[in ? t : 0] != 0 : true);
-      float z[NV], rest[1], lse;
-      load_row<NV>((const char*)a.logits + (in ? t : t0) * a.ld * (BF16 ? 2 : 4), BF16, a.vec != 0, i * NV,
-                   a.E, z);
-      mask_row<NV>(on ? bits : 0, z);
-      const bool has = shares<LPT, NV, BF16, SIG, false>(z, rest, &lse);
-#pragma unroll
-      for (int j = 0; j < NV; ++j) acc[j] += z[j];
-      if (i == 0 && has) {
-        ++live;
-        lse2 += (double)lse * (double)lse;
-      }
-      if (b.cnt && on && i < a.k) {
-        const int e = b.expert[t * a.k + i];
-        const bool named = e >= 0 && e < a.E;
-        if (named && (a.expert_mask ? a.expert_mask[named ? e : 0] != 0 : true)) {
-          ++filled;
-          atomicAdd(&hist[e], 1);
-        }
-      }
-    }
-    // the tokens of a wave, then the waves, in order
-#pragma unroll
-    for (int j = 0; j < NV; ++j) {
-      if constexpr (LPT == 16) acc[j] = across<16>(acc[j], OpAdd());
-      if constexpr (LPT <= 32) acc[j] = across<32>(acc[j], OpAdd());
-    }
-    live = wave_sum(live);
-    filled = wave_sum(filled);
-    lse2 = wave_sum(lse2);
-    if (lane_id() == 0) part[w] = BalanceRow{lse2, live, filled};
-    for (int q = 0; q < (NR == 1 ? NW : 1); ++q) {
-      if ((NR > 1 || q == w) && lane_id() < LPT) {
-        float* row = dyn + (NR > 1 ? w : 0) * a.E;
-#pragma unroll
-        for (int j = 0; j < NV; ++j) {
-          const int e = i * NV + j;
-          if (e < a.E) row[e] = NR > 1 || q == 0 ? acc[j] : row[e] + acc[j];
-        }
-      }
-      __syncthreads();
-    }
-    const int64_t at = (int64_t)blockIdx.x + s;
-    for (int e = threadIdx.x; e < a.E; e += NT) {
-      float v = dyn[e];
-      for (int q = 1; q < NR; ++q) v += dyn[q * a.E + e];
-      b.sums[at * a.E + e] = v;
-      if (b.cnt) {
-        b.cnt[at * a.E + e] = hist[e];
-        hist[e] = 0;
-      }
-    }
-    if (threadIdx.x == 0) {
-      BalanceRow v = part[0];
-      for (int q = 1; q < NW; ++q) {
-        v.lse2 += part[q].lse2;
-        v.live += part[q].live;
-        v.filled += part[q].filled;
-      }
-      b.rows[at] = v;
+    __syncthreads();
+    count_slots(a, b.expert, t0, t1, kThreads, log_kk, hist);
+    __syncthreads();
+    for (int e = threadIdx.x; e < a.E; e += kThreads) {
+      if (hist[e]) atomicAdd(&out[(int64_t)s * a.E + e], hist[e]);
+      hist[e] = 0;
     }
   }
 }
 
-// Sum over a block of 1024 threads, in a fixed order, in every thread.
-__device__ __forceinline__ double block_sum(double v, double* lds) {
-  v = wave_sum(v);
-  __syncthreads();
-  if (lane_id() == 0) lds[threadIdx.x >> 6] = v;
-  __syncthreads();
-  double s = lds[0];
-  for (int q = 1; q < 16; ++q) s += lds[q];
+// ------------------------------------------------------------------- loss
+// What a thread adds up over its tokens of [t0, t1), one at least: w the counts of
+// its experts.  (fp32 over a chunk's tokens and the lanes of a wave: at most 16 and 6
+// additions; fp64 from there.)
+struct Sums {
+  float dot, lse2;
+  int live;
+};
+__device__ __forceinline__ BalanceRow wave_row(const Sums& v) {
+  return BalanceRow{(double)wave_add(v.dot), (double)wave_add(v.lse2), wave_add(v.live), 0};
+}
+template <int LPT, int NV, bool SIG, bool VEC, bool BF16>
+__device__ __forceinline__ Sums pass(const RouteArgs& a, bool z_wanted, int64_t t0, int64_t t1, int tpb,
+                                     uint64_t bits, const int32_t* counts) {
+  const int i = threadIdx.x & (LPT - 1), slot = threadIdx.x / LPT;
+  const bool masked = a.expert_mask || a.token_mask;
+  // the place of the thread's next row (tokens behind the last one: the last place again)
+  const int64_t stride = (int64_t)tpb * a.ld * (BF16 ? 2 : 4);
+  const int n = (int)(t1 - t0);
+  int ahead = slot;
+  const char* next = (const char*)a.logits + (t0 + (slot < n ? slot : 0)) * a.ld * (BF16 ? 2 : 4);
+  auto step = [&] {
+    ahead += tpb;
+    next += ahead < n ? stride : 0;
+  };
+  Sums s{0.f, 0.f, 0};
+  // DEEP rows of a place on their way at once: a chunk is short, its time the loads' latency
+  constexpr int DEEP = NV == 8 ? 4 : 1;
+  Row<LPT, NV, VEC, BF16> raw[DEEP];
+#pragma unroll
+  for (int q = 0; q < DEEP; ++q) {
+    raw[q].fetch(next, i, a.E);
+    step();
+  }
+  float w[NV];
+  numbers_row<LPT, NV, VEC>(counts, i, a.E, w);
+  for (int r = 0; r < n; r += DEEP * tpb) {
+#pragma unroll
+    for (int q = 0; q < DEEP; ++q) {
+      const int t = r + slot + q * tpb;
+      const bool in = t < n;
+      float z[NV], rest[1], inv, lse, dot = 0.f;
+      raw[q].values(i, a.E, z);
+      if (r + (q + DEEP) * tpb < n) {
+        raw[q].fetch(next, i, a.E);
+        step();
+      }
+      if (q > 0 && r + q * tpb >= n) break;
+      if (masked) mask_row<NV>(in && (a.token_mask ? a.token_mask[t0 + (in ? t : 0)] != 0 : true) ? bits : 0, z);
+      const bool live = shares<LPT, NV, SIG, false>(z, rest, z_wanted, &inv, &lse) && in;
+#pragma unroll
+      for (int j = 0; j < NV; ++j) dot = fmaf(z[j], w[j], dot);
+      s.dot = fmaf(dot, in ? inv : 0.f, s.dot);
+      const bool one = live && i == 0;
+      s.live += one ? 1 : 0;
+      lse = one ? lse : 0.f;
+      s.lse2 = fmaf(lse, lse, s.lse2);
+    }
+  }
   return s;
 }
 
-// The losses and the batch's factors from the sums over all sequences.
-__device__ __forceinline__ void balance_end(const BalanceArgs& b, int E, double bal, double lse2,
-                                            double n, double full) {
-  const double fb = full > 0.0 ? (double)b.coef / full : 0.0;
-  const double fz = n > 0.0 ? (double)b.z_coef / n : 0.0;
-  b.loss[0] = (float)(fb * bal);
-  b.loss[1] = (float)(fz * lse2);
-  b.saved[(int64_t)b.S * E] = (float)((double)b.coef / (full > 0.0 ? full : 1.0));
-  b.saved[(int64_t)b.S * E + 1] = (float)(2.0 * (double)b.z_coef / (n > 0.0 ? n : 1.0));
+template <int LPT, int NV, bool SIG, bool VEC, bool BF16>
+__global__ __launch_bounds__(kThreads) void k_balance(RouteArgs a, BalanceArgs b) {
+  __shared__ BalanceRow part[kThreads / kWave];
+  const int i = threadIdx.x & (LPT - 1);
+  const uint64_t bits = open_bits<LPT, NV, VEC>(a.expert_mask, i, a.E);
+  const int64_t k0 = (int64_t)blockIdx.x * b.chunk;
+  const int64_t k1 = at_most(k0 + b.chunk, a.T);
+  for (int s = b.seq ? sequence_at(b.seq, b.S, k0) : 0; s < b.S; ++s) {
+    int64_t t0 = k0, t1 = k1;
+    if (b.seq) {
+      t0 = at_least(k0, b.seq[s]);
+      t1 = at_most(k1, b.seq[s + 1]);
+      if (b.seq[s] >= k1) break;
+      if (t0 >= t1) continue;
+    }
+    const BalanceRow v = wave_row(pass<LPT, NV, SIG, VEC, BF16>(
+        a, b.z_coef != 0.f, t0, t1, kThreads / LPT, bits, b.counts + (int64_t)s * a.E));
+    __syncthreads();  // (part of the sequence before has been read)
+    if (lane_id() == 0) part[threadIdx.x >> 6] = v;
+    __syncthreads();
+    if (threadIdx.x == 0) {
+      BalanceRow x = part[0];
+      for (int q = 1; q < kThreads / kWave; ++q) {
+        x.dot += part[q].dot;
+        x.lse2 += part[q].lse2;
+        x.live += part[q].live;
+      }
+      b.rows[(int64_t)blockIdx.x + s] = x;
+    }
+  }
 }
 
-// One block for CW columns of one sequence: 1024 / CW threads a column, each
-// sixteen rows at a time.
-template <int CW>
+// Over all sequences: sum of M dot_s / (filled_s n_s), of log^2, of n_s, and how many have tokens.
+struct Batch {
+  double bal, lse2, live, full;
+};
+__device__ __forceinline__ void balance_end(const BalanceArgs& b, int E, const Batch& v) {
+  const double fb = (double)b.coef / (v.full > 0.0 ? v.full : 1.0);
+  const double fz = (double)b.z_coef / (v.live > 0.0 ? v.live : 1.0);
+  b.loss[0] = (float)(fb * v.bal);
+  b.loss[1] = (float)(fz * v.lse2);
+  b.saved[(int64_t)b.S * E] = (float)fb;
+  b.saved[(int64_t)b.S * E + 1] = (float)(2.0 * fz);
+}
+
+// One wave for a sequence with these sums and counts: its part of saved and of the
+// batch (the same in every lane).
+__device__ __forceinline__ void sequence_end(const RouteArgs& a, const BalanceArgs& b, int s, double experts,
+                                             const BalanceRow& v, const int32_t* counts, Batch* out) {
+  double filled = 0.0;
+  for (int e = lane_id(); e < a.E; e += 4 * kWave) {
+    int n[4];
+#pragma unroll
+    for (int q = 0; q < 4; ++q) n[q] = counts[e + q * kWave < a.E ? e + q * kWave : e];
+#pragma unroll
+    for (int q = 0; q < 4; ++q) filled += e + q * kWave < a.E ? (double)n[q] : 0.0;
+  }
+  filled = wave_add(filled);
+  const double f = filled > 0.0 && v.live > 0 ? experts / (filled * (double)v.live) : 0.0;
+  for (int e = lane_id(); e < a.E; e += kWave) {
+    const int n = counts[e];
+    b.saved[(int64_t)s * a.E + e] = (float)(f * (double)n);
+    if (b.counts_out) b.counts_out[(int64_t)s * a.E + e] = n;
+  }
+  out->bal += f * v.dot;
+  out->lse2 += v.lse2;
+  out->live += (double)v.live;
+  out->full += v.live > 0 ? 1.0 : 0.0;
+}
+__device__ __forceinline__ double open_experts(const RouteArgs& a) {
+  if (!a.expert_mask) return (double)a.E;
+  int n = 0;
+  for (int e = lane_id(); e < a.E; e += kWave) n += a.expert_mask[e] ? 1 : 0;
+  return (double)wave_add(n);
+}
+
+// A sequence at a time for every wave, or (ALL) one sequence for the block; a single
+// block finishes the batch too.
+template <bool ALL>
 __global__ __launch_bounds__(1024) void k_balance_join(RouteArgs a, BalanceArgs b) {
-  constexpr int RG = 1024 / CW;
-  __shared__ double part[RG][CW];
-  __shared__ int ipart[RG][CW];
-  __shared__ double lds[16];
-  const int col = threadIdx.x % CW, rg = threadIdx.x / CW;
-  const int e = blockIdx.x * CW + col, ec = e < a.E ? e : 0;
-  for (int s = blockIdx.y; s < b.S; s += gridDim.y) {
+  __shared__ Batch part[16];
+  __shared__ BalanceRow rows[16];
+  const int w = threadIdx.x >> 6, l = lane_id();
+  const int64_t waves = (int64_t)gridDim.x * 16;
+  const double experts = open_experts(a);
+  constexpr int step = ALL ? 1024 : kWave;
+  Batch mine{0.0, 0.0, 0.0, 0.0};
+  for (int64_t s = ALL ? 0 : (int64_t)blockIdx.x * 16 + w; s < b.S; s += waves) {
     // the rows of this sequence (offsets held to the tokens)
     int64_t t0 = 0, t1 = a.T;
     if (b.seq) {
-      t0 = max<int64_t>(b.seq[s], 0);
-      t1 = min<int64_t>(b.seq[s + 1], a.T);
+      t0 = at_least(b.seq[s], 0);
+      t1 = at_most(b.seq[s + 1], a.T);
     }
     const int64_t r0 = t0 < t1 ? t0 / b.chunk + s : 0;
     const int64_t r1 = t0 < t1 ? (t1 - 1) / b.chunk + s + 1 : 0;
-    double live = 0.0, filled = 0.0, experts = 0.0, lse2 = 0.0;  // (whole numbers below 2^53)
-    for (int64_t r = r0 + threadIdx.x; r < r1; r += 1024) {
-      const BalanceRow v = b.rows[r];
-      live += (double)v.live;
-      filled += (double)v.filled;
-      lse2 += v.lse2;
-    }
-    for (int c = threadIdx.x; c < a.E; c += 1024) {
-      experts += !a.expert_mask || a.expert_mask[c] ? 1.0 : 0.0;
-      if (b.counts) filled += (double)b.counts[(int64_t)s * a.E + c];
-    }
-    double P = 0.0;
-    int n = 0;
-    for (int64_t rr = r0 + rg; rr < r1; rr += 16 * RG) {
-      float x[16];
-      int y[16];
+    BalanceRow v{0.0, 0.0, 0, 0};
+    for (int64_t rr = r0 + (ALL ? threadIdx.x : l); rr < r1; rr += 4 * step) {
+      BalanceRow x[4];
 #pragma unroll
-      for (int q = 0; q < 16; ++q) {
-        const int64_t r = rr + q * RG < r1 ? rr + q * RG : rr;
-        x[q] = b.sums[r * a.E + ec];
-        y[q] = b.cnt ? b.cnt[r * a.E + ec] : 0;
-      }
+      for (int q = 0; q < 4; ++q) x[q] = b.rows[rr + q * step < r1 ? rr + q * step : rr];
 #pragma unroll
-      for (int q = 0; q < 16; ++q) {
-        const bool ok = rr + q * RG < r1;
-        P += ok ? (double)x[q] : 0.0;
-        n += ok ? y[q] : 0;
+      for (int q = 0; q < 4; ++q) {
+        const bool ok = rr + q * step < r1;
+        v.dot += ok ? x[q].dot : 0.0;
+        v.lse2 += ok ? x[q].lse2 : 0.0;
+        v.live += ok ? x[q].live : 0;
       }
     }
-    live = block_sum(live, lds);
-    filled = block_sum(filled, lds);
-    experts = block_sum(experts, lds);
-    lse2 = block_sum(lse2, lds);
-    part[rg][col] = P;
-    ipart[rg][col] = n;
-    __syncthreads();
-    double bal = 0.0;
-    if (rg == 0 && e < a.E) {
-      for (int q = 1; q < RG; ++q) {
-        P += part[q][col];
-        n += ipart[q][col];
-      }
-      if (b.counts) n = b.counts[(int64_t)s * a.E + e];
-      const double f = filled > 0.0 ? (double)n / filled : 0.0;
-      const double v = live > 0.0 ? experts * f / live : 0.0;
-      b.saved[(int64_t)s * a.E + e] = (float)v;
-      if (b.counts_out) b.counts_out[(int64_t)s * a.E + e] = n;
-      bal = v * P;
-    }
-    bal = block_sum(bal, lds);
-    if (threadIdx.x == 0) {
-      if (b.S == 1 && gridDim.x == 1) {
-        balance_end(b, a.E, bal, lse2, live, live > 0.0 ? 1.0 : 0.0);
-      } else {
-        b.seq_bal[(int64_t)s * gridDim.x + blockIdx.x] = bal;
-        if (blockIdx.x == 0) b.seq_rows[s] = BalanceSeq{lse2, live};
+    v = BalanceRow{wave_add(v.dot), wave_add(v.lse2), wave_add(v.live), 0};
+    if constexpr (ALL) {
+      if (l == 0) rows[w] = v;
+      __syncthreads();
+      if (w > 0) return;
+      v = rows[0];
+      for (int q = 1; q < 16; ++q) {
+        v.dot += rows[q].dot;
+        v.lse2 += rows[q].lse2;
+        v.live += rows[q].live;
       }
     }
+    sequence_end(a, b, (int)s, experts, v, b.counts + s * a.E, &mine);
+  }
+  if constexpr (ALL) {
+    if (l == 0) balance_end(b, a.E, mine);
+    return;
+  }
+  if (l == 0) part[w] = mine;
+  __syncthreads();
+  if (threadIdx.x != 0) return;
+  for (int q = 1; q < 16; ++q) {
+    mine.bal += part[q].bal;
+    mine.lse2 += part[q].lse2;
+    mine.live += part[q].live;
+    mine.full += part[q].full;
+  }
+  if (gridDim.x == 1) {
+    balance_end(b, a.E, mine);
+  } else {
+    double* o = b.blocks + (int64_t)blockIdx.x * 4;
+    o[0] = mine.bal; o[1] = mine.lse2; o[2] = mine.live; o[3] = mine.full;
   }
 }
 
-// The sequences: n of their columns' sums and their numbers, in a fixed order.
-__global__ __launch_bounds__(1024) void k_balance_end(int64_t n, int E, BalanceArgs b) {
-  __shared__ double lds[16];
-  double bal = 0.0, lse2 = 0.0, live = 0.0, full = 0.0;
-  for (int64_t i = threadIdx.x; i < n; i += 1024) bal += b.seq_bal[i];
-  for (int s = threadIdx.x; s < b.S; s += 1024) {
-    const BalanceSeq v = b.seq_rows[s];
-    lse2 += v.lse2;
-    live += v.live;
-    full += v.live > 0.0 ? 1.0 : 0.0;
+// The blocks of the join, in order.
+__global__ __launch_bounds__(64) void k_balance_end(int n, int E, BalanceArgs b) {
+  Batch v{0.0, 0.0, 0.0, 0.0};
+  for (int i = threadIdx.x; i < n; i += kWave) {
+    v.bal += b.blocks[4 * i];
+    v.lse2 += b.blocks[4 * i + 1];
+    v.live += b.blocks[4 * i + 2];
+    v.full += b.blocks[4 * i + 3];
   }
-  bal = block_sum(bal, lds);
-  lse2 = block_sum(lse2, lds);
-  live = block_sum(live, lds);
-  full = block_sum(full, lds);
-  if (threadIdx.x == 0) balance_end(b, E, bal, lse2, live, full);
+  v.bal = wave_add(v.bal);
+  v.lse2 = wave_add(v.lse2);
+  v.live = wave_add(v.live);
+  v.full = wave_add(v.full);
+  if (threadIdx.x == 0) balance_end(b, E, v);
+}
+
+// Few tokens, one sequence: everything in one launch of one block.
+template <int LPT, int NV, bool SIG, bool VEC, bool BF16>
+__global__ __launch_bounds__(1024) void k_balance_one(RouteArgs a, BalanceArgs b, int log_kk) {
+  LRM_DYN_SHARED(int, hist);  // [E]
+  __shared__ BalanceRow part[16];
+  const int i = threadIdx.x & (LPT - 1);
+  for (int e = threadIdx.x; e < a.E; e += 1024) hist[e] = b.counts ? b.counts[e] : 0;
+  __syncthreads();
+  if (!b.counts) count_slots(a, b.expert, 0, a.T, 1024, log_kk, hist);
+  __syncthreads();
+  const BalanceRow v = wave_row(pass<LPT, NV, SIG, VEC, BF16>(
+      a, b.z_coef != 0.f, 0, a.T, 1024 / LPT, open_bits<LPT, NV, VEC>(a.expert_mask, i, a.E), hist));
+  if (lane_id() == 0) part[threadIdx.x >> 6] = v;
+  __syncthreads();
+  if (threadIdx.x >= kWave) return;
+  BalanceRow x = part[0];
+  for (int q = 1; q < 16; ++q) {
+    x.dot += part[q].dot;
+    x.lse2 += part[q].lse2;
+    x.live += part[q].live;
+  }
+  Batch all{0.0, 0.0, 0.0, 0.0};
+  sequence_end(a, b, 0, open_experts(a), x, hist, &all);
+  if (threadIdx.x == 0) balance_end(b, a.E, all);
 }
 
 // --------------------------------------------------------------- gradient
 // A block takes a run of tokens; the lanes of a token hold a whole row of p and
 // of a.  The chosen slots' part is added in LDS, all slots of a token at once; slot
 // after slot where a choice names an expert twice.
-template <int LPT, int NV, bool BF16, bool SIG>
-__global__ __launch_bounds__(NV > 8 ? kWave : 256) void k_balance_bwd(RouteArgs a, BalanceBwdArgs b) {
-  constexpr int NT = NV > 8 ? kWave : 256, tpb = NT / LPT;
+template <int LPT, int NV, bool SIG, bool VEC, bool BF16>
+__global__ __launch_bounds__(NV > 8 ? kWave : kThreads) void k_balance_bwd(RouteArgs a, BalanceBwdArgs b) {
+  constexpr int NT = NV > 8 ? kWave : kThreads, tpb = NT / LPT;
   alignas(16) __shared__ float lds[NT * NV];
   const int i = threadIdx.x & (LPT - 1), slot = threadIdx.x / LPT;
-  const int c0 = i * NV;
-  const uint64_t bits = expert_bits<NV>(a, c0);
+  const bool masked = a.expert_mask || a.token_mask;
+  const uint64_t bits = open_bits<LPT, NV, VEC>(a.expert_mask, i, a.E);
   float* row = lds + slot * LPT * NV;
   const float db = (b.dloss ? b.dloss[0] : 1.f) * b.saved[(int64_t)b.S * a.E];
   const float dz = (b.dloss ? b.dloss[1] : 1.f) * b.saved[(int64_t)b.S * a.E + 1];
   float w[NV];
   int s = -1;        // the sequence whose row is in w
-  bool inside = false;
+  bool inside = true;
   const int64_t r0 = (int64_t)blockIdx.x * b.chunk;
-  const int64_t r1 = min<int64_t>(r0 + b.chunk, a.T);
+  const int64_t r1 = at_most(r0 + b.chunk, a.T);
   int at = 0;        // the sequence of the token, or of the last one before it
-  if (b.seq) at = sequence_at(b.seq, b.S, r0 + slot);
-  for (int64_t r = r0; r < r1; r += tpb) {
-    const int64_t t = r + slot;
-    const bool in = t < r1;
-    const int64_t tc = in ? t : r0;
-    const bool on = in && (a.token_mask ? a.token_mask[tc] != 0 : true);
-    const char* lrow = (const char*)a.logits + tc * a.ld * (BF16 ? 2 : 4);
-    float z[NV], o[NV], rest[SIG ? NV : 1], lse;
-    load_row<NV>(lrow, BF16, a.vec != 0, c0, a.E, z);
+  if (b.seq) at = sequence_at(b.seq, b.S, r0);
+  // a token's row and slots are on their way while the one before it is worked on
+  // (behind the last token: the last place again)
+  const int n = (int)(r1 - r0);
+  const int64_t t0 = r0 + (slot < n ? slot : 0);
+  const char* next = (const char*)a.logits + t0 * a.ld * (BF16 ? 2 : 4);
+  int64_t next_slot = t0 * a.k + (i < a.k ? i : 0);
+  int64_t out = (r0 + slot) * b.ldd;
+  Row<LPT, NV, VEC, BF16> raw;
+  int e1 = -1;
+  float v1 = 0.f;
+  raw.fetch(next, i, a.E);
+  if (b.dweight) {
+    e1 = b.expert[next_slot];
+    v1 = b.dweight[next_slot];
+  }
+  for (int r = slot; r - slot < n; r += tpb, out += tpb * b.ldd) {
+    const int64_t t = r0 + r;
+    const bool in = r < n;
+    const bool on = in && (a.token_mask ? a.token_mask[in ? t : r0] != 0 : true);
+    float z[NV], o[NV], rest[SIG ? NV : 1], inv, lse;
+    const int e0 = e1;
+    const float v0 = v1;
+    raw.values(i, a.E, z);
+    if (r - slot + tpb < n) {
+      const bool more = r + tpb < n;
+      next += more ? (int64_t)tpb * a.ld * (BF16 ? 2 : 4) : 0;
+      next_slot += more ? tpb * a.k : 0;
+      raw.fetch(next, i, a.E);
+      if (b.dweight) {
+        e1 = b.expert[next_slot];
+        v1 = b.dweight[next_slot];
+      }
+    }
+    if (masked) mask_row<NV>(on ? bits : 0, z);
     int e = -1;
-    float zc = -__builtin_inff(), v = 0.f;
-    if (b.dweight && on && i < a.k) {
-      const int e0 = b.expert[t * a.k + i];
-      const bool named = e0 >= 0 && e0 < a.E;
-      const int ec = named ? e0 : 0;
-      const float x = load_one(lrow, BF16, ec);
-      const bool has = named && (a.expert_mask ? a.expert_mask[ec] != 0 : true) && x != -__builtin_inff();
+    float zc = -__builtin_inff();
+    bool twice = false;
+    if (b.dweight) {
+      // the chosen logits (masked ones: -inf), and whether a choice names an expert twice
+#pragma unroll
+      for (int j = 0; j < NV; ++j) row[column<LPT, NV, VEC>(i, j)] = z[j];
+      wave_sync();
+      const bool named = on && i < a.k && e0 >= 0 && e0 < a.E;
+      zc = row[named ? e0 : 0];
+      const bool has = named && zc != -__builtin_inff();
       e = has ? e0 : -1;
-      zc = has ? x : -__builtin_inff();
-      v = has ? a.scale * b.dweight[t * a.k + i] : 0.f;
+      zc = has ? zc : -__builtin_inff();
+      wave_sync();
+      if (has) row[e] = (float)i;
+      wave_sync();
+      twice = has && row[e] != (float)i;
+      wave_sync();
     }
     if (b.seq) {
       while (at + 1 < b.S && b.seq[at + 1] <= t) ++at;
       inside = b.seq[at] <= t && t < b.seq[at + 1];
-    } else {
-      inside = true;
     }
     if (at != s) {
       s = at;
-#pragma unroll
-      for (int j = 0; j < NV; ++j) w[j] = c0 + j < a.E ? b.saved[(int64_t)s * a.E + c0 + j] : 0.f;
+      numbers_row<LPT, NV, VEC>(b.saved + (int64_t)s * a.E, i, a.E, w);
     }
-    mask_row<NV>(on ? bits : 0, z);
-    shares<LPT, NV, BF16, SIG, true>(z, rest, &lse);
+    shares<LPT, NV, SIG, true>(z, rest, true, &inv, &lse);
     float dot = 0.f;
 #pragma unroll
     for (int j = 0; j < NV; ++j) dot = fmaf(z[j], w[j], dot);
-    dot = group_all<LPT>(dot, OpAdd());
-    const float gb = inside ? db : 0.f, gz = inside && !SIG ? dz * lse : 0.f;
+    dot = group_all<LPT>(dot, OpAdd()) * inv;
     // the chosen slots' part: d on the slot, and (softmax of all) dw p_j on every expert
     float d = 0.f, dw = 0.f;
     if (b.dweight) {
       const bool has = e >= 0;
+      const float v = has ? a.scale * v0 : 0.f;
       if (a.renorm) {
-        float m = group_all<LPT>(zc, OpMax());
+        float m = group_all<LPT>(zc, OpMaxF());
         if (SIG) m = m < 0.f ? m : 0.f;
         float f = 0.f, q = 1.f;
-        if (has) {
-          if (!SIG) {
-            f = exp_of(zc - m);
-          } else {
-            q = inv_of(1.f + exp_of(zc));  // 1 - sigmoid
-            f = zc <= 0.f ? exp_of(zc - m) * q : inv_of(1.f + exp_of(-zc));
-          }
+        if (!SIG) {
+          f = has ? __builtin_amdgcn_exp2f((zc - m) * kLog2e) : 0.f;
+        } else if (has) {
+          q = inv_of(1.f + exp_of(zc));  // 1 - sigmoid
+          f = zc <= 0.f ? exp_of(zc - m) * q : inv_of(1.f + exp_of(-zc));
         }
         const float sum = group_all<LPT>(f, OpAdd());
-        const float n = has ? f / sum : 0.f;
-        const float nv = group_all<LPT>(has ? n * v : 0.f, OpAdd());
+        const float n = has ? f * inv_of(sum) : 0.f;  // (sum is 1/2 at least)
+        const float nv = group_all<LPT>(n * v, OpAdd());
         d = n * (v - nv) * q;
       } else if (SIG) {
         d = has ? v * inv_of(1.f + exp_of(-zc)) * inv_of(1.f + exp_of(zc)) : 0.f;
       } else {
         // (p of the chosen: log p = z - lse)
-        d = has ? exp_of(zc - lse) * v : 0.f;
+        d = has ? __builtin_amdgcn_exp2f((zc - lse) * kLog2e) * v : 0.f;
         dw = group_all<LPT>(d, OpAdd());
       }
     }
+    // p_j (gb (w_j - dot) [rest_j] + gz lse - dw)
+    const float gb = inside ? db : 0.f, gz = (inside && !SIG ? dz * lse : 0.f) - dw;
+    const float pb = gb * inv, pz = (SIG ? 0.f : fmaf(-gb, dot, gz)) * inv;
 #pragma unroll
-    for (int j = 0; j < NV; ++j) {
-      float g = gb * (w[j] - dot);
-      if constexpr (SIG) g *= rest[j];
-      o[j] = z[j] * (g + (gz - dw));
-    }
+    for (int j = 0; j < NV; ++j)
+      o[j] = SIG ? z[j] * (pb * (w[j] - dot) * rest[j]) : z[j] * fmaf(pb, w[j], pz);
     if (b.dweight) {
-      // does a choice name an expert twice?
-      if (e >= 0) row[e] = (float)i;
-      wave_sync();
-      const bool twice = e >= 0 && row[e] != (float)i;
-      wave_sync();
 #pragma unroll
-      for (int j = 0; j < NV; ++j) row[c0 + j] = o[j];
+      for (int j = 0; j < NV; ++j) row[column<LPT, NV, VEC>(i, j)] = o[j];
       wave_sync();
       if (__ballot(twice)) {
         for (int q = 0; q < a.k; ++q) {
@@ -435,78 +635,105 @@ __global__ __launch_bounds__(NV > 8 ? kWave : 256) void k_balance_bwd(RouteArgs 
         wave_sync();
       }
 #pragma unroll
-      for (int j = 0; j < NV; ++j) o[j] = row[c0 + j];
+      for (int j = 0; j < NV; ++j) o[j] = row[column<LPT, NV, VEC>(i, j)];
       wave_sync();
     }
-    if (in) store_row<NV>(b.dlogits, BF16, b.vec_out != 0, t * b.ldd, c0, a.E, o);
+    if (in) store_row<LPT, NV, VEC, BF16>(b.dlogits, b.vec_out != 0, out, i, a.E, o);
   }
 }
 
-template <int LPT, int NV, bool BF16, bool SIG>
+int log2_up(int k) {
+  int l = 0;
+  while ((1 << l) < k) ++l;
+  return l;
+}
+
+template <int LPT, int NV, bool SIG, bool VEC, bool BF16>
 hipError_t balance_launch(const RouteArgs& a, const BalanceArgs& b, hipStream_t s) {
-  constexpr int NT = balance_threads<NV>(), NR = NV == 8 ? NT / kWave : 1;
-  LRM_LAUNCH(b.chunks, NT, (size_t)(NR + 1) * a.E * 4, s, k_balance<LPT, NV, BF16, SIG>)(a, b);
+  if constexpr (NV == 8) {
+    if (balance_in_one(a.T, a.E, b.S)) {
+      LRM_LAUNCH(1, 1024, (size_t)a.E * 4, s, k_balance_one<LPT, NV, SIG, VEC, BF16>)(a, b, log2_up(a.k));
+      return hipGetLastError();
+    }
+  }
+  LRM_LAUNCH(b.chunks, kThreads, 0, s, k_balance<LPT, NV, SIG, VEC, BF16>)(a, b);
   return hipGetLastError();
 }
 
-template <int LPT, int NV, bool BF16, bool SIG>
+template <int LPT, int NV, bool SIG, bool VEC, bool BF16>
 hipError_t balance_bwd_launch(const RouteArgs& a, const BalanceBwdArgs& b0, hipStream_t s) {
-  constexpr int tpb = (NV > 8 ? kWave : 256) / LPT;
+  constexpr int NT = NV > 8 ? kWave : kThreads, tpb = NT / LPT;
   BalanceBwdArgs b = b0;
   // runs of at least four tokens a place where that leaves four blocks a CU
   const int64_t steps = ((int64_t)a.T + tpb - 1) / tpb;
   const int64_t per = steps > 4096 ? (steps + 4095) / 4096 : (steps > 1024 ? (steps + 1023) / 1024 : 1);
   b.chunk = per * tpb;
-  LRM_LAUNCH((unsigned)((steps + per - 1) / per), NV > 8 ? kWave : 256, 0, s,
-             k_balance_bwd<LPT, NV, BF16, SIG>)(a, b);
+  LRM_LAUNCH((unsigned)((steps + per - 1) / per), NT, 0, s, k_balance_bwd<LPT, NV, SIG, VEC, BF16>)(a, b);
   return hipGetLastError();
 }
 
+// (whole lanes of aligned elements: rows of a multiple of a lane's V)
+#define LRM_BALANCE_TYPE(F, L, V, VEC)                                                         \
+  (a.bf16 ? (a.softmax ? F<L, V, false, VEC, true>(a, b, s) : F<L, V, true, VEC, true>(a, b, s)) \
+          : (a.softmax ? F<L, V, false, VEC, false>(a, b, s) : F<L, V, true, VEC, false>(a, b, s)))
+#define LRM_BALANCE_CALL(F, L, V) \
+  (a.vec && a.E % V == 0 ? LRM_BALANCE_TYPE(F, L, V, true) : LRM_BALANCE_TYPE(F, L, V, false))
+
 }  // namespace
 
-// Tokens of a chunk: about kBalanceChunks chunks, of at most 512 tokens (the sums
-// over one are fp32).
-int balance_chunk(int T) {
+// Tokens of a chunk: four of a place and more in about kBalanceChunks chunks, 16 at
+// most (whose sums are fp32).
+int balance_chunk(int T, int E, int k) {
+  const int places = k <= 16 && E <= 128 ? 16 : (k <= 32 && E <= 256 ? 8 : 4);  // of a block
   const int64_t c = ((int64_t)T + kBalanceChunks - 1) / kBalanceChunks;
-  return c < 32 ? 32 : (c > 512 ? 512 : (int)c);
+  const int64_t per = (c + places - 1) / places;
+  return places * (int)(per < 4 ? 4 : (per > 16 ? 16 : per));
 }
 
-hipError_t launch_balance(const RouteArgs& a, const BalanceArgs& b, hipStream_t s) {
-  if (b.chunks > 0) {
-    hipError_t e;
-#define LRM_CALL4(L, V) \
-  (a.bf16 ? (a.softmax ? balance_launch<L, V, true, false>(a, b, s)    \
-                       : balance_launch<L, V, true, true>(a, b, s))    \
-          : (a.softmax ? balance_launch<L, V, false, false>(a, b, s)   \
-                       : balance_launch<L, V, false, true>(a, b, s)))
-    auto run = [&]() -> hipError_t { LRM_ROUTE_DISPATCH(LRM_CALL4) };
-#undef LRM_CALL4
-    e = run();
+// One block for all: few tokens, but some, of one sequence (up to 512 experts).
+bool balance_in_one(int T, int E, int S) {
+  return S == 1 && T > 0 && E <= 512 && (int64_t)T * E <= kBalanceOne;
+}
+
+// Blocks of the join: 16 sequences each, 1024 at most.
+int balance_join_blocks(int S) { return S <= 64 ? 1 : (S < 16384 ? (S + 15) / 16 : 1024); }
+
+hipError_t launch_balance(const RouteArgs& a, const BalanceArgs& b0, hipStream_t s) {
+  BalanceArgs b = b0;
+  const bool one = balance_in_one(a.T, a.E, b.S);
+  if (!one && !b.counts) {
+    // about 1024 slots a block, more for over half a million
+    const int log_kk = log2_up(a.k);
+    int64_t chunk = 1024 >> log_kk;
+    if (a.T / chunk > 512) chunk = (a.T / 512 + chunk - 1) / chunk * chunk;
+    hipError_t e = launch_fill_u32(reinterpret_cast<uint32_t*>(b.cnt), 0u, (int64_t)b.S * a.E, s);
     if (e != hipSuccess) return e;
+    if (a.T > 0)
+      LRM_LAUNCH((unsigned)((a.T + chunk - 1) / chunk), kThreads, (size_t)a.E * 4, s, k_balance_count)(
+          a, b, chunk, log_kk, b.cnt);
+    b.counts = b.cnt;
   }
-  if (a.E <= 64 && b.S == 1) {
-    LRM_LAUNCH(1, 1024, 0, s, k_balance_join<64>)(a, b);
-  } else if (a.E <= 128 && b.S == 1) {
-    LRM_LAUNCH(1, 1024, 0, s, k_balance_join<128>)(a, b);
-  } else if (a.E <= 256 && b.S == 1) {
-    LRM_LAUNCH(1, 1024, 0, s, k_balance_join<256>)(a, b);
-  } else {
-    const int tiles = (a.E + kJoinCols - 1) / kJoinCols;
-    LRM_LAUNCH(dim3(tiles, b.S < 65535 ? b.S : 65535), 1024, 0, s, k_balance_join<kJoinCols>)(a, b);
-    LRM_LAUNCH(1, 1024, 0, s, k_balance_end)((int64_t)b.S * tiles, a.E, b);
+  if (one || b.chunks > 0) {
+#define LRM_CALL2(L, V) LRM_BALANCE_CALL(balance_launch, L, V)
+    auto run = [&]() -> hipError_t { LRM_ROUTE_DISPATCH(LRM_CALL2) };
+#undef LRM_CALL2
+    const hipError_t e = run();
+    if (e != hipSuccess || one) return e;
   }
+  const int blocks = balance_join_blocks(b.S);
+  if (b.S == 1)
+    LRM_LAUNCH(1, 1024, 0, s, k_balance_join<true>)(a, b);
+  else
+    LRM_LAUNCH(blocks, 1024, 0, s, k_balance_join<false>)(a, b);
+  if (blocks > 1) LRM_LAUNCH(1, 64, 0, s, k_balance_end)(blocks, a.E, b);
   return hipGetLastError();
 }
 
 hipError_t launch_balance_bwd(const RouteArgs& a, const BalanceBwdArgs& b, hipStream_t s) {
   if (a.T <= 0) return hipSuccess;
-#define LRM_CALL4(L, V) \
-  (a.bf16 ? (a.softmax ? balance_bwd_launch<L, V, true, false>(a, b, s)    \
-                       : balance_bwd_launch<L, V, true, true>(a, b, s))    \
-          : (a.softmax ? balance_bwd_launch<L, V, false, false>(a, b, s)   \
-                       : balance_bwd_launch<L, V, false, true>(a, b, s)))
-  LRM_ROUTE_DISPATCH(LRM_CALL4)
-#undef LRM_CALL4
+#define LRM_CALL2(L, V) LRM_BALANCE_CALL(balance_bwd_launch, L, V)
+  LRM_ROUTE_DISPATCH(LRM_CALL2)
+#undef LRM_CALL2
 }
 
 }  // namespace lrm

@@ -259,18 +259,15 @@ hipError_t launch_route_share(int64_t n, int k, const int32_t* expert, const flo
                               int32_t* out_slot, int32_t* out_n, int32_t* cnt, hipStream_t s);
 
 // --------------------------------------------------- balance of the load
-// What a chunk of tokens and a sequence have in common: live tokens, filled slots,
-// sum of log^2; and the same of a whole sequence.
+// What a chunk of tokens and a sequence have in common: sum of the counts' products
+// with the shares, of log^2, live tokens.
 struct BalanceRow {
-  double lse2;
-  int live, filled;
+  double dot, lse2;
+  int live, _pad;
 };
-struct BalanceSeq {
-  double lse2, live;
-};
-// lrm_balance_loss: chunks runs of chunk tokens (balance_chunk), sums and cnt
-// [chunks + S][E], rows [chunks + S], seq_bal [S][tiles of kJoinCols experts],
-// seq_rows [S].  cnt is null where counts is given.
+// lrm_balance_loss: chunks runs of chunk tokens (balance_chunk), rows [chunks + S],
+// blocks [4 * balance_join_blocks(S)]; cnt [S][E], where counts is null (and the call is not
+// one of balance_in_one).
 struct BalanceArgs {
   int S, chunk, chunks;
   float coef, z_coef;
@@ -280,15 +277,15 @@ struct BalanceArgs {
   float* loss;
   float* saved;
   int32_t* counts_out;
-  float* sums;
   int32_t* cnt;
   BalanceRow* rows;
-  double* seq_bal;
-  BalanceSeq* seq_rows;
+  double* blocks;
 };
-constexpr int kBalanceChunks = 512;
-constexpr int kJoinCols = 64;
-int balance_chunk(int T);
+constexpr int kBalanceChunks = 1024;
+constexpr int64_t kBalanceOne = 16384;
+int balance_chunk(int T, int E, int k);
+bool balance_in_one(int T, int E, int S);
+int balance_join_blocks(int S);
 hipError_t launch_balance(const RouteArgs& a, const BalanceArgs& b, hipStream_t s);
 struct BalanceBwdArgs {
   int S, vec_out;

@@ -366,8 +366,9 @@ inline V4 ds_read_tr16(const V4* p) {
 }
 }  // namespace emu
 #define __builtin_amdgcn_ds_read_tr16_b64_v4i16(p) ::emu::ds_read_tr16(p)
-// the hardware exp2, reciprocal and square root, modelled correctly rounded
+// the hardware exp2, log2, reciprocal and square root, modelled correctly rounded
 #define __builtin_amdgcn_exp2f(x) ::exp2f(x)
+#define __builtin_amdgcn_logf(x) ::log2f(x)
 #define __builtin_amdgcn_rcpf(x) (1.0f / (x))
 #define __builtin_amdgcn_sqrtf(x) ::sqrtf(x)
 // (instruction order is the compiler's business)

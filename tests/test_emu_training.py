@@ -101,6 +101,25 @@ def test_balance(run, name):
     assert (pad[:, E:].contiguous().view(torch.uint8) == 0xCD).all()
 
 
+@pytest.mark.parametrize("S,counts", [(1, False), (1, True), (3, False)])
+def test_balance_without_tokens(run, S, counts):
+    """No tokens, and no logits: nothing is read."""
+    E, k = 8, 2
+    c = torch.ones(S, E, dtype=torch.int32) if counts else None
+    seq = torch.zeros(S + 1, dtype=torch.int32) if S > 1 else None
+    nums = [0, 0, E, k, 0, 1, 0, E, S]
+    arrays = [numbers(bits(0.5), bits(0.25)), None, None, None, None if counts else
+              torch.empty(0, dtype=torch.int32), c, seq]
+    outs = [((2,), torch.float32), ((S * E + 2,), torch.float32)]
+    if not counts:
+        outs.append(((S, E), torch.int32))
+    got = run(nums, arrays, outs)
+    assert got[0].tolist() == [0.0, 0.0] and got[1].tolist() == [0.0] * (S * E) + [0.5, 0.5]
+    assert counts or not got[2].any()
+    nums[0] = 1
+    run(nums + [-1, E], arrays + [got[1], None, None], [])
+
+
 PAR = sorted(TC.PARAMS) if FULL else ["odd_f32", "eight_bf16", "unaligned_eight", "master", "forty"]
 
 

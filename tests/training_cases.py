@@ -8,7 +8,7 @@ relative) and half = half a step of the output type:
   exponent's product is rounded to 2^-24 of it; sums of up to 4096 experts are
   added in at most 64 + 6 steps);
 * the log of the exps' sum is off by (R + 80) u + 3 u |lse|;
-* a sum over tokens is fp32 over at most 512 of them, in at most 64 steps, then fp64;
+* a sum over tokens is fp32 over at most 256 of them, in at most 64 + 6 steps, then fp64;
 * the sums of the gradient, one term at a time: every factor's error times the others;
 * an AdamW step: m and v are off by 6 u of their terms (the factors' and three
   roundings), the update by what that makes of it and 10 u, the weight by 3 u more;
@@ -47,6 +47,8 @@ BALANCE = {
     "wide": dict(T=20, E=200, k=20, renorm=False, dtype="bf16"),
     "wider": dict(T=12, E=300, k=5, seq=[0, 5, 12]),
     "thousand": dict(T=9, E=700, k=6, score="sigmoid", dtype="bf16"),
+    "aligned_thousand": dict(T=6, E=528, k=3),
+    "aligned_1104": dict(T=5, E=1104, k=3, dtype="bf16"),
     "most": dict(T=6, E=1100, k=33, renorm=False),
     "twice": dict(T=17, E=12, k=5, repeat=True, renorm=False),
 }
