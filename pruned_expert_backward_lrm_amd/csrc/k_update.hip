@@ -73,10 +73,19 @@ __device__ __forceinline__ void load8(const void* base, int64_t i, int64_t n, bo
       x[j] = BF16 ? bf16_to_f32(((const uint16_t*)base)[i + j]) : ((const float*)base)[i + j];
   }
 }
+// (Stores past the caches' need: what is written is not read again in the call.)
+template <typename V>
+__device__ __forceinline__ void store_stream(void* p, V v) {
+#ifdef LRM_CPU_EMU
+  *reinterpret_cast<V*>(p) = v;
+#else
+  __builtin_nontemporal_store(v, reinterpret_cast<V*>(p));
+#endif
+}
 __device__ __forceinline__ void store8(float* base, int64_t i, int64_t n, bool vec, const float (&x)[8]) {
   if (vec && i + 8 <= n) {
-    *reinterpret_cast<f32x4*>(base + i) = f32x4{x[0], x[1], x[2], x[3]};
-    *reinterpret_cast<f32x4*>(base + i + 4) = f32x4{x[4], x[5], x[6], x[7]};
+    store_stream(base + i, f32x4{x[0], x[1], x[2], x[3]});
+    store_stream(base + i + 4, f32x4{x[4], x[5], x[6], x[7]});
     return;
   }
 #pragma unroll
@@ -90,7 +99,7 @@ __device__ __forceinline__ void store8_hi(uint16_t* base, int64_t i, int64_t n, 
     u32x4 q;
 #pragma unroll
     for (int j = 0; j < 4; ++j) q[j] = (x[2 * j] >> 16) | (x[2 * j + 1] & 0xffff0000u);
-    *reinterpret_cast<u32x4*>(base + i) = q;
+    store_stream(base + i, q);
     return;
   }
 #pragma unroll
@@ -109,7 +118,7 @@ __device__ __forceinline__ u32x2 load_codes(const uint8_t* base, int64_t i, int6
 }
 __device__ __forceinline__ void store_codes(uint8_t* base, int64_t i, int64_t n, bool vec, u32x2 q) {
   if (vec && i + 8 <= n) {
-    *reinterpret_cast<u32x2*>(base + i) = q;
+    store_stream(base + i, q);
     return;
   }
 #pragma unroll
@@ -120,17 +129,30 @@ __device__ __forceinline__ void store_codes(uint8_t* base, int64_t i, int64_t n,
 // Octaves below the shared exponent's: 15 (m) or 31 (v).
 constexpr int kTopM = 15, kTopV = 31;
 
+// Codes are handled two at a time in 16-bit halves: elements 0 and 2, and 1 and 3,
+// of a word (a float's upper half holds sign, exponent and 7 bits of mantissa).
+typedef uint16_t u16x2 __attribute__((ext_vector_type(2)));
+typedef int16_t s16x2 __attribute__((ext_vector_type(2)));
+__device__ __forceinline__ u16x2 halves(uint32_t w) { return __builtin_bit_cast(u16x2, w); }
+__device__ __forceinline__ uint32_t word_of(u16x2 v) { return __builtin_bit_cast(uint32_t, v); }
+// The upper halves of lo and hi.
+__device__ __forceinline__ uint32_t upper_halves(uint32_t lo, uint32_t hi) {
+  return __builtin_amdgcn_perm(hi, lo, 0x07060302u);
+}
+
 template <bool SECOND>
 __device__ __forceinline__ void decode8(u32x2 q, uint32_t e, float (&x)[8]) {
-  const uint32_t low = (e - (SECOND ? kTopV : kTopM)) << 23;
+  const uint32_t low = (e - (SECOND ? kTopV : kTopM)) << 7;
+  const u16x2 base = halves(low * 0x10001u);
 #pragma unroll
-  for (int j = 0; j < 8; ++j) {
-    const uint32_t b = q[j >> 2] >> (8 * (j & 3));
-    const uint32_t c = b & (SECOND ? 255u : 127u);
-    uint32_t u = (c << 20) + low;
-    u = c ? u : 0u;
-    if (!SECOND) u |= (b << 24) & 0x80000000u;
-    x[j] = __uint_as_float(u);
+  for (int p = 0; p < 4; ++p) {
+    const uint32_t b = (p & 1 ? q[p >> 1] >> 8 : q[p >> 1]) & 0x00ff00ffu;
+    const u16x2 c = halves(SECOND ? b : b & 0x007f007fu);
+    const u16x2 some = __builtin_elementwise_min(c, (u16x2)1);  // (code 0 stands for 0)
+    uint32_t t = word_of((c * (uint16_t)16 + base) * some);
+    if (!SECOND) t |= (b << 8) & 0x80008000u;
+    x[4 * (p >> 1) + (p & 1)] = __uint_as_float(t << 16);
+    x[4 * (p >> 1) + (p & 1) + 2] = __uint_as_float(t & 0xffff0000u);
   }
 }
 
@@ -155,17 +177,37 @@ __device__ __forceinline__ uint32_t block_exponent(const float (&x)[8]) {
 template <bool SECOND>
 __device__ __forceinline__ u32x2 encode8(const float (&x)[8], uint32_t e, const uint32_t (&r)[8]) {
   constexpr int top = SECOND ? kTopV : kTopM, most = 8 * top + 7;
-  const int low = (int)((e - top) << 23);
-  u32x2 q = {0u, 0u};
+  const uint32_t low = (e - top) << 23;
+  uint32_t t[8];
 #pragma unroll
   for (int j = 0; j < 8; ++j) {
-    const uint32_t u = __float_as_uint(x[j]), mag = u & 0x7fffffffu;
-    const uint32_t add = ((SECOND ? r[j] >> 16 : r[j] & 0xffffu) << 4) | 8u;
-    int c = ((int)(mag + add) - low) >> 20;
-    const int least = SECOND && mag ? 1 : 0;
-    c = c < least ? least : (c > most ? most : c);
-    if (!SECOND) c |= c ? (int)(u >> 24 & 128u) : 0;
-    q[j >> 2] |= (uint32_t)c << (8 * (j & 3));
+    const uint32_t mag = SECOND ? __float_as_uint(x[j]) : __float_as_uint(x[j]) & 0x7fffffffu;
+    const uint32_t add = SECOND ? (r[j] >> 12 & 0xffff0u) | 8u : ((r[j] & 0xffffu) << 4) | 8u;
+    t[j] = mag + add - low;
+  }
+  u32x2 q;
+#pragma unroll
+  for (int w = 0; w < 2; ++w) {
+    uint32_t c[2];
+#pragma unroll
+    for (int p = 0; p < 2; ++p) {
+      const int j = 4 * w + p;
+      s16x2 v = __builtin_bit_cast(s16x2, upper_halves(t[j], t[j + 2])) >> (int16_t)4;
+      if (SECOND) {  // (what is not 0 stays so)
+        const uint32_t a = __float_as_uint(x[j]), b = __float_as_uint(x[j + 2]);
+        const uint32_t some = (a < 1u ? a : 1u) | (b < 1u ? b : 1u) << 16;
+        v = __builtin_elementwise_max(v, __builtin_bit_cast(s16x2, some));
+      } else {
+        v = __builtin_elementwise_max(v, (s16x2)0);
+      }
+      v = __builtin_elementwise_min(v, (s16x2)(int16_t)most);
+      if (!SECOND) {
+        const uint32_t sign = upper_halves(__float_as_uint(x[j]), __float_as_uint(x[j + 2])) >> 8 & 0x00800080u;
+        v += __builtin_elementwise_min(v, (s16x2)1) * __builtin_bit_cast(s16x2, sign);
+      }
+      c[p] = __builtin_bit_cast(uint32_t, v);
+    }
+    q[w] = c[0] | c[1] << 8;
   }
   return q;
 }
@@ -204,15 +246,15 @@ __global__ __launch_bounds__(256) void k_grad_sumsq(ParamTable t, double* part) 
 
 __global__ __launch_bounds__(256) void k_sumsq_join(int n, const double* part, double* sumsq) {
   __shared__ double lds[4];
-  double v[kUpdateBlocks / 256];
+  double v[kSumBlocks / 256];
 #pragma unroll
-  for (int q = 0; q < kUpdateBlocks / 256; ++q) {
+  for (int q = 0; q < kSumBlocks / 256; ++q) {
     const int i = q * 256 + threadIdx.x;
     v[q] = i < n ? part[i] : 0.0;
   }
   double sum = 0.0;
 #pragma unroll
-  for (int q = 0; q < kUpdateBlocks / 256; ++q) sum += v[q];
+  for (int q = 0; q < kSumBlocks / 256; ++q) sum += v[q];
   sum = wave_sum(sum);
   if (lane_id() == 0) lds[threadIdx.x >> 6] = sum;
   __syncthreads();
@@ -236,13 +278,18 @@ __global__ __launch_bounds__(256) void k_adamw(ParamTable t, AdamArgs a) {
     const double norm = fabs(a.grad_scale) * sqrt(sum);
     if (a.max_norm > 0.0 && norm > a.max_norm) f *= a.max_norm / norm;
   }
-  const int64_t step = a.steps ? a.steps[0] + 1 : a.step;
+  double bias = a.bias;
+  float root = a.root;
+  uint32_t key = a.key;
+  if (a.steps) {
+    const int64_t step = a.steps[0] + 1;
+    bias = -1.0 / expm1((double)step * a.ln1);
+    root = (float)(1.0 / sqrt(-expm1((double)step * a.ln2)));
+    key = step_key(a.seed, (uint64_t)step);
+  }
   const double lr = a.lr_dev ? (double)a.lr_dev[0] : a.lr;
-  const double size = lr / -expm1((double)step * a.ln1);
-  const float root = (float)(1.0 / sqrt(-expm1((double)step * a.ln2)));
-  const uint32_t key = step_key(a.seed, (uint64_t)step);
-  const float c = (float)f, b1 = (float)a.beta1, d1 = (float)(1.0 - a.beta1), b2 = (float)a.beta2,
-              d2 = (float)(1.0 - a.beta2), eps = (float)a.eps;
+  const double size = lr * bias;
+  const float c = (float)f, b1 = a.b1, d1 = a.d1, b2 = a.b2, d2 = a.d2, eps = a.eps;
   constexpr bool RANDOM_P = P == 1;
   const int64_t chunks = t.chunk0[t.n];
   for (int64_t ch = blockIdx.x; ch < chunks; ch += gridDim.x) {
@@ -352,7 +399,7 @@ void adamw_launch(const ParamTable& t, int grid, int eight, const AdamArgs& a, h
     LRM_LAUNCH(grid, 256, 0, s, k_adamw<P, GB, false>)(t, a);
 }
 
-int update_grid(int64_t chunks) { return (int)(chunks < kUpdateBlocks ? chunks : kUpdateBlocks); }
+int grid_of(int64_t chunks, int most) { return (int)(chunks < most ? chunks : most); }
 
 }  // namespace
 
@@ -366,7 +413,7 @@ hipError_t launch_params_table(const TableBatch& b, int first, int count, int n,
 
 hipError_t launch_grad_sumsq(const ParamTable& t, int64_t chunks, int g_bf16, double* part,
                              double* sumsq, hipStream_t s) {
-  const int grid = update_grid(chunks);
+  const int grid = grid_of(chunks, kSumBlocks);
   if (grid > 0) {
     if (g_bf16)
       LRM_LAUNCH(grid, 256, 0, s, k_grad_sumsq<true>)(t, part);
@@ -379,7 +426,10 @@ hipError_t launch_grad_sumsq(const ParamTable& t, int64_t chunks, int g_bf16, do
 
 hipError_t launch_adamw(const ParamTable& t, int64_t chunks, int p, int g_bf16, int eight,
                         const AdamArgs& a, int64_t* steps, hipStream_t s) {
-  const int grid = update_grid(chunks);
+  // Blocks that end after one chunk stream best (bf16 weights with masters, 151 M:
+  // 945 us with the norm, 997 with 16384 blocks, 1046 with 4096); with 8-bit moments the
+  // start of a block weighs more (567, 533, 559).
+  const int grid = grid_of(chunks, eight ? 1 << 14 : 1 << 20);
   if (grid > 0) {
     if (p == 0 && !g_bf16) adamw_launch<0, false>(t, grid, eight, a, s);
     else if (p == 0) adamw_launch<0, true>(t, grid, eight, a, s);
@@ -397,7 +447,7 @@ hipError_t launch_moment_read(int64_t n, int second, const uint8_t* codes, const
   if (n <= 0) return hipSuccess;
   const bool vec = (reinterpret_cast<uintptr_t>(codes) & 7u) == 0 && (reinterpret_cast<uintptr_t>(out) & 15u) == 0;
   const int64_t blocks = (n + 2047) / 2048;
-  const int grid = (int)(blocks < 8 * kUpdateBlocks ? blocks : 8 * kUpdateBlocks);
+  const int grid = grid_of(blocks, 1 << 14);
   if (second && bf16)
     LRM_LAUNCH(grid, 256, 0, s, k_moment_read<true, true>)(n, codes, exps, vec, out);
   else if (second)

@@ -41,10 +41,14 @@ struct TableBatch {
 };
 
 struct AdamArgs {
-  double lr, eps, grad_scale, max_norm;
-  double beta1, beta2;
+  double lr, grad_scale, max_norm;
+  float b1, d1, b2, d2, eps;  // betas and one less them
+  // of a step that the host counts: 1 / (1 - beta1^t), 1 / sqrt(1 - beta2^t), the key
+  double bias;
+  float root;
+  uint32_t key;
+  // of one that the GPU counts
   double ln1, ln2;  // logarithms of the betas
-  int64_t step;
   uint64_t seed;
   const double* sumsq;
   int n_sumsq;
@@ -69,7 +73,7 @@ __host__ __device__ inline uint32_t step_key(uint64_t seed, uint64_t step) {
   return mix32((k ^ (uint32_t)(step >> 32)) + kGold);
 }
 
-constexpr int kUpdateBlocks = 2048;  // persistent blocks, at most
+constexpr int kSumBlocks = 1024;  // persistent blocks, at most
 
 hipError_t launch_params_table(const TableBatch& b, int first, int count, int n, int64_t chunks,
                                void* table, hipStream_t s);

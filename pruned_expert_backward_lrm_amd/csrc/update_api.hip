@@ -93,7 +93,7 @@ lrm_status lrm_params_table(lrm_params* ps, size_t table_bytes, void* stream) {
 size_t lrm_sumsq_workspace_size(const lrm_params* ps) {
   if (check_params(ps, false) != LRM_OK) return 0;
   Carve c(nullptr);
-  c.take<double>(kUpdateBlocks);
+  c.take<double>(kSumBlocks);
   return c.size();
 }
 
@@ -102,7 +102,7 @@ lrm_status lrm_grad_sumsq(const lrm_params* ps, double* sumsq, void* ws, size_t 
   LRM_TRY(check_params(ps, false));
   if (!sumsq) return LRM_ERR_NULL;
   if (!on(sumsq, 8)) return LRM_ERR_ALIGN;
-  if (!ws || ws_bytes < kUpdateBlocks * sizeof(double)) return LRM_ERR_WORKSPACE;
+  if (!ws || ws_bytes < kSumBlocks * sizeof(double)) return LRM_ERR_WORKSPACE;
   if (!on(ws, 8)) return LRM_ERR_ALIGN;
   if (ps->chunks < 0) return LRM_ERR_SHAPE;
   LRM_TRY_HIP(launch_grad_sumsq(table_of(ps), ps->chunks, ps->g_dtype == LRM_BF16,
@@ -125,10 +125,15 @@ lrm_status lrm_adamw(const lrm_params* ps, const lrm_adamw_step* a, void* stream
   if (a->max_norm > 0.0 && !a->sumsq) return LRM_ERR_NULL;
   if (!on(a->sumsq, 8) || !on(a->lr_dev, 4) || !on(a->steps, 8)) return LRM_ERR_ALIGN;
   AdamArgs g{};
-  g.lr = a->lr; g.eps = a->eps; g.grad_scale = a->grad_scale; g.max_norm = a->max_norm;
-  g.beta1 = a->beta1; g.beta2 = a->beta2;
+  g.lr = a->lr; g.grad_scale = a->grad_scale; g.max_norm = a->max_norm;
+  g.b1 = (float)a->beta1; g.d1 = (float)(1.0 - a->beta1);
+  g.b2 = (float)a->beta2; g.d2 = (float)(1.0 - a->beta2);
+  g.eps = (float)a->eps;
   g.ln1 = std::log(a->beta1); g.ln2 = std::log(a->beta2);
-  g.step = a->step; g.seed = a->seed; g.sumsq = a->sumsq; g.n_sumsq = a->n_sumsq;
+  g.bias = -1.0 / std::expm1((double)a->step * g.ln1);
+  g.root = (float)(1.0 / std::sqrt(-std::expm1((double)a->step * g.ln2)));
+  g.key = step_key(a->seed, (uint64_t)a->step);
+  g.seed = a->seed; g.sumsq = a->sumsq; g.n_sumsq = a->n_sumsq;
   g.lr_dev = a->lr_dev; g.steps = a->steps;
   const int p = ps->masters ? 2 : (ps->p_dtype == LRM_BF16 ? 1 : 0);
   LRM_TRY_HIP(launch_adamw(table_of(ps), ps->chunks, p, ps->g_dtype == LRM_BF16,
