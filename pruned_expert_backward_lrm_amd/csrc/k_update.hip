@@ -4,8 +4,8 @@
 //
 // All are bound by memory: one pass over every array, each element read and
 // written once.  The tensors of a list are cut into chunks of 2048 elements, 8
-// neighbours a thread; persistent blocks take the chunks in turn and find a
-// chunk's tensor in the table by bisection (wave-uniform, so scalar loads).
+// neighbours a thread; blocks take the chunks in turn and find a chunk's
+// tensor in the table.
 //
 // 8-bit moments (see lrm.h): 4 lanes hold a block of 32, whose largest magnitude
 // they find with two quad permutations.  The shared exponent x is the largest's,
@@ -30,18 +30,21 @@ namespace {
 #define LRM_CONST __attribute__((address_space(4)))
 #endif
 
-// The tensor that holds chunk c: the last one that starts at or before it.
-__device__ __forceinline__ ParamEntry tensor_of(const ParamTable& t, int64_t c) {
-  const LRM_CONST int64_t* chunk0 = (const LRM_CONST int64_t*)t.chunk0;
-  int lo = 0, hi = t.n;
-  while (hi - lo > 1) {
-    const int mid = (lo + hi) >> 1;
-    if (chunk0[mid] <= c) lo = mid;
-    else hi = mid;
+// The tensor that holds chunk c: the last one that starts at or before it.  64 of them
+// are looked at at a time.  Returns the chunk behind its last one.
+__device__ __forceinline__ int64_t tensor_of(const ParamTable& t, int64_t c, ParamEntry* out) {
+  int lo = 0, n = t.n;
+  while (n > 1) {
+    const int step = (n + kWave - 1) / kWave, at = lane_id() * step;
+    const bool before = at < n && t.chunk0[lo + (at < n ? at : 0)] <= c;
+    const int k = (__popcll(__ballot(before)) - 1) * step;  // (the first one is)
+    lo += k;
+    n = n - k < step ? n - k : step;
   }
   const LRM_CONST ParamEntry* e = (const LRM_CONST ParamEntry*)t.entry + lo;
-  return ParamEntry{e->p, e->g, e->master, e->m, e->v, e->m_exp, e->v_exp, e->n,
+  *out = ParamEntry{e->p, e->g, e->master, e->m, e->v, e->m_exp, e->v_exp, e->n,
                     e->chunk0, e->block0, e->lr, e->decay, e->vec, 0};
+  return e->chunk0 + (e->n + kChunk - 1) / kChunk;
 }
 
 // Eight neighbours from element i (those at or past n: 0).
@@ -73,7 +76,8 @@ __device__ __forceinline__ void load8(const void* base, int64_t i, int64_t n, bo
       x[j] = BF16 ? bf16_to_f32(((const uint16_t*)base)[i + j]) : ((const float*)base)[i + j];
   }
 }
-// (Stores past the caches' need: what is written is not read again in the call.)
+// Past the caches: the arrays are larger, and lines left to be written back slow the
+// kernel that comes next (the sum of squares after the moments were read: 114 us, 76 so).
 template <typename V>
 __device__ __forceinline__ void store_stream(void* p, V v) {
 #ifdef LRM_CPU_EMU
@@ -231,8 +235,10 @@ __global__ __launch_bounds__(256) void k_grad_sumsq(ParamTable t, double* part) 
   __shared__ double lds[4];
   const int64_t chunks = t.chunk0[t.n];
   double sum = 0.0;
+  ParamEntry e;
+  int64_t end = 0;  // of e's chunks
   for (int64_t c = blockIdx.x; c < chunks; c += gridDim.x) {
-    const ParamEntry e = tensor_of(t, c);
+    if (c >= end) end = tensor_of(t, c, &e);
     float x[8];
     load8<BF16>(e.g, (c - e.chunk0) * kChunk + threadIdx.x * 8, e.n, e.vec != 0, x);
 #pragma unroll
@@ -292,8 +298,10 @@ __global__ __launch_bounds__(256) void k_adamw(ParamTable t, AdamArgs a) {
   const float c = (float)f, b1 = a.b1, d1 = a.d1, b2 = a.b2, d2 = a.d2, eps = a.eps;
   constexpr bool RANDOM_P = P == 1;
   const int64_t chunks = t.chunk0[t.n];
+  ParamEntry e;
+  int64_t end = 0;  // of e's chunks
   for (int64_t ch = blockIdx.x; ch < chunks; ch += gridDim.x) {
-    const ParamEntry e = tensor_of(t, ch);
+    if (ch >= end) end = tensor_of(t, ch, &e);
     const int64_t i = (ch - e.chunk0) * kChunk + threadIdx.x * 8, n = e.n;
     const bool vec = e.vec != 0;
     const float up = (float)(size * (double)e.lr), down = (float)(lr * (double)e.lr * (double)e.decay);
