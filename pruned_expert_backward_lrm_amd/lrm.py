@@ -822,8 +822,25 @@ def lrm_pair_grad(g: PairGrad, outputs, ws=None, stream=None):
 
 
 # ---------------------------------------------- update of the parameters
-def _bytes(t):
-    return t.data_ptr(), t.data_ptr() + t.numel() * t.element_size()
+def _apart(spans):
+    """Refuses arrays that share memory, where one of them is written.  spans:
+    (name, addresses, bytes, written) a list of arrays."""
+    lo = np.concatenate([p for _, p, _, _ in spans])
+    hi = lo + np.concatenate([n for _, _, n, _ in spans])
+    w = np.concatenate([np.full(len(p), x) for _, p, _, x in spans])
+    at = np.nonzero(hi > lo)[0]
+    at = at[np.argsort(lo[at], kind="stable")]
+    lo, hi, w = lo[at], hi[at], w[at]
+    # the end of what starts before: of everything, and of what is written
+    end = np.concatenate([[0], np.maximum.accumulate(hi)[:-1]]) if len(hi) else hi
+    end_w = np.concatenate([[0], np.maximum.accumulate(np.where(w, hi, 0))[:-1]]) if len(hi) else hi
+    bad = np.nonzero(lo < np.where(w, end, end_w))[0]
+    if len(bad):
+        i = int(at[bad[0]])
+        for name, p, _, _ in spans:
+            if i < len(p):
+                raise ValueError(f"{name}[{i}] shares memory with another tensor of the list")
+            i -= len(p)
 
 
 class Params:
@@ -841,38 +858,35 @@ class Params:
         g = list(g)
         n = len(g)
         lists = {"p": p, "master": master, "m": m, "v": v, "m_exp": m_exp, "v_exp": v_exp}
-        lists = {k: list(x) for k, x in lists.items() if x is not None}
+        lists = {"g": g, **{k: list(x) for k, x in lists.items() if x is not None}}
         if not g:
             raise ValueError("at least one tensor is wanted")
         self.device = g[0].device
         eight = "m_exp" in lists
+        moment = torch.uint8 if eight else torch.float32
         want = {"g": g[0].dtype, "p": lists["p"][0].dtype if lists.get("p") else None,
-                "master": torch.float32, "m": torch.uint8 if eight else torch.float32,
-                "v": torch.uint8 if eight else torch.float32, "m_exp": torch.uint8,
+                "master": torch.float32, "m": moment, "v": moment, "m_exp": torch.uint8,
                 "v_exp": torch.uint8}
-        written = []
-        for name, ts in [("g", g), *lists.items()]:
+        counts = [t.numel() for t in g]
+        blocks = [(x + 31) // 32 for x in counts]
+        self.param = (lrm_param * n)()
+        rows = np.frombuffer(self.param, dtype=np.dtype(lrm_param))
+        rows["n"] = counts
+        spans = []
+        for name, ts in lists.items():
             if len(ts) != n:
                 raise ValueError(f"{name} must have {n} tensors, as g has")
-            for i, t in enumerate(ts):
-                size = g[i].numel()
-                size = (size + 31) // 32 if name.endswith("_exp") else size
-                if t.dtype != want[name] or t.numel() != size or not t.is_contiguous() or \
-                        t.device != self.device:
-                    raise ValueError(f"{name}[{i}] must be a contiguous {want[name]} tensor of "
-                                     f"{size} elements on {self.device}")
-                if size:
-                    written.append((*_bytes(t), name != "g", f"{name}[{i}]"))
+            dt, sizes = want[name], blocks if name.endswith("_exp") else counts
+            for i, (t, x) in enumerate(zip(ts, sizes)):
+                if t.dtype is not dt or t.numel() != x or t.device != self.device or \
+                        not t.is_contiguous():
+                    raise ValueError(f"{name}[{i}] must be a contiguous {dt} tensor of {x} elements "
+                                     f"on {self.device}")
+            at = np.array([t.data_ptr() for t in ts], np.int64)
+            rows[name] = at
+            spans.append((name, at, np.array(sizes, np.int64) * ts[0].element_size(), name != "g"))
         # (what is written lies apart from everything; gradients may share memory)
-        written.sort()
-        end, last, end_w, last_w = -1, "", -1, ""
-        for lo, hi, w, name in written:
-            if lo < (end if w else end_w):
-                raise ValueError(f"{name} shares memory with {last if w else last_w}")
-            if hi > end:
-                end, last = hi, name
-            if w and hi > end_w:
-                end_w, last_w = hi, name
+        _apart(spans)
 
         def each(x, name):
             x = [float(y) for y in x] if isinstance(x, (list, tuple)) else [float(x)] * n
@@ -880,14 +894,9 @@ class Params:
                 raise ValueError(f"{name} must be a number or {n} of them")
             return x
 
-        lr, weight_decay = each(lr, "lr"), each(weight_decay, "weight_decay")
-        self.param = (lrm_param * n)()
-        for i, q in enumerate(self.param):
-            q.g, q.n, q.lr, q.weight_decay = _ptr(g[i]), g[i].numel(), lr[i], weight_decay[i]
-            for name, ts in lists.items():
-                setattr(q, name, _ptr(ts[i]))
+        rows["lr"], rows["weight_decay"] = each(lr, "lr"), each(weight_decay, "weight_decay")
         self.n = n
-        self.keep = [g, lists]
+        self.keep = lists
         self.table = _scratch(int(_lib.lrm_params_table_size(n)), self.device, stream)
         self.c = lrm_params(n, dtype_code(lists["p"][0]) if lists.get("p") else LRM_F32,
                             dtype_code(g[0]), LRM_MOMENTS_8BIT if eight else LRM_MOMENTS_F32,
