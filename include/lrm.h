@@ -749,7 +749,8 @@ typedef struct lrm_params {
   int32_t _pad;
   const lrm_param* param; /* HOST [n], read during the call */
   void* table;        /* device, lrm_params_table_size(n) bytes, 256-byte aligned */
-  int64_t chunks;     /* sum of (param[i].n + 2047) / 2048, as lrm_params_table sets it */
+  int64_t chunks;     /* sum of (param[i].n + 2047) / 2048, as lrm_params_table sets it
+                         (LRM_ERR_SHAPE where another call finds another) */
 } lrm_params;
 
 /* Describes the tensors to the GPU: checks them, writes the table (kernels on the
@@ -787,13 +788,13 @@ size_t lrm_sumsq_workspace_size(const lrm_params* ps);
 typedef struct lrm_adamw_step {
   double lr;            /* finite, >= 0 */
   double beta1, beta2;  /* [0, 1) */
-  double eps;           /* finite, > 0 */
+  double eps;           /* finite, 1e-30 at least */
   double grad_scale;    /* finite */
   double max_norm;      /* finite, > 0; 0: no clipping */
   int64_t step;         /* t, 1..2^53 (not read where steps is given) */
   uint64_t seed;
   const double* sumsq;  /* device [n_sumsq], or NULL (max_norm 0) */
-  int32_t n_sumsq;      /* 1..1024 (0: sumsq NULL) */
+  int32_t n_sumsq;      /* 1..64 (0: sumsq NULL) */
   int32_t _pad;
   const float* lr_dev;  /* device [1], read in place of lr (schedules under a captured
                            graph), or NULL */

@@ -515,8 +515,6 @@ __global__ __launch_bounds__(NV > 8 ? kWave : kThreads) void k_balance_bwd(Route
   float* row = lds + slot * LPT * NV;
   const float db = (b.dloss ? b.dloss[0] : 1.f) * b.saved[(int64_t)b.S * a.E];
   const float dz = (b.dloss ? b.dloss[1] : 1.f) * b.saved[(int64_t)b.S * a.E + 1];
-  float w[NV];
-  int s = -1;        // the sequence whose row is in w
   bool inside = true;
   const int64_t r0 = (int64_t)blockIdx.x * b.chunk;
   const int64_t r1 = at_most(r0 + b.chunk, a.T);
@@ -537,6 +535,9 @@ __global__ __launch_bounds__(NV > 8 ? kWave : kThreads) void k_balance_bwd(Route
     e1 = b.expert[next_slot];
     v1 = b.dweight[next_slot];
   }
+  float w[NV];
+  int s = at;        // the sequence whose row is in w
+  numbers_row<LPT, NV, VEC>(b.saved + (int64_t)s * a.E, i, a.E, w);
   for (int r = slot; r - slot < n; r += tpb, out += tpb * b.ldd) {
     const int64_t t = r0 + r;
     const bool in = r < n;

@@ -13,7 +13,8 @@ namespace {
 bool on(const void* p, size_t bytes) { return reinterpret_cast<uintptr_t>(p) % bytes == 0; }
 
 // The descriptor and its tensors; step: they are to be updated, not only read.
-lrm_status check_params(const lrm_params* ps, bool step) {
+// total: their chunks.
+lrm_status check_params(const lrm_params* ps, bool step, int64_t* total) {
   if (!ps) return LRM_ERR_NULL;
   if (ps->n < 0 || ps->n > kMaxTensors) return LRM_ERR_SHAPE;
   if ((ps->p_dtype != LRM_F32 && ps->p_dtype != LRM_BF16) ||
@@ -25,9 +26,11 @@ lrm_status check_params(const lrm_params* ps, bool step) {
   if (!ps->table || (ps->n > 0 && !ps->param)) return LRM_ERR_NULL;
   if (!on(ps->table, kAlign)) return LRM_ERR_ALIGN;
   const bool eight = ps->moments == LRM_MOMENTS_8BIT;
+  int64_t chunks = 0;
   for (int i = 0; i < ps->n; ++i) {
     const lrm_param& q = ps->param[i];
     if (q.n < 0 || q.n > (1ll << 40)) return LRM_ERR_SHAPE;
+    chunks += (q.n + kChunk - 1) / kChunk;
     if (!std::isfinite(q.lr) || q.lr < 0.f || !std::isfinite(q.weight_decay)) return LRM_ERR_UNSUPPORTED;
     if (q.n == 0) continue;
     if (!q.g) return LRM_ERR_NULL;
@@ -40,6 +43,7 @@ lrm_status check_params(const lrm_params* ps, bool step) {
     if (!on(q.p, esize(ps->p_dtype)) || !on(q.master, 4)) return LRM_ERR_ALIGN;
     if (!eight && (!on(q.m, 4) || !on(q.v, 4))) return LRM_ERR_ALIGN;
   }
+  *total = chunks;
   return LRM_OK;
 }
 
@@ -63,11 +67,10 @@ size_t lrm_params_table_size(int32_t n) {
 }
 
 lrm_status lrm_params_table(lrm_params* ps, size_t table_bytes, void* stream) {
-  LRM_TRY(check_params(ps, false));
+  int64_t chunks = 0, blocks = 0;
+  LRM_TRY(check_params(ps, false, &chunks));
   if (table_bytes < lrm_params_table_size(ps->n)) return LRM_ERR_WORKSPACE;
   const bool eight = ps->moments == LRM_MOMENTS_8BIT;
-  int64_t chunks = 0, blocks = 0;
-  for (int i = 0; i < ps->n; ++i) chunks += (ps->param[i].n + kChunk - 1) / kChunk;
   ps->chunks = chunks;
   chunks = 0;
   for (int first = 0; first == 0 || first < ps->n; first += kTableBatch) {
@@ -91,7 +94,8 @@ lrm_status lrm_params_table(lrm_params* ps, size_t table_bytes, void* stream) {
 }
 
 size_t lrm_sumsq_workspace_size(const lrm_params* ps) {
-  if (check_params(ps, false) != LRM_OK) return 0;
+  int64_t chunks;
+  if (check_params(ps, false, &chunks) != LRM_OK) return 0;
   Carve c(nullptr);
   c.take<double>(kSumBlocks);
   return c.size();
@@ -99,28 +103,30 @@ size_t lrm_sumsq_workspace_size(const lrm_params* ps) {
 
 lrm_status lrm_grad_sumsq(const lrm_params* ps, double* sumsq, void* ws, size_t ws_bytes,
                           void* stream) {
-  LRM_TRY(check_params(ps, false));
+  int64_t chunks;
+  LRM_TRY(check_params(ps, false, &chunks));
   if (!sumsq) return LRM_ERR_NULL;
   if (!on(sumsq, 8)) return LRM_ERR_ALIGN;
   if (!ws || ws_bytes < kSumBlocks * sizeof(double)) return LRM_ERR_WORKSPACE;
   if (!on(ws, 8)) return LRM_ERR_ALIGN;
-  if (ps->chunks < 0) return LRM_ERR_SHAPE;
+  if (ps->chunks != chunks) return LRM_ERR_SHAPE;  // (no table of these tensors)
   LRM_TRY_HIP(launch_grad_sumsq(table_of(ps), ps->chunks, ps->g_dtype == LRM_BF16,
                                 static_cast<double*>(ws), sumsq, as_stream(stream)));
   return LRM_OK;
 }
 
 lrm_status lrm_adamw(const lrm_params* ps, const lrm_adamw_step* a, void* stream) {
-  LRM_TRY(check_params(ps, true));
+  int64_t chunks;
+  LRM_TRY(check_params(ps, true, &chunks));
   if (!a) return LRM_ERR_NULL;
-  if (ps->chunks < 0) return LRM_ERR_SHAPE;
-  if (!std::isfinite(a->lr) || a->lr < 0.0 || !std::isfinite(a->eps) || !(a->eps > 0.0) ||
+  if (ps->chunks != chunks) return LRM_ERR_SHAPE;  // (no table of these tensors)
+  if (!std::isfinite(a->lr) || a->lr < 0.0 || !std::isfinite(a->eps) || !(a->eps >= 1e-30) ||
       !std::isfinite(a->grad_scale) || !std::isfinite(a->max_norm) || a->max_norm < 0.0)
     return LRM_ERR_UNSUPPORTED;
   if (!(a->beta1 >= 0.0 && a->beta1 < 1.0) || !(a->beta2 >= 0.0 && a->beta2 < 1.0))
     return LRM_ERR_UNSUPPORTED;
   if (!a->steps && (a->step < 1 || a->step > (1ll << 53))) return LRM_ERR_SHAPE;
-  if (a->n_sumsq < 0 || a->n_sumsq > 1024 || (a->n_sumsq > 0) != (a->sumsq != nullptr))
+  if (a->n_sumsq < 0 || a->n_sumsq > 64 || (a->n_sumsq > 0) != (a->sumsq != nullptr))
     return LRM_ERR_SHAPE;
   if (a->max_norm > 0.0 && !a->sumsq) return LRM_ERR_NULL;
   if (!on(a->sumsq, 8) || !on(a->lr_dev, 4) || !on(a->steps, 8)) return LRM_ERR_ALIGN;

@@ -234,6 +234,11 @@ def test_params_call_refusals():
     assert lib.lrm_grad_sumsq(ref(ps), P, None, big, None) == 7
     assert lib.lrm_grad_sumsq(ref(ps), P, P, 8, None) == 7
     assert lib.lrm_grad_sumsq(ref(ps), P, P + 4, big, None) == 5
+    ps.chunks = 2  # another table's
+    assert lib.lrm_grad_sumsq(ref(ps), P, P, big, None) == 2
+    a = step()
+    assert lib.lrm_adamw(ref(ps), ref(a), None) == 2
+    ps.chunks = 1
     # gradients alone: to be read, not updated
     only = params(p=None, m=None, v=None)
     assert lib.lrm_sumsq_workspace_size(ref(only)) > 0
@@ -243,11 +248,11 @@ def test_params_call_refusals():
 
 
 STEP_REFUSALS = [
-    (dict(lr=-0.1), 10), (dict(lr=float("nan")), 10), (dict(eps=0.0), 10), (dict(eps=float("inf")), 10),
+    (dict(lr=-0.1), 10), (dict(lr=float("nan")), 10), (dict(eps=0.0), 10), (dict(eps=1e-31), 10), (dict(eps=float("inf")), 10),
     (dict(beta1=1.0), 10), (dict(beta1=-0.1), 10), (dict(beta2=1.5), 10), (dict(beta2=float("nan")), 10),
     (dict(grad_scale=float("inf")), 10), (dict(max_norm=-1.0, sumsq=P, n_sumsq=1), 10),
     (dict(step=0), 2), (dict(step=(1 << 53) + 1), 2), (dict(n_sumsq=1), 2), (dict(sumsq=P), 2),
-    (dict(sumsq=P, n_sumsq=1025), 2), (dict(max_norm=1.0), 1), (dict(sumsq=P + 4, n_sumsq=1), 5),
+    (dict(sumsq=P, n_sumsq=65), 2), (dict(max_norm=1.0), 1), (dict(sumsq=P + 4, n_sumsq=1), 5),
     (dict(lr_dev=P + 2), 5), (dict(steps=P + 4), 5),
 ]
 
