@@ -33,6 +33,11 @@ the workload's real selection, and the optimal peak against fixed ownership.
 the workload's own quotas with the same pair budget spent by the quota
 controller (water-filling caps, lrm_quota_waterfill).
 
+`--update` instead prints one JSON line on the step that the call's weight
+gradients go into: their norm and an AdamW update of the layer's weights
+(lrm_grad_sumsq, lrm_adamw), with fp32 moments (and fp32 masters of bf16
+weights) and with 8-bit moments, beside the fused call.
+
 `--sweep` instead prints one JSON line of the keep-ratio sweep: the fused call
 with every quota at floor(r * n_e) for r in 0.1, 0.25, 0.5, 0.75, 1.0 (all
 projections alike), and the unpruned call, on the chosen workload.
@@ -94,6 +99,8 @@ def parse():
                     help="compare the workload's quotas with water-filling quotas of equal budget")
     ap.add_argument("--redistribute", action="store_true",
                     help="time the redistribution onto replicas instead of the bench line")
+    ap.add_argument("--update", action="store_true",
+                    help="time the gradients' norm and the AdamW step of the layer's weights")
     ap.add_argument("--sweep", action="store_true",
                     help="keep-ratio sweep (quota = floor(r n_e)) instead of the bench line")
     ap.add_argument("--summarize-trace", metavar="DIR",
@@ -749,6 +756,41 @@ def redistribution(L, p, dev, steps, warmup, G=8, hot=16):
             "steps": steps, "warmup": warmup}
 
 
+def update(L, p, dev, dw_bf16, steps, warmup):
+    """The gradients' norm and the AdamW step on the layer's weights (which it
+    changes), with clipping and the step count on the GPU: ms and GB/s of what
+    each has to read and write, beside the ms of the fused call."""
+    W = Workload(L, p, dev, dw_bf16)
+    t_bwd = time_loop(W.step, steps, warmup)
+    names = ["W"] if p["kind"] == "linear" else ["W_gate", "W_up", "W_down"]
+    w, g = [p[k] for k in names], [W.out["d" + k] for k in names]
+    n, ge, we = sum(x.numel() for x in w), g[0].element_size(), w[0].element_size()
+    sumsq = torch.empty(1, dtype=torch.float64, device=dev)
+    res = {}
+    for name, eight in (("moments_f32", False), ("moments_8bit", True)):
+        dt = torch.uint8 if eight else torch.float32
+        kw = {k: [torch.zeros(x.shape, dtype=dt, device=dev) for x in w] for k in "mv"}
+        if eight:
+            kw.update({k: [torch.zeros((x.numel() + 31) // 32, dtype=dt, device=dev) for x in w]
+                       for k in ("m_exp", "v_exp")})
+        masters = we == 2 and not eight
+        ps = L.Params(g=g, p=w, master=[x.float() for x in w] if masters else None,
+                      weight_decay=0.1, **kw)
+        opt = L.AdamW(lr=1e-5, seed=1, max_norm=1.0, sumsq=sumsq,
+                      steps=torch.zeros(1, dtype=torch.int64, device=dev))
+        ws = torch.empty(L.lrm_sumsq_workspace_size(ps), dtype=torch.uint8, device=dev)
+        t_norm = time_loop(lambda: L.lrm_grad_sumsq(ps, sumsq, ws=ws), steps, warmup)
+        t_step = time_loop(lambda: L.lrm_adamw(ps, opt), steps, warmup)
+        per = ge + (we + 8 if masters else 2 * we) + (4 * (1 + 1 / 32) if eight else 16)
+        res[name] = {"masters": masters, "norm_ms": round(t_norm * 1e3, 4),
+                     "norm_gbs": round(n * ge / t_norm / 1e9, 1), "step_ms": round(t_step * 1e3, 4),
+                     "step_gbs": round(n * per / t_step / 1e9, 1)}
+        del ps, kw, opt
+    return {"metric": "AdamW update of the layer's weights", "weights": n, "grad_dtype":
+            "bf16" if ge == 2 else "f32", "weight_dtype": p["dtype"],
+            "backward_ms": round(t_bwd * 1e3, 4), "steps": steps, "warmup": warmup, **res}
+
+
 def time_loop(fn, steps, warmup):
     for _ in range(warmup):
         fn()
@@ -830,6 +872,12 @@ def main():
     if a.redistribute:
         log("bench: redistribution onto replicas")
         line = redistribution(L, p, dev, a.steps, a.warmup)
+        line["config"] = {"workload": synth.CONFIGS[a.config]["name"]}
+        print(json.dumps(line), flush=True)
+        return
+    if a.update:
+        log("bench: norm and AdamW step of the layer's weights")
+        line = update(L, p, dev, a.dw_bf16, a.steps, a.warmup)
         line["config"] = {"workload": synth.CONFIGS[a.config]["name"]}
         print(json.dumps(line), flush=True)
         return

@@ -496,3 +496,25 @@ def test_two_streams_at_once(L):  # noqa: F811
     for (c, b, q, ps, lists, s), (got, _) in zip(runs, outs):
         TC.check_balance(c, got[0].cpu(), got[1].cpu(), got[2].cpu())
         TC.check_adamw(q, back(q, lists))
+
+
+@pytest.mark.parametrize("kind", ["linear", "swiglu"])
+def test_benchmark_of_the_update(L, kind, root):  # noqa: F811
+    import sys
+    sys.path.insert(0, root)
+    import bench
+    from pruned_expert_backward_lrm_amd import synth
+    if kind == "linear":
+        p = synth.make_linear(256, 4, 2, 64, 96, dtype="bf16", seed=3)
+        names = ["W"]
+    else:
+        p = synth.make_swiglu(256, 4, 2, 64, 96, dtype="bf16", seed=3)
+        names = ["W_gate", "W_up", "W_down"]
+    p = {k: v.to(DEV) if isinstance(v, torch.Tensor) else v for k, v in p.items()}
+    before = [p[k].clone() for k in names]
+    line = bench.update(L, p, DEV, False, 2, 1)
+    assert line["weights"] == sum(w.numel() for w in before)
+    for key, masters in (("moments_f32", True), ("moments_8bit", False)):
+        assert line[key]["masters"] is masters and line[key]["step_ms"] > 0
+    for k, w in zip(names, before):
+        assert torch.isfinite(p[k]).all() and not torch.equal(p[k], w)
