@@ -269,32 +269,36 @@ __global__ __launch_bounds__(256) void k_sumsq_join(int n, const double* part, d
 
 // ------------------------------------------------------------------ AdamW
 __device__ __forceinline__ double total_of(const double* sumsq, int n) {
+  const LRM_CONST double* x = (const LRM_CONST double*)sumsq;
   double s = 0.0;
-  for (int i = 0; i < n; ++i) s += sumsq[i];
+  for (int i = 0; i < n; ++i) s += x[i];
   return s;
 }
 __device__ __forceinline__ bool finite64(double x) { return x - x == 0.0; }
 
 template <int P, bool GB, bool EIGHT>
 __global__ __launch_bounds__(256) void k_adamw(ParamTable t, AdamArgs a) {
+  // (Every block starts with this: uniform loads are scalar, and what becomes a
+  // factor in fp32 is formed with few fp64 instructions.)
   double f = a.grad_scale;
   if (a.sumsq) {
     const double sum = total_of(a.sumsq, a.n_sumsq);
     if (!finite64(sum)) return;
-    const double norm = fabs(a.grad_scale) * sqrt(sum);
-    if (a.max_norm > 0.0 && norm > a.max_norm) f *= a.max_norm / norm;
+    // max_norm / norm: 1 / sqrt(sum) from the hardware's estimate (2^-24) and a Newton step
+    const double r = __builtin_amdgcn_rsq(sum);
+    const double over = a.over * fma(r, fma(-0.5 * sum * r, r, 0.5), r);
+    if (sum > 0.0 && over < 1.0) f *= over;  // (over: infinite without clipping)
   }
-  double bias = a.bias;
-  float root = a.root;
+  float bias = a.bias, root = a.root;
   uint32_t key = a.key;
   if (a.steps) {
-    const int64_t step = a.steps[0] + 1;
-    bias = -1.0 / expm1((double)step * a.ln1);
-    root = (float)(1.0 / sqrt(-expm1((double)step * a.ln2)));
+    const int64_t step = *(const LRM_CONST int64_t*)a.steps + 1;
+    bias = -1.f / expm1f((float)((double)step * a.ln1));
+    root = 1.f / __builtin_amdgcn_sqrtf(-expm1f((float)((double)step * a.ln2)));
     key = step_key(a.seed, (uint64_t)step);
   }
-  const double lr = a.lr_dev ? (double)a.lr_dev[0] : a.lr;
-  const double size = lr * bias;
+  const float lr = a.lr_dev ? *(const LRM_CONST float*)a.lr_dev : a.lr;
+  const float size = lr * bias;
   const float c = (float)f, b1 = a.b1, d1 = a.d1, b2 = a.b2, d2 = a.d2, eps = a.eps;
   constexpr bool RANDOM_P = P == 1;
   const int64_t chunks = t.chunk0[t.n];
@@ -304,7 +308,7 @@ __global__ __launch_bounds__(256) void k_adamw(ParamTable t, AdamArgs a) {
     if (ch >= end) end = tensor_of(t, ch, &e);
     const int64_t i = (ch - e.chunk0) * kChunk + threadIdx.x * 8, n = e.n;
     const bool vec = e.vec != 0;
-    const float up = (float)(size * (double)e.lr), down = (float)(lr * (double)e.lr * (double)e.decay);
+    const float up = size * e.lr, down = lr * e.lr * e.decay;
     float g[8], w[8], m[8], v[8];
     const int64_t blk = i >> 5, blkc = i < n ? blk : 0;
     load8<GB>(e.g, i, n, vec, g);
@@ -434,10 +438,14 @@ hipError_t launch_grad_sumsq(const ParamTable& t, int64_t chunks, int g_bf16, do
 
 hipError_t launch_adamw(const ParamTable& t, int64_t chunks, int p, int g_bf16, int eight,
                         const AdamArgs& a, int64_t* steps, hipStream_t s) {
-  // Blocks that end after one chunk stream best (bf16 weights with masters, 151 M:
-  // 945 us with the norm, 997 with 16384 blocks, 1046 with 4096); with 8-bit moments the
-  // start of a block weighs more (567, 533, 559).
-  const int grid = grid_of(chunks, eight ? 1 << 14 : 1 << 20);
+  // Blocks that end after one chunk stream best (151 M bf16 weights with masters and the
+  // norm: 945 us, 997 with 16384 blocks, 1046 with 4096).  With 8-bit moments the start of a
+  // block weighs more, once there are many: one, two or four chunks a block take 1451,
+  // 1437 and 1555 us with fp32 gradients, 1461, 1277 and 1243 with bf16 ones (604 M
+  // bf16 weights); 19 M fp32 weights, 9400 chunks, 93, 96 and 99 with the norm.
+  const int64_t per = eight && chunks > 16384 ? (g_bf16 ? 4 : 2) : 1;
+  const int64_t fewer = (chunks + per - 1) / per;
+  const int grid = grid_of(per > 1 && fewer < 16384 ? 16384 : fewer, 1 << 20);
   if (grid > 0) {
     if (p == 0 && !g_bf16) adamw_launch<0, false>(t, grid, eight, a, s);
     else if (p == 0) adamw_launch<0, true>(t, grid, eight, a, s);

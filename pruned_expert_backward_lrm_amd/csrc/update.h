@@ -41,11 +41,11 @@ struct TableBatch {
 };
 
 struct AdamArgs {
-  double lr, grad_scale, max_norm;
-  float b1, d1, b2, d2, eps;  // betas and one less them
+  double grad_scale;
+  double over;  // max_norm / |grad_scale|, infinite without clipping
+  float lr, b1, d1, b2, d2, eps;  // betas and one less them
   // of a step that the host counts: 1 / (1 - beta1^t), 1 / sqrt(1 - beta2^t), the key
-  double bias;
-  float root;
+  float bias, root;
   uint32_t key;
   // of one that the GPU counts
   double ln1, ln2;  // logarithms of the betas

@@ -131,12 +131,13 @@ lrm_status lrm_adamw(const lrm_params* ps, const lrm_adamw_step* a, void* stream
   if (a->max_norm > 0.0 && !a->sumsq) return LRM_ERR_NULL;
   if (!on(a->sumsq, 8) || !on(a->lr_dev, 4) || !on(a->steps, 8)) return LRM_ERR_ALIGN;
   AdamArgs g{};
-  g.lr = a->lr; g.grad_scale = a->grad_scale; g.max_norm = a->max_norm;
+  g.lr = (float)a->lr; g.grad_scale = a->grad_scale;
+  g.over = a->max_norm > 0.0 ? a->max_norm / std::fabs(a->grad_scale) : HUGE_VAL;
   g.b1 = (float)a->beta1; g.d1 = (float)(1.0 - a->beta1);
   g.b2 = (float)a->beta2; g.d2 = (float)(1.0 - a->beta2);
   g.eps = (float)a->eps;
   g.ln1 = std::log(a->beta1); g.ln2 = std::log(a->beta2);
-  g.bias = -1.0 / std::expm1((double)a->step * g.ln1);
+  g.bias = (float)(-1.0 / std::expm1((double)a->step * g.ln1));
   g.root = (float)(1.0 / std::sqrt(-std::expm1((double)a->step * g.ln2)));
   g.key = step_key(a->seed, (uint64_t)a->step);
   g.seed = a->seed; g.sumsq = a->sumsq; g.n_sumsq = a->n_sumsq;

@@ -371,6 +371,7 @@ inline V4 ds_read_tr16(const V4* p) {
 #define __builtin_amdgcn_logf(x) ::log2f(x)
 #define __builtin_amdgcn_rcpf(x) (1.0f / (x))
 #define __builtin_amdgcn_sqrtf(x) ::sqrtf(x)
+#define __builtin_amdgcn_rsq(x) (1.0 / ::sqrt(x))
 // (instruction order is the compiler's business)
 #define __builtin_amdgcn_sched_group_barrier(mask, n, id) ((void)0)
 // memory operations complete at once here: waits have nothing to wait for
