@@ -425,7 +425,7 @@ hipError_t launch_params_table(const TableBatch& b, int first, int count, int n,
 
 hipError_t launch_grad_sumsq(const ParamTable& t, int64_t chunks, int g_bf16, double* part,
                              double* sumsq, hipStream_t s) {
-  const int grid = grid_of(chunks, kSumBlocks);
+  const int grid = grid_of(chunks, g_bf16 ? kSumBlocks : kSumBlocks / 2);
   if (grid > 0) {
     if (g_bf16)
       LRM_LAUNCH(grid, 256, 0, s, k_grad_sumsq<true>)(t, part);

@@ -73,7 +73,7 @@ __host__ __device__ inline uint32_t step_key(uint64_t seed, uint64_t step) {
   return mix32((k ^ (uint32_t)(step >> 32)) + kGold);
 }
 
-constexpr int kSumBlocks = 1024;  // persistent blocks, at most
+constexpr int kSumBlocks = 2048;  // persistent blocks of the sum, at most
 
 hipError_t launch_params_table(const TableBatch& b, int first, int count, int n, int64_t chunks,
                                void* table, hipStream_t s);
