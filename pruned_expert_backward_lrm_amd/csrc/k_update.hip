@@ -144,20 +144,37 @@ __device__ __forceinline__ uint32_t upper_halves(uint32_t lo, uint32_t hi) {
   return __builtin_amdgcn_perm(hi, lo, 0x07060302u);
 }
 
-template <bool SECOND>
-__device__ __forceinline__ void decode8(u32x2 q, uint32_t e, float (&x)[8]) {
-  const uint32_t low = (e - (SECOND ? kTopV : kTopM)) << 7;
-  const u16x2 base = halves(low * 0x10001u);
+// The upper words of eight codes' values: of floats, or (F64) of doubles, whose lower
+// words are 0.
+template <bool SECOND, bool F64>
+__device__ __forceinline__ void decode8(u32x2 q, uint32_t e, uint32_t (&x)[8]) {
+  constexpr int shift = F64 ? 1 : 4;  // of the mantissa's 3 bits in the upper half
+  const uint32_t low = (e - (SECOND ? kTopV : kTopM) + (F64 ? 1023 - 127 : 0)) << (shift + 3);
+  const u16x2 base = halves((low & 0xffffu) * 0x10001u);
 #pragma unroll
   for (int p = 0; p < 4; ++p) {
     const uint32_t b = (p & 1 ? q[p >> 1] >> 8 : q[p >> 1]) & 0x00ff00ffu;
     const u16x2 c = halves(SECOND ? b : b & 0x007f007fu);
     const u16x2 some = __builtin_elementwise_min(c, (u16x2)1);  // (code 0 stands for 0)
-    uint32_t t = word_of((c * (uint16_t)16 + base) * some);
+    uint32_t t = word_of((c * (uint16_t)(1 << shift) + base) * some);
     if (!SECOND) t |= (b << 8) & 0x80008000u;
-    x[4 * (p >> 1) + (p & 1)] = __uint_as_float(t << 16);
-    x[4 * (p >> 1) + (p & 1) + 2] = __uint_as_float(t & 0xffff0000u);
+    x[4 * (p >> 1) + (p & 1)] = t << 16;
+    x[4 * (p >> 1) + (p & 1) + 2] = t & 0xffff0000u;
   }
+}
+__device__ __forceinline__ double upper_word(uint32_t hi) {
+  return __builtin_bit_cast(double, (uint64_t)hi << 32);
+}
+
+// The bits of x in fp32, rounded towards 0 (beyond its range: the largest numbers; below
+// 2^-126: what is left of the mantissa).  A sum with the random bits then
+// crosses a border exactly where x itself does.
+__device__ __forceinline__ uint32_t f32_bits_down(double x) {
+  const uint64_t b = __builtin_bit_cast(uint64_t, x);
+  const uint32_t hi = (uint32_t)(b >> 32);
+  int u = (int)(hi & 0x7fffffffu) - (896 << 20);
+  u = u < 0 ? 0 : (u > (255 << 20) - 1 ? (255 << 20) - 1 : u);
+  return (hi & 0x80000000u) | ((uint32_t)u << 3 | (uint32_t)b >> 29);
 }
 
 // The exponent that a block's four lanes share, from the bits of their largest
@@ -169,23 +186,26 @@ __device__ __forceinline__ uint32_t quad_max(uint32_t u) {
   return o > u ? o : u;
 }
 template <bool SECOND>
-__device__ __forceinline__ uint32_t block_exponent(const float (&x)[8]) {
+__device__ __forceinline__ uint32_t block_exponent(const uint32_t (&x)[8]) {
   constexpr uint32_t least = (SECOND ? kTopV : kTopM) + 1;
-  float top = 0.f;
+  uint32_t top = 0;
 #pragma unroll
-  for (int j = 0; j < 8; ++j) top = fmaxf(top, fabsf(x[j]));
-  const uint32_t e = (quad_max(__float_as_uint(top)) + 0xfffffu) >> 23;
+  for (int j = 0; j < 8; ++j) {
+    const uint32_t mag = SECOND ? x[j] : x[j] & 0x7fffffffu;
+    top = mag > top ? mag : top;
+  }
+  const uint32_t e = (quad_max(top) + 0xfffffu) >> 23;
   return e > least ? e : least;
 }
-// r: 16 random bits an element at bit SECOND ? 16 : 0 of each.
+// x: bits of floats; r: 16 random bits an element at bit SECOND ? 16 : 0 of each.
 template <bool SECOND>
-__device__ __forceinline__ u32x2 encode8(const float (&x)[8], uint32_t e, const uint32_t (&r)[8]) {
+__device__ __forceinline__ u32x2 encode8(const uint32_t (&x)[8], uint32_t e, const uint32_t (&r)[8]) {
   constexpr int top = SECOND ? kTopV : kTopM, most = 8 * top + 7;
   const uint32_t low = (e - top) << 23;
   uint32_t t[8];
 #pragma unroll
   for (int j = 0; j < 8; ++j) {
-    const uint32_t mag = SECOND ? __float_as_uint(x[j]) : __float_as_uint(x[j]) & 0x7fffffffu;
+    const uint32_t mag = SECOND ? x[j] : x[j] & 0x7fffffffu;
     const uint32_t add = SECOND ? (r[j] >> 12 & 0xffff0u) | 8u : ((r[j] & 0xffffu) << 4) | 8u;
     t[j] = mag + add - low;
   }
@@ -198,7 +218,7 @@ __device__ __forceinline__ u32x2 encode8(const float (&x)[8], uint32_t e, const 
       const int j = 4 * w + p;
       s16x2 v = __builtin_bit_cast(s16x2, upper_halves(t[j], t[j + 2])) >> (int16_t)4;
       if (SECOND) {  // (what is not 0 stays so)
-        const uint32_t a = __float_as_uint(x[j]), b = __float_as_uint(x[j + 2]);
+        const uint32_t a = x[j], b = x[j + 2];
         const uint32_t some = (a < 1u ? a : 1u) | (b < 1u ? b : 1u) << 16;
         v = __builtin_elementwise_max(v, __builtin_bit_cast(s16x2, some));
       } else {
@@ -206,7 +226,7 @@ __device__ __forceinline__ u32x2 encode8(const float (&x)[8], uint32_t e, const 
       }
       v = __builtin_elementwise_min(v, (s16x2)(int16_t)most);
       if (!SECOND) {
-        const uint32_t sign = upper_halves(__float_as_uint(x[j]), __float_as_uint(x[j + 2])) >> 8 & 0x00800080u;
+        const uint32_t sign = upper_halves(x[j], x[j + 2]) >> 8 & 0x00800080u;
         v += __builtin_elementwise_min(v, (s16x2)1) * __builtin_bit_cast(s16x2, sign);
       }
       c[p] = __builtin_bit_cast(uint32_t, v);
@@ -313,20 +333,30 @@ __global__ __launch_bounds__(256) void k_adamw(ParamTable t, AdamArgs a) {
     const int64_t blk = i >> 5, blkc = i < n ? blk : 0;
     load8<GB>(e.g, i, n, vec, g);
     load8<P == 1>(P == 2 ? (const void*)e.master : e.p, i, n, vec, w);
+    uint32_t um[8], uv[8];  // 8 bits: words of the moments
     if constexpr (EIGHT) {
       const u32x2 qm = load_codes((const uint8_t*)e.m, i, n, vec);
       const u32x2 qv = load_codes((const uint8_t*)e.v, i, n, vec);
-      decode8<false>(qm, e.m_exp[blkc], m);
-      decode8<true>(qv, e.v_exp[blkc], v);
+      decode8<false, true>(qm, e.m_exp[blkc], um);
+      decode8<true, true>(qv, e.v_exp[blkc], uv);
     } else {
       load8<false>(e.m, i, n, vec, m);
       load8<false>(e.v, i, n, vec, v);
     }
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
-      const float x = c * g[j];
-      m[j] = fmaf(b1, m[j], d1 * x);
-      v[j] = fmaf(b2, v[j], d2 * (x * x));
+      if constexpr (EIGHT) {
+        // in fp64 (as many instructions as in fp32): the codes are the definition's
+        const double x = f * (double)g[j];
+        um[j] = f32_bits_down(fma(a.beta1, upper_word(um[j]), (1.0 - a.beta1) * x));
+        uv[j] = f32_bits_down(fma(a.beta2, upper_word(uv[j]), (1.0 - a.beta2) * (x * x)));
+        m[j] = __uint_as_float(um[j]);
+        v[j] = __uint_as_float(uv[j]);
+      } else {
+        const float x = c * g[j];
+        m[j] = fmaf(b1, m[j], d1 * x);
+        v[j] = fmaf(b2, v[j], d2 * (x * x));
+      }
       const float den = fmaf(__builtin_amdgcn_sqrtf(v[j]), root, eps);
       w[j] = fmaf(-up, m[j] * __builtin_amdgcn_rcpf(den), fmaf(-down, w[j], w[j]));
     }
@@ -344,10 +374,10 @@ __global__ __launch_bounds__(256) void k_adamw(ParamTable t, AdamArgs a) {
       }
     }
     if constexpr (EIGHT) {
-      const uint32_t em = block_exponent<false>(m), ev = block_exponent<true>(v);
+      const uint32_t em = block_exponent<false>(um), ev = block_exponent<true>(uv);
       if (i < n) {
-        store_codes((uint8_t*)e.m, i, n, vec, encode8<false>(m, em, r));
-        store_codes((uint8_t*)e.v, i, n, vec, encode8<true>(v, ev, r));
+        store_codes((uint8_t*)e.m, i, n, vec, encode8<false>(um, em, r));
+        store_codes((uint8_t*)e.v, i, n, vec, encode8<true>(uv, ev, r));
         if ((i & 31) == 0) {
           e.m_exp[blk] = (uint8_t)em;
           e.v_exp[blk] = (uint8_t)ev;
@@ -390,14 +420,14 @@ __global__ __launch_bounds__(256) void k_moment_read(int64_t n, const uint8_t* c
                                                      bool vec, void* out) {
   const int64_t step = (int64_t)gridDim.x * 2048;
   for (int64_t i = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 8; i < n; i += step) {
-    float x[8];
-    decode8<SECOND>(load_codes(codes, i, n, vec), exps[i >> 5], x);
+    uint32_t u[8];
+    decode8<SECOND, false>(load_codes(codes, i, n, vec), exps[i >> 5], u);
     if constexpr (BF16) {
-      uint32_t u[8];
-#pragma unroll
-      for (int j = 0; j < 8; ++j) u[j] = __float_as_uint(x[j]);
       store8_hi((uint16_t*)out, i, n, vec, u);
     } else {
+      float x[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) x[j] = __uint_as_float(u[j]);
       store8((float*)out, i, n, vec, x);
     }
   }

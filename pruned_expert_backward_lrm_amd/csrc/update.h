@@ -43,6 +43,7 @@ struct TableBatch {
 struct AdamArgs {
   double grad_scale;
   double over;  // max_norm / |grad_scale|, infinite without clipping
+  double beta1, beta2;
   float lr, b1, d1, b2, d2, eps;  // betas and one less them
   // of a step that the host counts: 1 / (1 - beta1^t), 1 / sqrt(1 - beta2^t), the key
   float bias, root;

@@ -133,6 +133,7 @@ lrm_status lrm_adamw(const lrm_params* ps, const lrm_adamw_step* a, void* stream
   AdamArgs g{};
   g.lr = (float)a->lr; g.grad_scale = a->grad_scale;
   g.over = a->max_norm > 0.0 ? a->max_norm / std::fabs(a->grad_scale) : HUGE_VAL;
+  g.beta1 = a->beta1; g.beta2 = a->beta2;
   g.b1 = (float)a->beta1; g.d1 = (float)(1.0 - a->beta1);
   g.b2 = (float)a->beta2; g.d2 = (float)(1.0 - a->beta2);
   g.eps = (float)a->eps;
