@@ -24,6 +24,7 @@ namespace lrm {
 namespace {
 
 constexpr int kThreads = 256;
+constexpr int64_t kCountOne = 16384;  // places of slots that one block counts
 constexpr float kLog2e = 1.44269504f, kLn2 = 0.693147181f;
 
 __device__ __forceinline__ int64_t at_most(int64_t a, int64_t b) { return a < b ? a : b; }
@@ -229,25 +230,31 @@ __device__ __forceinline__ void count_slots(const RouteArgs& a, const int32_t* e
   }
 }
 
-// Chunks of tokens; integer sums, so their order does not show.  out is clear.
-__global__ __launch_bounds__(kThreads) void k_balance_count(RouteArgs a, BalanceArgs b, int64_t chunk,
-                                                            int log_kk, int32_t* out) {
+// Chunks of tokens; integer sums, so their order does not show.  ONE: a single block of a
+// single sequence, which writes its counts; otherwise out is clear before.
+template <bool ONE>
+__global__ __launch_bounds__(ONE ? 1024 : kThreads) void k_balance_count(RouteArgs a, BalanceArgs b,
+                                                                         int64_t chunk, int log_kk,
+                                                                         int32_t* out) {
   LRM_DYN_SHARED(int, hist);  // [E]
+  constexpr int NT = ONE ? 1024 : kThreads;
   const int64_t c0 = (int64_t)blockIdx.x * chunk, c1 = at_most(c0 + chunk, a.T);
-  for (int e = threadIdx.x; e < a.E; e += kThreads) hist[e] = 0;
+  for (int e = threadIdx.x; e < a.E; e += NT) hist[e] = 0;
   for (int s = b.seq ? sequence_at(b.seq, b.S, c0) : 0; s < b.S; ++s) {
     int64_t t0 = c0, t1 = c1;
     if (b.seq) {
       t0 = at_least(c0, b.seq[s]);
       t1 = at_most(c1, b.seq[s + 1]);
-      if (b.seq[s] >= c1) break;
-      if (t0 >= t1) continue;
+      if (ONE) t1 = at_least(t0, t1);
+      if (!ONE && b.seq[s] >= c1) break;
+      if (!ONE && t0 >= t1) continue;
     }
     __syncthreads();
-    count_slots(a, b.expert, t0, t1, kThreads, log_kk, hist);
+    count_slots(a, b.expert, t0, t1, NT, log_kk, hist);
     __syncthreads();
-    for (int e = threadIdx.x; e < a.E; e += kThreads) {
-      if (hist[e]) atomicAdd(&out[(int64_t)s * a.E + e], hist[e]);
+    for (int e = threadIdx.x; e < a.E; e += NT) {
+      if constexpr (ONE) out[(int64_t)s * a.E + e] = hist[e];
+      else if (hist[e]) atomicAdd(&out[(int64_t)s * a.E + e], hist[e]);
       hist[e] = 0;
     }
   }
@@ -481,12 +488,15 @@ __global__ __launch_bounds__(1024) void k_balance_one(RouteArgs a, BalanceArgs b
   LRM_DYN_SHARED(int, hist);  // [E]
   __shared__ BalanceRow part[16];
   const int i = threadIdx.x & (LPT - 1);
+  const int64_t t0 = b.seq ? at_least(b.seq[0], 0) : 0, t1 = b.seq ? at_most(b.seq[1], a.T) : a.T;
   for (int e = threadIdx.x; e < a.E; e += 1024) hist[e] = b.counts ? b.counts[e] : 0;
   __syncthreads();
-  if (!b.counts) count_slots(a, b.expert, 0, a.T, 1024, log_kk, hist);
+  if (!b.counts) count_slots(a, b.expert, t0, t1, 1024, log_kk, hist);
   __syncthreads();
-  const BalanceRow v = wave_row(pass<LPT, NV, SIG, VEC, BF16>(
-      a, b.z_coef != 0.f, 0, a.T, 1024 / LPT, open_bits<LPT, NV, VEC>(a.expert_mask, i, a.E), hist));
+  BalanceRow v{0.0, 0.0, 0, 0};
+  if (t0 < t1)
+    v = wave_row(pass<LPT, NV, SIG, VEC, BF16>(a, b.z_coef != 0.f, t0, t1, 1024 / LPT,
+                                               open_bits<LPT, NV, VEC>(a.expert_mask, i, a.E), hist));
   if (lane_id() == 0) part[threadIdx.x >> 6] = v;
   __syncthreads();
   if (threadIdx.x >= kWave) return;
@@ -652,7 +662,7 @@ int log2_up(int k) {
 template <int LPT, int NV, bool SIG, bool VEC, bool BF16>
 hipError_t balance_launch(const RouteArgs& a, const BalanceArgs& b, hipStream_t s) {
   if constexpr (NV == 8) {
-    if (balance_in_one(a.T, a.E, b.S)) {
+    if (balance_in_one(a.T, a.E, a.k, b.S, b.counts != nullptr)) {
       LRM_LAUNCH(1, 1024, (size_t)a.E * 4, s, k_balance_one<LPT, NV, SIG, VEC, BF16>)(a, b, log2_up(a.k));
       return hipGetLastError();
     }
@@ -682,18 +692,25 @@ hipError_t balance_bwd_launch(const RouteArgs& a, const BalanceBwdArgs& b0, hipS
 
 }  // namespace
 
-// Tokens of a chunk: four of a place and more in about kBalanceChunks chunks, 16 at
-// most (whose sums are fp32).
+// Places of a block of 256 threads: tokens that it holds at once (LRM_ROUTE_DISPATCH).
+int balance_places(int E, int k) { return k <= 16 && E <= 128 ? 16 : (k <= 32 && E <= 256 ? 8 : 4); }
+
+// Tokens of a chunk: four of a place and more in about 512 chunks, 16 at most (whose
+// sums are fp32).  512, 1024 and 2048 chunks: 65536 x 128 11.2, 11.9 and 11.8 us, 8192 x
+// 256 in nine sequences 17.1, 17.5 and 17.4.
 int balance_chunk(int T, int E, int k) {
-  const int places = k <= 16 && E <= 128 ? 16 : (k <= 32 && E <= 256 ? 8 : 4);  // of a block
-  const int64_t c = ((int64_t)T + kBalanceChunks - 1) / kBalanceChunks;
-  const int64_t per = (c + places - 1) / places;
+  const int places = balance_places(E, k);
+  const int64_t per = (((int64_t)T + 511) / 512 + places - 1) / places;
   return places * (int)(per < 4 ? 4 : (per > 16 ? 16 : per));
 }
 
-// One block for all: few tokens, but some, of one sequence (up to 512 experts).
-bool balance_in_one(int T, int E, int S) {
-  return S == 1 && T > 0 && E <= 512 && (int64_t)T * E <= kBalanceOne;
+// One block of 1024 threads for all: few tokens, but some, of one sequence (up to 512
+// experts); up to 8 of a place, 16 where the counts would take two more launches.  One
+// block against several, counts at hand: 512 x 128 8.1 and 11.1 us, 1024 x 16 13.7 and
+// 11.2; from the choice: 512 x 128 9.0 and 17.2, 1024 x 16 14.5 and 17.1, 4096 x 16 47
+// and 17.3.
+bool balance_in_one(int T, int E, int k, int S, bool counts) {
+  return S == 1 && T > 0 && E <= 512 && T <= 4 * balance_places(E, k) * (counts ? 8 : 16);
 }
 
 // Blocks of the join: 16 sequences each, 1024 at most.
@@ -701,17 +718,22 @@ int balance_join_blocks(int S) { return S <= 64 ? 1 : (S < 16384 ? (S + 15) / 16
 
 hipError_t launch_balance(const RouteArgs& a, const BalanceArgs& b0, hipStream_t s) {
   BalanceArgs b = b0;
-  const bool one = balance_in_one(a.T, a.E, b.S);
+  const bool one = balance_in_one(a.T, a.E, a.k, b.S, b.counts != nullptr);
   if (!one && !b.counts) {
-    // about 1024 slots a block, more for over half a million
     const int log_kk = log2_up(a.k);
-    int64_t chunk = 1024 >> log_kk;
-    if (a.T / chunk > 512) chunk = (a.T / 512 + chunk - 1) / chunk * chunk;
-    hipError_t e = launch_fill_u32(reinterpret_cast<uint32_t*>(b.cnt), 0u, (int64_t)b.S * a.E, s);
-    if (e != hipSuccess) return e;
-    if (a.T > 0)
-      LRM_LAUNCH((unsigned)((a.T + chunk - 1) / chunk), kThreads, (size_t)a.E * 4, s, k_balance_count)(
-          a, b, chunk, log_kk, b.cnt);
+    if (b.S == 1 && a.T > 0 && (int64_t)a.T << log_kk <= kCountOne) {
+      LRM_LAUNCH(1, 1024, (size_t)a.E * 4, s, k_balance_count<true>)(a, b, a.T, log_kk, b.cnt);
+    } else {
+      // about 1024 slots a block, more for over half a million
+      int64_t chunk = 1024 >> log_kk;
+      if (a.T / chunk > 512) chunk = (a.T / 512 + chunk - 1) / chunk * chunk;
+      const hipError_t e =
+          launch_fill_u32(reinterpret_cast<uint32_t*>(b.cnt), 0u, (int64_t)b.S * a.E, s);
+      if (e != hipSuccess) return e;
+      if (a.T > 0)
+        LRM_LAUNCH((unsigned)((a.T + chunk - 1) / chunk), kThreads, (size_t)a.E * 4, s,
+                   k_balance_count<false>)(a, b, chunk, log_kk, b.cnt);
+    }
     b.counts = b.cnt;
   }
   if (one || b.chunks > 0) {

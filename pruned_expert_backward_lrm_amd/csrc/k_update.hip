@@ -470,10 +470,11 @@ hipError_t launch_adamw(const ParamTable& t, int64_t chunks, int p, int g_bf16, 
                         const AdamArgs& a, int64_t* steps, hipStream_t s) {
   // Blocks that end after one chunk stream best (151 M bf16 weights with masters and the
   // norm: 945 us, 997 with 16384 blocks, 1046 with 4096).  With 8-bit moments the start of a
-  // block weighs more, once there are many: one, two or four chunks a block take 1451,
-  // 1437 and 1555 us with fp32 gradients, 1461, 1277 and 1243 with bf16 ones (604 M
-  // bf16 weights); 19 M fp32 weights, 9400 chunks, 93, 96 and 99 with the norm.
-  const int64_t per = eight && chunks > 16384 ? (g_bf16 ? 4 : 2) : 1;
+  // block weighs more, once there are many: one, two, four and eight chunks a block take
+  // 1584, 1509, 1541 and 1590 us with fp32 gradients, 1631, 1419, 1359 and 1322 with bf16
+  // ones (604 M bf16 weights, whose step counts itself); 19 M fp32 weights, 9400
+  // chunks, 93, 97, 100 and 102 with the norm.
+  const int64_t per = eight && chunks > 16384 ? (g_bf16 ? 8 : 2) : 1;
   const int64_t fewer = (chunks + per - 1) / per;
   const int grid = grid_of(per > 1 && fewer < 16384 ? 16384 : fewer, 1 << 20);
   if (grid > 0) {

@@ -281,10 +281,8 @@ struct BalanceArgs {
   BalanceRow* rows;
   double* blocks;
 };
-constexpr int kBalanceChunks = 1024;
-constexpr int64_t kBalanceOne = 16384;
 int balance_chunk(int T, int E, int k);
-bool balance_in_one(int T, int E, int S);
+bool balance_in_one(int T, int E, int k, int S, bool counts);
 int balance_join_blocks(int S);
 hipError_t launch_balance(const RouteArgs& a, const BalanceArgs& b, hipStream_t s);
 struct BalanceBwdArgs {

@@ -78,7 +78,7 @@ def balance_arrays(c):
             c["expert_mask"], c["token_mask"], c["expert"], c["counts_in"], seq]
 
 
-BAL = sorted(TC.BALANCE) if FULL else ["seqs", "sigmoid_low", "twice", "strided"]
+BAL = sorted(TC.BALANCE) if FULL else ["seqs", "one_seq", "sigmoid_low", "twice", "strided"]
 
 
 @pytest.mark.parametrize("name", BAL)

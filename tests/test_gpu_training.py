@@ -62,6 +62,8 @@ TC.BALANCE_LARGE = {
     "many": dict(T=4001, E=32, k=4),
     "many_bf16": dict(T=3000, E=48, k=3, dtype="bf16", renorm=False, padded=0.1),
     "many_seqs": dict(T=2500, E=40, k=2, score="sigmoid", seq=[0, 0, 1, 700, 701, 1500, 1500, 2400]),
+    "one_seq_mid": dict(T=1500, E=16, k=2, seq=[10, 1400], padded=0.1),
+    "one_seq_many": dict(T=9001, E=20, k=3, seq=[100, 8900], score="sigmoid"),
     "short_seqs": dict(T=900, E=16, k=2, seq=list(range(0, 901, 3))),
 }
 

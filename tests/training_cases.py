@@ -35,6 +35,9 @@ BALANCE = {
     "one_token": dict(T=1, E=4, k=1),
     "small_bf16": dict(T=37, E=16, k=2, dtype="bf16"),
     "seqs": dict(T=70, E=24, k=3, seq=[3, 3, 4, 40, 40, 66]),
+    "one_seq": dict(T=30, E=16, k=2, seq=[5, 22]),
+    "one_empty_seq": dict(T=9, E=8, k=2, seq=[4, 4]),
+    "one_seq_wide": dict(T=150, E=300, k=2, seq=[2, 147], dtype="bf16"),
     "seqs_bf16": dict(T=70, E=40, k=3, dtype="bf16", seq=[0, 1, 33, 70]),
     "sigmoid": dict(T=45, E=33, k=4, score="sigmoid", padded=0.2, down=3),
     "sigmoid_seqs": dict(T=66, E=40, k=2, score="sigmoid", dtype="bf16", seq=[0, 30, 64], renorm=False),
