@@ -144,6 +144,17 @@ __device__ __forceinline__ uint32_t upper_halves(uint32_t lo, uint32_t hi) {
   return __builtin_amdgcn_perm(hi, lo, 0x07060302u);
 }
 
+// 1 in the halves of v that are above 0 (v is not below 0), by a minimum with ones that
+// the compiler cannot see: it would compare and select every half instead.
+template <typename V>
+__device__ __forceinline__ V one_if(V v) {
+  uint32_t ones = 0x10001u;
+#ifndef LRM_CPU_EMU
+  asm("" : "+s"(ones));
+#endif
+  return __builtin_elementwise_min(v, __builtin_bit_cast(V, ones));
+}
+
 // The upper words of eight codes' values: of floats, or (F64) of doubles, whose lower
 // words are 0.
 template <bool SECOND, bool F64>
@@ -155,8 +166,7 @@ __device__ __forceinline__ void decode8(u32x2 q, uint32_t e, uint32_t (&x)[8]) {
   for (int p = 0; p < 4; ++p) {
     const uint32_t b = (p & 1 ? q[p >> 1] >> 8 : q[p >> 1]) & 0x00ff00ffu;
     const u16x2 c = halves(SECOND ? b : b & 0x007f007fu);
-    const u16x2 some = __builtin_elementwise_min(c, (u16x2)1);  // (code 0 stands for 0)
-    uint32_t t = word_of((c * (uint16_t)(1 << shift) + base) * some);
+    uint32_t t = word_of((c * (uint16_t)(1 << shift) + base) * one_if(c));  // (code 0 stands for 0)
     if (!SECOND) t |= (b << 8) & 0x80008000u;
     x[4 * (p >> 1) + (p & 1)] = t << 16;
     x[4 * (p >> 1) + (p & 1) + 2] = t & 0xffff0000u;
@@ -169,12 +179,14 @@ __device__ __forceinline__ double upper_word(uint32_t hi) {
 // The bits of x in fp32, rounded towards 0 (beyond its range: the largest numbers; below
 // 2^-126: what is left of the mantissa).  A sum with the random bits then
 // crosses a border exactly where x itself does.
+template <bool SIGNED>
 __device__ __forceinline__ uint32_t f32_bits_down(double x) {
   const uint64_t b = __builtin_bit_cast(uint64_t, x);
   const uint32_t hi = (uint32_t)(b >> 32);
-  int u = (int)(hi & 0x7fffffffu) - (896 << 20);
+  int u = (int)(SIGNED ? hi & 0x7fffffffu : hi) - (896 << 20);
   u = u < 0 ? 0 : (u > (255 << 20) - 1 ? (255 << 20) - 1 : u);
-  return (hi & 0x80000000u) | ((uint32_t)u << 3 | (uint32_t)b >> 29);
+  const uint32_t t = (uint32_t)u << 3 | (uint32_t)b >> 29;
+  return SIGNED ? (hi & 0x80000000u) | t : t;
 }
 
 // The exponent that a block's four lanes share, from the bits of their largest
@@ -227,7 +239,7 @@ __device__ __forceinline__ u32x2 encode8(const uint32_t (&x)[8], uint32_t e, con
       v = __builtin_elementwise_min(v, (s16x2)(int16_t)most);
       if (!SECOND) {
         const uint32_t sign = upper_halves(x[j], x[j + 2]) >> 8 & 0x00800080u;
-        v += __builtin_elementwise_min(v, (s16x2)1) * __builtin_bit_cast(s16x2, sign);
+        v += one_if(v) * __builtin_bit_cast(s16x2, sign);
       }
       c[p] = __builtin_bit_cast(uint32_t, v);
     }
@@ -319,6 +331,7 @@ __global__ __launch_bounds__(256) void k_adamw(ParamTable t, AdamArgs a) {
   }
   const float lr = a.lr_dev ? *(const LRM_CONST float*)a.lr_dev : a.lr;
   const float size = lr * bias;
+  const double f1 = (1.0 - a.beta1) * f, f2 = (1.0 - a.beta2) * f * f;
   const float c = (float)f, b1 = a.b1, d1 = a.d1, b2 = a.b2, d2 = a.d2, eps = a.eps;
   constexpr bool RANDOM_P = P == 1;
   const int64_t chunks = t.chunk0[t.n];
@@ -347,9 +360,9 @@ __global__ __launch_bounds__(256) void k_adamw(ParamTable t, AdamArgs a) {
     for (int j = 0; j < 8; ++j) {
       if constexpr (EIGHT) {
         // in fp64 (as many instructions as in fp32): the codes are the definition's
-        const double x = f * (double)g[j];
-        um[j] = f32_bits_down(fma(a.beta1, upper_word(um[j]), (1.0 - a.beta1) * x));
-        uv[j] = f32_bits_down(fma(a.beta2, upper_word(uv[j]), (1.0 - a.beta2) * (x * x)));
+        const double x = (double)g[j];
+        um[j] = f32_bits_down<true>(fma(a.beta1, upper_word(um[j]), f1 * x));
+        uv[j] = f32_bits_down<false>(fma(a.beta2, upper_word(uv[j]), f2 * (x * x)));
         m[j] = __uint_as_float(um[j]);
         v[j] = __uint_as_float(uv[j]);
       } else {
