@@ -3,9 +3,14 @@
 // LRMoE backward pass makes; the pages leave the optimizer as it is.)
 //
 // All are bound by memory: one pass over every array, each element read and
-// written once.  The tensors of a list are cut into chunks of 2048 elements, 8
-// neighbours a thread; blocks take the chunks in turn and find a chunk's
-// tensor in the table.
+// written once, stored past the caches.  The tensors of a list are cut into chunks of
+// 2048 elements, 8 neighbours a thread (16 or 32 bytes of every array); a block takes
+// its chunks in turn and finds a chunk's tensor in the table, 64 at a time.  Measured (a
+// large copy makes 5.1 TB/s): sum of squares of 151 M fp32 gradients 95 us, 6.3 TB/s, of
+// 604 M bf16 ones 202 us, 6.0; the step of 151 M bf16 weights with masters and fp32
+// moments 794 us, 5.7 TB/s; with 8-bit moments, bf16 weights and gradients 316 us, 4.9,
+// its vector instructions (some 560 for 512 elements) taking as long as the memory; the
+// values of 151 M codes in bf16 79 us, 5.8 TB/s.
 //
 // 8-bit moments (see lrm.h): 4 lanes hold a block of 32, whose largest magnitude
 // they find with two quad permutations.  The shared exponent x is the largest's,
