@@ -628,7 +628,8 @@ size_t lrm_balance_workspace_size(const lrm_balance* b);
  *            router's settings apply), or NULL
  *   dlogits: device [T][E] output of the logits' dtype, rows ldd >= E elements
  *            apart, every element written (0 for masked ones); tokens of no
- *            sequence have the gradient of the weights only */
+ *            sequence have the gradient of the weights only (0 without slots,
+ *            whatever their logits hold) */
 lrm_status lrm_balance_bwd(const lrm_balance* b, const float* saved, const float* dloss,
                            const float* dweight, void* dlogits, int64_t ldd, void* stream);
 
@@ -788,7 +789,7 @@ size_t lrm_sumsq_workspace_size(const lrm_params* ps);
 typedef struct lrm_adamw_step {
   double lr;            /* finite, >= 0 */
   double beta1, beta2;  /* [0, 1) */
-  double eps;           /* finite, 1e-30 at least */
+  double eps;           /* finite, 1e-16 at least */
   double grad_scale;    /* finite */
   double max_norm;      /* finite, > 0; 0: no clipping */
   int64_t step;         /* t, 1..2^53 (not read where steps is given) */

@@ -642,6 +642,10 @@ __global__ __launch_bounds__(NV > 8 ? kWave : kThreads) void k_balance_bwd(Route
 #pragma unroll
     for (int j = 0; j < NV; ++j)
       o[j] = SIG ? z[j] * (pb * (w[j] - dot) * rest[j]) : z[j] * fmaf(pb, w[j], pz);
+    if (b.seq) {  // (the shares of a token of no sequence may be no numbers)
+#pragma unroll
+      for (int j = 0; j < NV; ++j) o[j] = inside || dw != 0.f ? o[j] : 0.f;
+    }
     if (b.dweight) {
 #pragma unroll
       for (int j = 0; j < NV; ++j) row[column<LPT, NV, VEC>(i, j)] = o[j];

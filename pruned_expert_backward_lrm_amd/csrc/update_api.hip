@@ -120,7 +120,7 @@ lrm_status lrm_adamw(const lrm_params* ps, const lrm_adamw_step* a, void* stream
   LRM_TRY(check_params(ps, true, &chunks));
   if (!a) return LRM_ERR_NULL;
   if (ps->chunks != chunks) return LRM_ERR_SHAPE;  // (no table of these tensors)
-  if (!std::isfinite(a->lr) || a->lr < 0.0 || !std::isfinite(a->eps) || !(a->eps >= 1e-30) ||
+  if (!std::isfinite(a->lr) || a->lr < 0.0 || !std::isfinite(a->eps) || !(a->eps >= 1e-16) ||
       !std::isfinite(a->grad_scale) || !std::isfinite(a->max_norm) || a->max_norm < 0.0)
     return LRM_ERR_UNSUPPORTED;
   if (!(a->beta1 >= 0.0 && a->beta1 < 1.0) || !(a->beta2 >= 0.0 && a->beta2 < 1.0))

@@ -248,7 +248,7 @@ def test_params_call_refusals():
 
 
 STEP_REFUSALS = [
-    (dict(lr=-0.1), 10), (dict(lr=float("nan")), 10), (dict(eps=0.0), 10), (dict(eps=1e-31), 10), (dict(eps=float("inf")), 10),
+    (dict(lr=-0.1), 10), (dict(lr=float("nan")), 10), (dict(eps=0.0), 10), (dict(eps=1e-17), 10), (dict(eps=float("inf")), 10),
     (dict(beta1=1.0), 10), (dict(beta1=-0.1), 10), (dict(beta2=1.5), 10), (dict(beta2=float("nan")), 10),
     (dict(grad_scale=float("inf")), 10), (dict(max_norm=-1.0, sumsq=P, n_sumsq=1), 10),
     (dict(step=0), 2), (dict(step=(1 << 53) + 1), 2), (dict(n_sumsq=1), 2), (dict(sumsq=P), 2),

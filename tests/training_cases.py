@@ -38,6 +38,9 @@ BALANCE = {
     "one_seq": dict(T=30, E=16, k=2, seq=[5, 22]),
     "one_empty_seq": dict(T=9, E=8, k=2, seq=[4, 4]),
     "one_seq_wide": dict(T=150, E=300, k=2, seq=[2, 147], dtype="bf16"),
+    "garbage_outside": dict(T=40, E=16, k=2, seq=[3, 20, 31], garbage=True),
+    "garbage_outside_dense": dict(T=40, E=24, k=2, seq=[3, 20, 31], garbage=True, renorm=False,
+                                  dtype="bf16"),
     "seqs_bf16": dict(T=70, E=40, k=3, dtype="bf16", seq=[0, 1, 33, 70]),
     "sigmoid": dict(T=45, E=33, k=4, score="sigmoid", padded=0.2, down=3),
     "sigmoid_seqs": dict(T=66, E=40, k=2, score="sigmoid", dtype="bf16", seq=[0, 30, 64], renorm=False),
@@ -59,10 +62,10 @@ BALANCE = {
 
 def balance_case(name, **over):
     c = dict(dtype="f32", score="softmax", renorm=True, seq=None, padded=0.0, down=0, shift=0.0,
-             counts=False, ld=None, closed_rows=0, repeat=False, coef=0.5,
+             counts=False, ld=None, closed_rows=0, repeat=False, garbage=False, coef=0.5,
              **{k: v for k, v in BALANCE.get(name, {}).items()
                 if k not in ("dtype", "score", "renorm", "seq", "padded", "down", "shift", "counts",
-                             "ld", "closed_rows", "repeat")})
+                             "ld", "closed_rows", "repeat", "garbage")})
     c.update(BALANCE.get(name, {}))
     c.update(over)
     g = gen("balance", name)
@@ -95,6 +98,12 @@ def balance_case(name, **over):
         e[::2, 1] = e[::2, 0]
         e[::4, 3] = e[::4, 0]
         e[1, 0], e[1, 1] = E, -7
+        e = e.reshape(-1)
+    if c["garbage"]:  # tokens of no sequence, without slots: their logits may be anything
+        e = e.reshape(T, k)
+        for t in (*range(c["seq"][0]), *range(c["seq"][-1], T)):
+            e[t] = -1
+            z[t] = float("nan")
         e = e.reshape(-1)
     c["expert"] = torch.as_tensor(e).int()
     if c["counts"]:
