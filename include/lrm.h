@@ -774,7 +774,7 @@ size_t lrm_sumsq_workspace_size(const lrm_params* ps);
  *   m = beta1 m + (1 - beta1) c g         v = beta2 v + (1 - beta2) (c g)^2
  *   p = p (1 - r wd) - r / (1 - beta1^t) m / (sqrt(v / (1 - beta2^t)) + eps)
  * with r = lr * param.lr and wd = param.weight_decay, in fp32 (p the master, where
- * there is one).
+ * there is one); m and v that are kept in 8 bits are formed in fp64.
  * Clipping: norm = |grad_scale| sqrt(sum of sumsq[0 .. n_sumsq)) (several
  * entries: of several lists, or GPUs), c = grad_scale * min(1, max_norm /
  * norm).  If the sum is not finite the call leaves everything as it was, the
